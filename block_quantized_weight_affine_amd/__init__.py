@@ -37,6 +37,7 @@ SYMBOLS = [
     "qg_conv2d",
     "qg_moe_plan_host", "qg_moe_plan", "qg_x_half", "qg_x_half_guard", "qgemm_moe_grouped", "qg_swiglu", "qg_moe_combine",
     "qg_moe_ffn_workspace", "qg_moe_ffn", "qg_moe_ffn_noalloc",
+    "qg_kv8_write", "qg_kv8_read", "qg_attn_kv8_workspace", "qg_attn_kv8", "qgemm_w8a8_workspace", "qgemm_w8a8",
 ]
 
 
@@ -94,8 +95,17 @@ def lib() -> C.CDLL:
         L.qg_moe_ffn_workspace.argtypes = [_i, _i, _i, _i, _i]
         L.qg_moe_ffn.argtypes = [_i, _p, _p, _i, _i, _i, _i, _p, _i, _i, _p, _p, _p, _p, _p, _i, _i, _p, _sz, _p]
         L.qg_moe_ffn_noalloc.argtypes = [_i, _p, _p, _i, _i, _i, _i, _p, _i, _i, _p, _p, _p, _p, _p, _i, _i, _p]
+        _i64 = C.c_int64
+        L.qg_kv8_write.argtypes = [_p, _p, _p, _i64, _i64, _p, _i64, _i64, _i, _p]
+        L.qg_kv8_read.argtypes = [_p, _p, _p, _i64, _i64, _p, _i64, _i64, _i, _p]
+        L.qg_attn_kv8_workspace.argtypes = [_p, _p, _i]
+        L.qg_attn_kv8.argtypes = [_p, _p, _p, _i64, _i64, _p, _i64, _i64, _i, _i, C.c_float, _i, _i, _p, _sz, _p]
+        L.qgemm_w8a8_workspace.argtypes = [_i, _i, _i]
+        L.qgemm_w8a8.argtypes = [_p, _p, _p, _i, _p, _i, _i, _i, _i, _p, _sz, _p]
+        for name in ("qg_attn_kv8_workspace", "qgemm_w8a8_workspace"):
+            getattr(L, name).restype = _sz
         for name in SYMBOLS:
-            if name not in ("qg_strerror", "qg_abi_version", "qg_moe_ffn_workspace"):
+            if name not in ("qg_strerror", "qg_abi_version") and not name.endswith("_workspace"):
                 getattr(L, name).restype = _i
         _lib = L
     return _lib
@@ -370,6 +380,120 @@ def qg_moe_ffn_noalloc(fmt, gate_up, down, group, E, H, I, X, T, k, seg_off, row
                                     I, _ptr(X), T, k, _ptr(seg_off), _ptr(row_src), _ptr(slot_row), _ptr(slot_w),
                                     _ptr(Y), int(accumulate), _mode(mode), _stream(stream)),
            "qg_moe_ffn_noalloc")
+
+
+# ---- 8-bit serving operators ------------------------------------------------------------------------
+class QgKv8Cache(C.Structure):
+    """qg_kv8_cache of qgemm.h."""
+    _fields_ = [("k_codes", C.c_void_p), ("k_scales", C.c_void_p), ("v_codes", C.c_void_p), ("v_scales", C.c_void_p),
+                ("pages", C.c_int), ("page", C.c_int), ("heads", C.c_int), ("dim", C.c_int)]
+
+
+class QgKv8Seqs(C.Structure):
+    """qg_kv8_seqs of qgemm.h."""
+    _fields_ = [("table", C.c_void_p), ("rows", C.c_void_p), ("kv_len", C.c_void_p), ("seqs", C.c_int),
+                ("width", C.c_int), ("T", C.c_int), ("max_new", C.c_int), ("max_kv", C.c_int)]
+
+
+class _Desc:
+    """A C descriptor and the tensors that its addresses point into."""
+    __slots__ = ("struct", "ptr", "keep", "T", "heads", "dim")
+
+    def __init__(self, struct, keep, T=0, heads=0, dim=0):
+        self.struct, self.keep, self.T, self.heads, self.dim = struct, keep, T, heads, dim
+        self.ptr = C.addressof(struct)
+
+
+def _expect(ok: bool, where: str, status: int = QG_EINVAL):
+    if not ok:
+        raise QGError(status, where)
+
+
+def kv8_pages(pages, page, heads, dim, device="cuda"):
+    """Empty cache tensors (k_codes, k_scales, v_codes, v_scales) for kv8_cache."""
+    import torch
+    n = pages * heads * (page // 16)
+    return (torch.empty(n * 16 * dim, dtype=torch.int8, device=device), torch.empty(n, device=device),
+            torch.empty(n * 16 * dim, dtype=torch.int8, device=device), torch.empty(n, device=device))
+
+
+def kv8_cache(k_codes, k_scales, v_codes, v_scales, page, heads, dim):
+    """Descriptor of an 8-bit key/value cache over contiguous device tensors (int8 codes, f32 scales; layouts
+    in qgemm.h); the number of pages follows from their sizes.  Keep it as long as the cache."""
+    import torch
+    t = (k_codes, k_scales, v_codes, v_scales)
+    _expect(page >= 16 and page % 16 == 0 and heads >= 1 and dim >= 1, "kv8_cache", QG_ESHAPE)
+    per = heads * (page // 16)
+    pages = k_scales.numel() // per
+    for x, dtype, n in zip(t, (torch.int8, torch.float32) * 2, (per * 16 * dim, per) * 2):
+        _expect(x.dtype == dtype and x.is_contiguous() and x.device == k_codes.device, "kv8_cache")
+        _expect(x.numel() == pages * n, "kv8_cache", QG_ESHAPE)
+    return _Desc(QgKv8Cache(*(x.data_ptr() for x in t), pages, page, heads, dim), t, heads=heads, dim=dim)
+
+
+def kv8_seqs(table, rows, kv_len, T, max_new, max_kv):
+    """Descriptor of a batch of sequences: int32 device tensors table [seqs][width], rows [seqs + 1] and
+    kv_len [seqs], and the host's bounds (qg_kv8_seqs in qgemm.h).  The tensors' contents may change later
+    within the bounds."""
+    import torch
+    t = (table, rows, kv_len)
+    for x in t:
+        _expect(x.dtype == torch.int32 and x.is_contiguous() and x.device == table.device, "kv8_seqs")
+    _expect(table.dim() == 2 and rows.numel() == table.shape[0] + 1 and kv_len.numel() == table.shape[0], "kv8_seqs",
+            QG_ESHAPE)
+    return _Desc(QgKv8Seqs(*(x.data_ptr() for x in t), table.shape[0], table.shape[1], T, max_new, max_kv), t, T=T)
+
+
+def _rows3(x, T, heads, dim, where):
+    """(address, row stride, head stride) of a [T][heads][dim] tensor."""
+    _expect(x.shape == (T, heads, dim), where, QG_ESHAPE)
+    row, head, one = x.stride()
+    _expect(one == 1, where, QG_EALIGN)
+    return x.data_ptr(), row, head
+
+
+def qg_kv8_write(cache, seqs, k, v, stream=None):
+    """Codes k, v [T][heads][dim] (any row and head strides) into the cache as their sequences' last tokens."""
+    _expect(k.dtype == v.dtype, "qg_kv8_write")
+    _check(lib().qg_kv8_write(cache.ptr, seqs.ptr, *_rows3(k, seqs.T, cache.heads, cache.dim, "qg_kv8_write"),
+                              *_rows3(v, seqs.T, cache.heads, cache.dim, "qg_kv8_write"), _xt(k), _stream(stream)),
+           "qg_kv8_write")
+
+
+def qg_kv8_read(cache, seqs, k_out, v_out, stream=None):
+    """Reads the sequences' last tokens back into k_out, v_out [T][heads][dim]."""
+    _expect(k_out.dtype == v_out.dtype, "qg_kv8_read")
+    _check(lib().qg_kv8_read(cache.ptr, seqs.ptr, *_rows3(k_out, seqs.T, cache.heads, cache.dim, "qg_kv8_read"),
+                             *_rows3(v_out, seqs.T, cache.heads, cache.dim, "qg_kv8_read"), _xt(k_out),
+                             _stream(stream)), "qg_kv8_read")
+
+
+def qg_attn_kv8_workspace(cache, seqs, q_heads) -> int:
+    return int(lib().qg_attn_kv8_workspace(cache.ptr, seqs.ptr, q_heads))
+
+
+def qg_attn_kv8(cache, seqs, q, o, q_heads, scale, causal=True, window=0, workspace=None, stream=None):
+    """Attention of q [T][q_heads][dim] over the cache into o (same shape and type); workspace: a device
+    tensor of at least qg_attn_kv8_workspace bytes."""
+    _expect(q.dtype == o.dtype, "qg_attn_kv8")
+    _check(lib().qg_attn_kv8(cache.ptr, seqs.ptr, *_rows3(q, seqs.T, q_heads, cache.dim, "qg_attn_kv8"),
+                             *_rows3(o, seqs.T, q_heads, cache.dim, "qg_attn_kv8"), _xt(q), q_heads, scale,
+                             int(bool(causal)), window, _ptr(workspace),
+                             0 if workspace is None else workspace.numel() * workspace.element_size(),
+                             _stream(stream)), "qg_attn_kv8")
+
+
+def qgemm_w8a8_workspace(N, K, T) -> int:
+    return int(lib().qgemm_w8a8_workspace(N, K, T))
+
+
+def qgemm_w8a8(w_codes, w_scales, X, Y, N, K, T, workspace=None, stream=None):
+    """Y [T][N] = X [T][K] times int8 weights [N][K] with a scale an output channel, X coded in 8 bits with a
+    scale a token on the way; types from the tensors' dtypes; workspace: a device tensor of at least
+    qgemm_w8a8_workspace bytes."""
+    _check(lib().qgemm_w8a8(_ptr(w_codes), _ptr(w_scales), _ptr(X), _xt(X), _ptr(Y), _xt(Y), N, K, T,
+                            _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
+                            _stream(stream)), "qgemm_w8a8")
 
 
 # ---- host layout helpers (byte movement only) ----------------------------------------------------

@@ -1,0 +1,409 @@
+// qg_attn8.hip -- attention over the 8-bit key/value cache.
+//
+//   o = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale q . k_j) over the tokens j that the row may see.
+//
+// K and V codes are integers of at most 8 bits, exact in f16, so the products run on the f16 matrix
+// instructions with f32 sums: q enters as f16 after an exact power of two per row (f32 q as two such
+// f16 pieces), the weights as f16 after the block's V scale.  Nothing of the cache is decoded into
+// memory.
+#include <hip/hip_runtime.h>
+
+#include "qg_device.hpp"
+#include "qg_internal.hpp"
+
+namespace qg {
+namespace {
+
+typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNegInf = -__builtin_inff();
+// A weight enters the second product as f16: p * vs * 2^(kBase - ev), where 2^ev >= the V scales so
+// far.  The running maximum may lag by kLag (in powers of two) before the sums are rescaled, so values
+// stay at or below 2^15 and keep f16's full precision down to 2^-23 of the row's largest.
+constexpr float kLag = 6.f;
+constexpr int kBase = 9;
+
+// Four codes as four f16 values, exactly: byte ^ 0x80 below 0x64 is 1024 + (code + 128).
+__device__ __forceinline__ void codes4_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const uint32_t u = w ^ 0x80808080u;
+    const half2_t bias = {(_Float16)1152.f, (_Float16)1152.f};
+    const half2_t a = __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u)) - bias;
+    const half2_t b = __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u)) - bias;
+    lo = __builtin_bit_cast(uint32_t, a);
+    hi = __builtin_bit_cast(uint32_t, b);
+}
+__device__ __forceinline__ half8_t codes8_f16(uint32_t w0, uint32_t w1) {
+    u32x4 r;
+    uint32_t a, b;
+    codes4_f16(w0, a, b);
+    r[0] = a, r[1] = b;
+    codes4_f16(w1, a, b);
+    r[2] = a, r[3] = b;
+    return __builtin_bit_cast(half8_t, r);
+}
+
+// Maximum / sum over the four lane groups of 16 (lanes l, l ^ 16, l ^ 32, l ^ 48).
+__device__ __forceinline__ float groups_max(float v) {
+    v = fmaxf(v, __shfl_xor(v, 16));
+    return fmaxf(v, __shfl_xor(v, 32));
+}
+__device__ __forceinline__ float groups_sum(float v) {
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+}
+
+// What the 16 rows of a tile see together, and how the splits divide it.
+struct TileRange {
+    int lo, hi, nact;  // tokens [lo, hi), lo a multiple of 64; splits that have any of them
+};
+__device__ __forceinline__ TileRange tile_range(const AttnParams& a, const KvSpan& sp, int r0, int rows) {
+    const int i0 = r0 / a.group, i1 = (min(r0 + rows, sp.n * a.group) - 1) / a.group;
+    TileRange t;
+    t.lo = kv8_sight(sp, i0, a.causal, a.window).lo & ~63;
+    t.hi = kv8_sight(sp, i1, a.causal, a.window).hi;
+    t.nact = (t.hi - t.lo + a.chunk - 1) / a.chunk;
+    return t;
+}
+
+// One workgroup takes 16 rows (query rows times the heads that share a K/V head, counted together) and
+// one split of the tokens they see; its wavefronts take 64 tokens in turn and are joined at the end.
+//
+// Layout of a wavefront's 64 tokens (four blocks): the first product is K Q^T with A row r of its
+// m-th instruction = token 4m + r % 4 of block r / 4, so result lane (row l % 16, group g = l / 16)
+// holds all 16 tokens of block g.  That is what the second product V^T P^T wants as its B operand, so
+// the weights never move between lanes, every lane has one K and one V scale, and both code loads are
+// 16 bytes a lane as the cache holds them.
+template <int XT, int D>
+__global__ __launch_bounds__(256) void attn8_rows_kernel(AttnParams a) {
+    constexpr int NP = XT == XT_F32 ? 2 : 1;  // f16 pieces of a q value and of a weight
+    constexpr int NH = (D + 63) / 64;         // 16-byte K loads a token
+    constexpr int NT = D / 16;
+    constexpr int DH = D > 128 ? D / 2 : D;   // dims joined at a time
+    __shared__ float sh_o[4][16][DH + 4];
+    __shared__ float sh_m[4][16], sh_l[4][16];
+
+    const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int b = blockIdx.x;
+    const int tile = b % a.tiles;
+    b /= a.tiles;
+    const int h = b % a.c.heads;
+    b /= a.c.heads;
+    const int split = b % a.splits, s = b / a.splits;
+    const KvSpan sp = kv8_span(a.q, s);
+    const int rows = sp.n * a.group;
+    if (tile * 16 >= rows) return;
+    const TileRange tr = tile_range(a, sp, tile * 16, 16);
+    if (split > 0 && split >= tr.nact) return;
+    const int t0 = tr.lo + split * a.chunk, t1 = min(t0 + a.chunk, tr.hi);
+
+    // this lane's row
+    const int r = tile * 16 + col, ri = min(r, rows - 1) / a.group;
+    const int head = h * a.group + min(r, rows - 1) % a.group;
+    KvSight see = kv8_sight(sp, ri, a.causal, a.window);
+    if (r >= rows) see.hi = see.lo;
+
+    // q as f16 pieces, scaled so that the row's largest lies in [2^14, 2^15)
+    half8_t qf[NP][NH][2];
+    float qs;
+    {
+        float x[NH][16];
+        const int64_t at = (int64_t)(sp.r0 + ri) * a.q_row + head * a.q_head;
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < NH; i++) {
+            const int ch = 4 * i + g;
+            if (ch < NT) {
+                float lo[8], hi[8];
+                x_load8<XT>(a.Q, at + 16 * ch, lo);
+                x_load8<XT>(a.Q, at + 16 * ch + 8, hi);
+#pragma unroll
+                for (int e = 0; e < 8; e++) x[i][e] = lo[e], x[i][8 + e] = hi[e];
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; e++) x[i][e] = 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < 16; e++) top = max(top, __float_as_uint(x[i][e]) & 0x7fffffffu);
+        }
+        top = max(top, (uint32_t)__shfl_xor((int)top, 16));
+        top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+        const int eb = top >> 23, ex = eb == 0 || eb == 255 ? 0 : 141 - eb;
+        qs = ldexpf(a.scale * kLog2e, -ex);
+#pragma unroll
+        for (int i = 0; i < NH; i++)
+#pragma unroll
+            for (int e = 0; e < 16; e++) {
+                const float v = ldexpf(x[i][e], ex);
+                const _Float16 hi = (_Float16)v;
+                qf[0][i][e >> 3][e & 7] = hi;
+                if constexpr (NP == 2) qf[1][i][e >> 3][e & 7] = (_Float16)(v - (float)hi);
+            }
+    }
+
+    f32x4_t o[NT];
+#pragma unroll
+    for (int i = 0; i < NT; i++) o[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    float m = kNegInf, l = 0.f;
+    int ev = -1000;  // exponent that the V scales are taken relative to
+
+    const int krow = (lane & 15) >> 2;  // block of the four that this lane loads K of
+    for (int tb = t0 + 64 * wave; tb < t1; tb += 256) {
+        const int blk = (tb >> 4) + g;
+        const int bi = 16 * blk < tr.hi ? kv8_block(a.c, a.q, s, h, blk) : -1;
+        const int kbi = max(0, __shfl(bi, krow * 16));
+        const int8_t* kp = a.c.kc + (int64_t)kbi * (16 * D) + (lane & 3) * 16;
+        const int8_t* vp = a.c.vc + (int64_t)max(bi, 0) * (16 * D) + col * 16;
+        // tokens of this lane's block that its row sees: [jl, jh)
+        const int jl = see.lo - 16 * blk, jh = bi < 0 ? 0 : see.hi - 16 * blk;
+        const bool any = jl < 16 && jh > 0 && jl < jh;
+        const float ks = any ? a.c.ks[max(bi, 0)] * qs : 0.f;
+        const float vb = bi < 0 ? 0.f : a.c.vs[bi], vs = any ? vb : 0.f;
+
+        uint4 kw[4][NH];
+#pragma unroll
+        for (int mi = 0; mi < 4; mi++)
+#pragma unroll
+            for (int i = 0; i < NH; i++)
+                kw[mi][i] = *(const uint4*)(kp + ((min(4 * i + g, NT - 1) * 16) + 4 * mi) * 16);
+        uint4 vw[NT];
+#pragma unroll
+        for (int i = 0; i < NT; i++) vw[i] = *(const uint4*)(vp + i * 256);
+
+        float p[16];
+#pragma unroll
+        for (int mi = 0; mi < 4; mi++) {
+            f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < NH; i++) {
+                const half8_t k0 = codes8_f16(kw[mi][i].x, kw[mi][i].y), k1 = codes8_f16(kw[mi][i].z, kw[mi][i].w);
+#pragma unroll
+                for (int n = 0; n < NP; n++) {
+                    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, qf[n][i][0], acc, 0, 0, 0);
+                    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, qf[n][i][1], acc, 0, 0, 0);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const int j = 4 * mi + e;
+                p[j] = j >= jl && j < jh ? acc[e] * ks : kNegInf;
+            }
+        }
+        float top = p[0];
+#pragma unroll
+        for (int j = 1; j < 16; j++) top = fmaxf(top, p[j]);
+        top = groups_max(top);
+        // the largest V scale's exponent, the same in the whole wavefront
+        const int eb = __builtin_amdgcn_readfirstlane((int)(__float_as_uint(groups_max(fabsf(vb))) >> 23)) - 126;
+        if (eb > ev || __any(top > m + kLag)) {
+            const float mn = fmaxf(m, top);
+            const int en = max(ev, eb);
+            const float f = m == kNegInf ? 0.f : ldexpf(__builtin_amdgcn_exp2f(m - mn), ev - en);
+            l *= m == kNegInf ? 0.f : __builtin_amdgcn_exp2f(m - mn);
+#pragma unroll
+            for (int i = 0; i < NT; i++) o[i] *= f;
+            m = mn;
+            ev = en;
+        }
+        const float mu = m == kNegInf ? 0.f : m;
+        const float vn = ldexpf(vs, kBase - ev);
+        half8_t pf[NP][2];
+#pragma unroll
+        for (int j = 0; j < 16; j++) {
+            const float w = __builtin_amdgcn_exp2f(p[j] - mu);
+            l += w;
+            const float wv = w * vn;
+            const _Float16 hi = (_Float16)wv;
+            pf[0][j >> 3][j & 7] = hi;
+            if constexpr (NP == 2) pf[1][j >> 3][j & 7] = (_Float16)(wv - (float)hi);
+        }
+#pragma unroll
+        for (int i = 0; i < NT; i++) {
+            const half8_t v0 = codes8_f16(vw[i].x, vw[i].y), v1 = codes8_f16(vw[i].z, vw[i].w);
+#pragma unroll
+            for (int n = 0; n < NP; n++) {
+                o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pf[n][0], o[i], 0, 0, 0);
+                o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pf[n][1], o[i], 0, 0, 0);
+            }
+        }
+    }
+
+    // join the wavefronts
+    l = groups_sum(l);
+    if (g == 0) {
+        sh_m[wave][col] = m;
+        sh_l[wave][col] = l;
+    }
+    __syncthreads();
+    const float mt = fmaxf(fmaxf(sh_m[0][col], sh_m[1][col]), fmaxf(sh_m[2][col], sh_m[3][col]));
+    const float f = m == kNegInf ? 0.f : ldexpf(__builtin_amdgcn_exp2f(m - mt), ev - kBase);
+#pragma unroll
+    for (int d0 = 0; d0 < D; d0 += DH) {
+        if (d0) __syncthreads();
+#pragma unroll
+        for (int i = 0; i < DH / 16; i++) {
+            const f32x4_t v = o[d0 / 16 + i] * f;
+            *(f32x4_t*)&sh_o[wave][col][16 * i + 4 * g] = v;
+        }
+        __syncthreads();
+        for (int x = threadIdx.x; x < 16 * (DH / 4); x += 256) {
+            const int row = x / (DH / 4), d = 4 * (x % (DH / 4));
+            const int rr = tile * 16 + row;
+            if (rr >= rows) continue;
+            float mr = kNegInf;
+#pragma unroll
+            for (int w = 0; w < 4; w++) mr = fmaxf(mr, sh_m[w][row]);
+            float lr = 0.f;
+#pragma unroll
+            for (int w = 0; w < 4; w++)
+                lr += sh_l[w][row] * (sh_m[w][row] == kNegInf ? 1.f : __builtin_amdgcn_exp2f(sh_m[w][row] - mr));
+            f32x4_t v = *(const f32x4_t*)&sh_o[0][row][d];
+#pragma unroll
+            for (int w = 1; w < 4; w++) v += *(const f32x4_t*)&sh_o[w][row][d];
+            const int64_t trow = sp.r0 + rr / a.group;
+            const int hd = h * a.group + rr % a.group;
+            if (tr.nact > 1) {
+                const int64_t pi = (trow * a.q_heads + hd) * a.splits + split;
+                *(f32x4_t*)(a.part_o + pi * D + d0 + d) = v;
+                if (d0 + d == 0) *(float2*)(a.part_ml + pi * 2) = make_float2(mr, lr);
+            } else {
+                const float inv = lr == 0.f ? 0.f : 1.0f / lr;
+                const int64_t at = trow * a.o_row + hd * a.o_head + d0 + d;
+                if constexpr (XT == XT_F32)
+                    *(f32x4_t*)((float*)a.O + at) = v * inv;
+                else {
+                    u32x2_t y;
+                    y[0] = (uint32_t)f32_to_16<XT>(v[0] * inv) | (uint32_t)f32_to_16<XT>(v[1] * inv) << 16;
+                    y[1] = (uint32_t)f32_to_16<XT>(v[2] * inv) | (uint32_t)f32_to_16<XT>(v[3] * inv) << 16;
+                    *(u32x2_t*)((uint16_t*)a.O + at) = y;
+                }
+            }
+        }
+    }
+}
+
+// Joins the splits of one row and head, one workgroup each: its wavefronts take the splits in turn.
+// The order of the sums is fixed, so results repeat bit for bit.
+template <int XT, int D>
+__global__ __launch_bounds__(256) void attn8_join_kernel(AttnParams a) {
+    constexpr int NV = (D + 127) / 128;  // pairs of dims a lane
+    __shared__ float sh_l[4];
+    __shared__ float sh_o[4][D];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int s = blockIdx.y, i = blockIdx.x / a.q_heads, head = blockIdx.x % a.q_heads;
+    const KvSpan sp = kv8_span(a.q, s);
+    if (i >= sp.n) return;
+    const int r = i * a.group + head % a.group;
+    const TileRange tr = tile_range(a, sp, r & ~15, 16);
+    if (tr.nact <= 1) return;
+    const int64_t p0 = ((int64_t)(sp.r0 + i) * a.q_heads + head) * a.splits;
+    float mt = kNegInf;
+    for (int x = lane; x < tr.nact; x += 64) mt = fmaxf(mt, a.part_ml[(p0 + x) * 2]);
+#pragma unroll
+    for (int e = 1; e < 64; e <<= 1) mt = fmaxf(mt, __shfl_xor(mt, e));
+    const float mu = mt == kNegInf ? 0.f : mt;
+    float l = 0.f;
+    float2 o[NV];
+#pragma unroll
+    for (int e = 0; e < NV; e++) o[e] = make_float2(0.f, 0.f);
+    for (int x = wave; x < tr.nact; x += 4) {
+        const float2 ml = *(const float2*)(a.part_ml + (p0 + x) * 2);
+        const float w = __builtin_amdgcn_exp2f(ml.x - mu);
+        l += ml.y * w;
+#pragma unroll
+        for (int e = 0; e < NV; e++) {
+            const int d = 2 * lane + 128 * e;
+            if (d < D) {
+                const float2 v = *(const float2*)(a.part_o + (p0 + x) * D + d);
+                o[e].x += v.x * w;
+                o[e].y += v.y * w;
+            }
+        }
+    }
+    if (lane == 0) sh_l[wave] = l;
+#pragma unroll
+    for (int e = 0; e < NV; e++) {
+        const int d = 2 * lane + 128 * e;
+        if (d < D) *(float2*)&sh_o[wave][d] = o[e];
+    }
+    __syncthreads();
+    const int d = threadIdx.x;
+    if (d >= D) return;
+    const float lt = sh_l[0] + sh_l[1] + sh_l[2] + sh_l[3];
+    const float v = sh_o[0][d] + sh_o[1][d] + sh_o[2][d] + sh_o[3][d];
+    const float y = lt == 0.f ? 0.f : v / lt;
+    const int64_t at = (int64_t)(sp.r0 + i) * a.o_row + head * a.o_head + d;
+    if constexpr (XT == XT_F32)
+        ((float*)a.O)[at] = y;
+    else
+        ((uint16_t*)a.O)[at] = f32_to_16<XT>(keep_f32(y));
+}
+
+template <int XT, int D>
+hipError_t launch_one(const AttnParams& a, hipStream_t s) {
+    const int64_t grid = (int64_t)a.q.seqs * a.splits * a.c.heads * a.tiles;
+    attn8_rows_kernel<XT, D><<<dim3((uint32_t)grid), 256, 0, s>>>(a);
+    if (a.splits > 1)
+        attn8_join_kernel<XT, D><<<dim3((uint32_t)(a.q.max_new * a.q_heads), a.q.seqs), 256, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <int XT>
+hipError_t launch_dim(const AttnParams& a, hipStream_t s) {
+    switch (a.c.dim) {
+        case 64: return launch_one<XT, 64>(a, s);
+        case 96: return launch_one<XT, 96>(a, s);
+        case 128: return launch_one<XT, 128>(a, s);
+        case 192: return launch_one<XT, 192>(a, s);
+        case 256: return launch_one<XT, 256>(a, s);
+    }
+    return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+namespace {
+constexpr int64_t kMinChunk = 1024, kFill = 2048;
+// Splits that fill the card several times over.
+int64_t wanted_splits(const AttnParams& a) {
+    const int64_t base = (int64_t)a.q.seqs * a.c.heads * a.tiles;
+    return (kFill + base - 1) / base;
+}
+}  // namespace
+
+int attn8_max_splits(const AttnParams& a) {
+    const int64_t most = (a.q.max_kv + kMinChunk - 1) / kMinChunk, want = wanted_splits(a);
+    return (int)(most < want ? most : want);
+}
+
+// Tiles and splits of a call, from the host's bounds alone.
+void attn8_plan(AttnParams& a) {
+    a.tiles = (int)(((int64_t)a.q.max_new * a.group + 15) / 16);
+    // tokens that a tile of 16 rows may see: all, or its window, started at a multiple of 64
+    int64_t span = a.q.max_kv;
+    if (a.causal && a.window > 0 && (int64_t)a.window + 16 / a.group + 65 < span) span = a.window + 16 / a.group + 65;
+    const int64_t want = wanted_splits(a);
+    int64_t chunk = (span + want - 1) / want;
+    if (chunk < kMinChunk) chunk = kMinChunk;
+    a.chunk = (int)((chunk + 255) / 256 * 256);
+    a.splits = (int)((span + a.chunk - 1) / a.chunk);
+    if (a.splits < 1) a.splits = 1;
+}
+
+size_t attn8_workspace(const AttnParams& a) {
+    if (a.splits <= 1) return 0;
+    return (size_t)a.q.T * a.q_heads * a.splits * (a.c.dim + 2) * sizeof(float);
+}
+
+hipError_t launch_attn8(AttnParams a, int xt, float* ws, hipStream_t s) {
+    a.part_o = ws;
+    a.part_ml = ws ? ws + (size_t)a.q.T * a.q_heads * a.splits * a.c.dim : nullptr;
+    if (xt == XT_F32) return launch_dim<XT_F32>(a, s);
+    if (xt == XT_F16) return launch_dim<XT_F16>(a, s);
+    return launch_dim<XT_BF16>(a, s);
+}
+
+}  // namespace qg

@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "qg_kv8.hpp"
+
 namespace qg {
 
 struct ExpertPtr {
@@ -101,5 +103,44 @@ hipError_t launch_repack_gguf_q8a16(int type, const void* src, size_t nblk16, vo
 hipError_t noalloc_scratch(void** ptr);
 hipError_t launch_moe_combine(const float* O, int R, const int32_t* slot_row, const float* slot_w, float* Y, int H,
                               int T, int k, int accumulate, hipStream_t s);
+
+
+// ---- 8-bit serving operators ------------------------------------------------------------------------
+// Elements between tokens and between heads of K and V rows.
+struct KvStrides {
+    int64_t k_row, k_head, v_row, v_head;
+};
+// New tokens into the cache (write), or a sequence's last tokens out of it.
+hipError_t launch_kv8(bool write, const KvCache& c, const KvSeqs& q, void* k, void* v, int xt, const KvStrides& st,
+                      hipStream_t s);
+
+struct AttnParams {
+    KvCache c;
+    KvSeqs q;
+    const void* Q;
+    void* O;
+    int64_t q_row, q_head, o_row, o_head;  // elements
+    int q_heads, group;
+    float scale;
+    int causal, window;
+    int tiles, splits, chunk;              // row tiles a K/V head, splits of the tokens, tokens a split
+    float *part_o, *part_ml;               // splits > 1: sums [row][head][split][dim], (maximum, weight sum)
+};
+void attn8_plan(AttnParams& a);
+int attn8_max_splits(const AttnParams& a);  // of any window
+size_t attn8_workspace(const AttnParams& a);
+hipError_t launch_attn8(AttnParams a, int xt, float* ws, hipStream_t s);
+
+// Y [T][N] = X [T][K] w^T in 8-bit integers; xq, xs: X's codes and row scales.
+struct W8A8Params {
+    const int8_t* w;
+    const float* ws;
+    const int8_t* xq;
+    const float* xs;
+    void* Y;
+    int N, K, T;
+};
+size_t w8a8_workspace(int N, int K, int T);
+hipError_t launch_w8a8(W8A8Params p, const void* X, int xt, int yt, void* ws, hipStream_t s);
 
 }  // namespace qg

@@ -458,6 +458,94 @@ qg_status qg_moe_ffn_noalloc(qg_format fmt, const qg_expert* gate_up, const qg_e
                              const int32_t* slot_row, const float* slot_w, float* Y,
                              int accumulate, qg_mode mode, hipStream_t stream);
 
+/* ==== 8-bit serving operators: a key/value cache, attention over it, an integer product ============
+ *
+ * The cache holds K and V as 8-bit codes in pages; a page holds `page` tokens of every head in blocks
+ * of 16 tokens, with one f32 scale a block and head for K and one for V: value = code * scale.
+ *   k_codes  int8 [pages][heads][page/16][dim/16][16 tokens][16 dims]
+ *   v_codes  int8 [pages][heads][page/16][dim][16 tokens]
+ *   k_scales, v_scales  f32 [pages][heads][page/16]
+ * dim is 64, 96, 128, 192 or 256; page a multiple of 16 from 16 to 65536; 1 <= heads <= 1024;
+ * pages * heads * page / 16 < 2^31; else QG_ESHAPE.  Codes 16-byte, scales 4-byte aligned (QG_EALIGN). */
+typedef struct {
+    int8_t* k_codes;
+    float* k_scales;
+    int8_t* v_codes;
+    float* v_scales;
+    int pages, page, heads, dim;
+} qg_kv8_cache;
+
+/* A batch of sequences (host struct, device arrays).  Sequence s has kv_len[s] tokens; token j lies in
+ * page table[s * width + j / page]; rows rows[s] .. rows[s+1] - 1 of the [T] row operands are its last
+ * tokens, in order.  T, max_new >= any rows[s+1] - rows[s], and max_kv >= any kv_len[s] are the host's
+ * bounds, from which launches are sized; the device arrays may change between replays of a captured
+ * graph as long as the bounds hold.
+ * The kernels check what they read: a sequence whose numbers contradict the bounds or each other
+ * (rows not ascending or past T, more rows than tokens) is left out, and a page outside 0..pages-1 or
+ * past `width` holds no tokens (not written, read as 0, hidden from attention).
+ * 0 <= seqs <= 65535, 1 <= width <= 2^20, 0 <= T <= 2^21, 0 <= max_new <= min(T, max_kv),
+ * max_kv <= 2^24, else QG_ESHAPE; 4-byte aligned (QG_EALIGN).  seqs, T or max_new 0: QG_OK, nothing is
+ * launched and no pointer is looked at. */
+typedef struct {
+    const int32_t* table;
+    const int32_t* rows;
+    const int32_t* kv_len;
+    int seqs, width, T, max_new, max_kv;
+} qg_kv8_seqs;
+
+/* Codes the rows k, v [T][heads][dim] into the cache as the last tokens of their sequences (kv_len
+ * counts them).  A block's scale is d = fl(amax / 127) over its tokens (amax times the f32 nearest to
+ * 1/127), its codes rint(x * min(fl(1/d), FLT_MAX)) limited to +-127, in f32; a block of zeros has
+ * d = 0.  A block that held earlier tokens keeps the larger of its scale and the new rows'; where that
+ * grows, the earlier codes become rint(code * fl(d_old / d)).  A NaN or infinity makes its block NaN.
+ * Codes past a sequence's last token are unspecified.  Two sequences must not write the same page in
+ * one call; pages shared for reading are fine.
+ * k_row, k_head, v_row, v_head: elements between tokens and between heads (a fused projection's K and V
+ * side by side need no copy); k, v and every stride in bytes a multiple of 16, else QG_EALIGN; strides
+ * 0..2^40 else QG_ESHAPE.  Null pointer or unknown type: QG_EINVAL.  Asynchronous on `stream`. */
+qg_status qg_kv8_write(const qg_kv8_cache* cache, const qg_kv8_seqs* seqs, const void* k, int64_t k_row,
+                       int64_t k_head, const void* v, int64_t v_row, int64_t v_head, qg_xtype xt,
+                       hipStream_t stream);
+
+/* Reads the last rows[s+1] - rows[s] tokens of every sequence back: code * scale in f32, rounded once to
+ * yt.  Arguments as qg_kv8_write; outputs whose rows or heads overlap give QG_ESHAPE. */
+qg_status qg_kv8_read(const qg_kv8_cache* cache, const qg_kv8_seqs* seqs, void* k, int64_t k_row,
+                      int64_t k_head, void* v, int64_t v_row, int64_t v_head, qg_xtype yt,
+                      hipStream_t stream);
+
+/* Bytes of workspace that qg_attn_kv8 needs for these descriptors and q_heads, whatever its mask (0: none,
+ * or arguments that it would refuse). */
+size_t qg_attn_kv8_workspace(const qg_kv8_cache* cache, const qg_kv8_seqs* seqs, int q_heads);
+
+/* Attention of the rows q [T][q_heads][dim] over the cache, o of the same shape and type.  Head h reads K/V
+ * head h / (q_heads / heads).  A row at position p of its sequence (the rows are its last tokens) sees the
+ * tokens j with j <= p if causal, and p - window < j if window > 0:
+ *     o = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale * q . k_j);  a row that sees nothing gets 0.
+ * Products of the exact codes with q, sums, maxima and weights are in f32; q (f16 / bf16 exactly, f32 in
+ * two pieces of 11 bits) and the weights (rounded to f16; for f32 rows in two pieces) feed f16 matrix
+ * instructions.  Single tokens, drafts and whole prompts take the same call.  The order of the sums is
+ * fixed: results repeat bit for bit.
+ * q_heads a multiple of heads, <= 65536, max_new * q_heads < 2^31, else QG_ESHAPE; strides as in
+ * qg_kv8_write (o as an output); workspace 16-byte aligned, QG_EWORKSPACE if NULL or too small.  It needs
+ * no initialisation; calls that overlap in time need one each. */
+qg_status qg_attn_kv8(const qg_kv8_cache* cache, const qg_kv8_seqs* seqs, const void* q, int64_t q_row,
+                      int64_t q_head, void* o, int64_t o_row, int64_t o_head, qg_xtype xt, int q_heads,
+                      float scale, int causal, int window, void* workspace, size_t ws_bytes,
+                      hipStream_t stream);
+
+/* Product in 8-bit integers, activations coded on the way:
+ *     Y[t][n] = fl(fl(float(sum_k xq[t][k] w[n][k]) * dx[t]) * w_scales[n])  rounded once to yt,
+ *     dx[t] = fl(amax_k |X[t][k]| / 127),  xq = rint(X * min(fl(1/dx), FLT_MAX)) limited to +-127.
+ * w_codes int8 [N][K], w_scales f32 [N] (a scale an output channel), X [T][K] (xt) and Y [T][N] (yt)
+ * row-major.  The integer sum is exact.  A NaN or infinity in a row of X makes that row of Y NaN.
+ * 1 <= N <= 2^24, 16 <= K <= 2^17, K % 16 == 0, 0 <= T <= 2^21, else QG_ESHAPE; T = 0: QG_OK; w_codes, X
+ * and workspace 16-byte aligned, w_scales 4, Y its element's size, else QG_EALIGN; null pointers or
+ * unknown types QG_EINVAL; QG_EWORKSPACE if ws_bytes < qgemm_w8a8_workspace(N, K, T).  Asynchronous. */
+size_t qgemm_w8a8_workspace(int N, int K, int T);
+qg_status qgemm_w8a8(const int8_t* w_codes, const float* w_scales, const void* X, qg_xtype xt, void* Y,
+                     qg_xtype yt, int N, int K, int T, void* workspace, size_t ws_bytes,
+                     hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
