@@ -131,15 +131,30 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_XT = {}
+
+
 def _xt(t) -> int:
-    import torch
-    return {torch.float32: QG_X_F32, torch.float16: QG_X_F16, torch.bfloat16: QG_X_BF16}[t.dtype]
+    if not _XT:
+        import torch
+        _XT.update({torch.float32: QG_X_F32, torch.float16: QG_X_F16, torch.bfloat16: QG_X_BF16})
+    return _XT[t.dtype]
+
+
+_raw_stream = None
 
 
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the current device's current stream as an address; torch.cuda.current_stream() builds an object
+        # around it first, 1 us that a launch of a few does not have
+        global _raw_stream
+        if _raw_stream is None:
+            import torch
+            torch.cuda.current_stream()  # initialises the device
+            get, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+            _raw_stream = lambda: get(device())  # noqa: E731
+        return _raw_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -444,28 +459,34 @@ def kv8_seqs(table, rows, kv_len, T, max_new, max_kv):
     return _Desc(QgKv8Seqs(*(x.data_ptr() for x in t), table.shape[0], table.shape[1], T, max_new, max_kv), t, T=T)
 
 
-def _rows3(x, T, heads, dim, where):
-    """(address, row stride, head stride) of a [T][heads][dim] tensor."""
-    _expect(x.shape == (T, heads, dim), where, QG_ESHAPE)
+def _rows3(x, shape, where):
+    """(address, row stride, head stride) of a tensor of this [T][heads][dim] shape."""
+    if x.shape != shape:
+        raise QGError(QG_ESHAPE, where)
     row, head, one = x.stride()
-    _expect(one == 1, where, QG_EALIGN)
+    if one != 1:
+        raise QGError(QG_EALIGN, where)
     return x.data_ptr(), row, head
 
 
 def qg_kv8_write(cache, seqs, k, v, stream=None):
     """Codes k, v [T][heads][dim] (any row and head strides) into the cache as their sequences' last tokens."""
-    _expect(k.dtype == v.dtype, "qg_kv8_write")
-    _check(lib().qg_kv8_write(cache.ptr, seqs.ptr, *_rows3(k, seqs.T, cache.heads, cache.dim, "qg_kv8_write"),
-                              *_rows3(v, seqs.T, cache.heads, cache.dim, "qg_kv8_write"), _xt(k), _stream(stream)),
-           "qg_kv8_write")
+    _kv8(lib().qg_kv8_write, "qg_kv8_write", cache, seqs, k, v, stream)
 
 
 def qg_kv8_read(cache, seqs, k_out, v_out, stream=None):
     """Reads the sequences' last tokens back into k_out, v_out [T][heads][dim]."""
-    _expect(k_out.dtype == v_out.dtype, "qg_kv8_read")
-    _check(lib().qg_kv8_read(cache.ptr, seqs.ptr, *_rows3(k_out, seqs.T, cache.heads, cache.dim, "qg_kv8_read"),
-                             *_rows3(v_out, seqs.T, cache.heads, cache.dim, "qg_kv8_read"), _xt(k_out),
-                             _stream(stream)), "qg_kv8_read")
+    _kv8(lib().qg_kv8_read, "qg_kv8_read", cache, seqs, k_out, v_out, stream)
+
+
+def _kv8(call, where, cache, seqs, k, v, stream):
+    _expect(k.dtype == v.dtype, where)
+    shape = (seqs.T, cache.heads, cache.dim)
+    kp, kr, kh = _rows3(k, shape, where)
+    vp, vr, vh = _rows3(v, shape, where)
+    status = call(cache.ptr, seqs.ptr, kp, kr, kh, vp, vr, vh, _xt(k), _stream(stream))
+    if status:
+        raise QGError(status, where)
 
 
 def qg_attn_kv8_workspace(cache, seqs, q_heads) -> int:
@@ -476,11 +497,14 @@ def qg_attn_kv8(cache, seqs, q, o, q_heads, scale, causal=True, window=0, worksp
     """Attention of q [T][q_heads][dim] over the cache into o (same shape and type); workspace: a device
     tensor of at least qg_attn_kv8_workspace bytes."""
     _expect(q.dtype == o.dtype, "qg_attn_kv8")
-    _check(lib().qg_attn_kv8(cache.ptr, seqs.ptr, *_rows3(q, seqs.T, q_heads, cache.dim, "qg_attn_kv8"),
-                             *_rows3(o, seqs.T, q_heads, cache.dim, "qg_attn_kv8"), _xt(q), q_heads, scale,
-                             int(bool(causal)), window, _ptr(workspace),
-                             0 if workspace is None else workspace.numel() * workspace.element_size(),
-                             _stream(stream)), "qg_attn_kv8")
+    shape = (seqs.T, q_heads, cache.dim)
+    qp, qr, qh = _rows3(q, shape, "qg_attn_kv8")
+    op, orow, oh = _rows3(o, shape, "qg_attn_kv8")
+    wp, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    status = lib().qg_attn_kv8(cache.ptr, seqs.ptr, qp, qr, qh, op, orow, oh, _xt(q), q_heads, scale, 1 if causal else 0,
+                               window, wp, size, _stream(stream))
+    if status:
+        raise QGError(status, "qg_attn_kv8")
 
 
 def qgemm_w8a8_workspace(N, K, T) -> int:
@@ -491,9 +515,11 @@ def qgemm_w8a8(w_codes, w_scales, X, Y, N, K, T, workspace=None, stream=None):
     """Y [T][N] = X [T][K] times int8 weights [N][K] with a scale an output channel, X coded in 8 bits with a
     scale a token on the way; types from the tensors' dtypes; workspace: a device tensor of at least
     qgemm_w8a8_workspace bytes."""
-    _check(lib().qgemm_w8a8(_ptr(w_codes), _ptr(w_scales), _ptr(X), _xt(X), _ptr(Y), _xt(Y), N, K, T,
-                            _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
-                            _stream(stream)), "qgemm_w8a8")
+    wp, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    status = lib().qgemm_w8a8(w_codes.data_ptr(), w_scales.data_ptr(), X.data_ptr(), _xt(X), Y.data_ptr(), _xt(Y), N, K, T,
+                              wp, size, _stream(stream))
+    if status:
+        raise QGError(status, "qgemm_w8a8")
 
 
 # ---- host layout helpers (byte movement only) ----------------------------------------------------

@@ -163,11 +163,14 @@ qg_status qgemm_w8a8(const int8_t* w_codes, const float* w_scales, const void* X
     qg::W8A8Params p{};
     p.w = w_codes;
     p.ws = w_scales;
+    p.X = X;
     p.Y = Y;
+    p.xt = xt;
+    p.yt = yt;
     p.N = N;
     p.K = K;
     p.T = T;
-    return launched(qg::launch_w8a8(p, X, xt, yt, workspace, stream));
+    return launched(qg::launch_w8a8(p, workspace, stream));
 }
 
 }  // extern "C"

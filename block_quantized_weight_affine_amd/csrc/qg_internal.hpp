@@ -131,16 +131,17 @@ int attn8_max_splits(const AttnParams& a);  // of any window
 size_t attn8_workspace(const AttnParams& a);
 hipError_t launch_attn8(AttnParams a, int xt, float* ws, hipStream_t s);
 
-// Y [T][N] = X [T][K] w^T in 8-bit integers; xq, xs: X's codes and row scales.
+// Y [T][N] = X [T][K] w^T in 8-bit integers; xq, xs: X's codes and row scales, set by the launcher.
 struct W8A8Params {
     const int8_t* w;
     const float* ws;
+    const void* X;
     const int8_t* xq;
     const float* xs;
     void* Y;
-    int N, K, T;
+    int N, K, T, xt, yt;
 };
 size_t w8a8_workspace(int N, int K, int T);
-hipError_t launch_w8a8(W8A8Params p, const void* X, int xt, int yt, void* ws, hipStream_t s);
+hipError_t launch_w8a8(W8A8Params p, void* ws, hipStream_t s);
 
 }  // namespace qg

@@ -27,6 +27,30 @@ __device__ __forceinline__ float row_scale(uint32_t top) {
     return top >= 0x7f800000u ? __builtin_nanf("") : __uint_as_float(top) * kPer127;
 }
 
+// 8 values as 8 code bytes.
+__device__ __forceinline__ uint2 code8x8(const float (&v)[8], float inv) {
+    uint32_t w[2];
+#pragma unroll
+    for (int e = 0; e < 2; e++)
+        w[e] = code8(v[4 * e] * inv) | code8(v[4 * e + 1] * inv) << 8 | code8(v[4 * e + 2] * inv) << 16 |
+               code8(v[4 * e + 3] * inv) << 24;
+    return make_uint2(w[0], w[1]);
+}
+
+__device__ __forceinline__ float inverse(float d) { return d > 0.f ? fminf(1.0f / d, 3.402823466e+38f) : 0.f; }
+
+__device__ __forceinline__ uint32_t max8(const float (&v)[8], uint32_t top) {
+#pragma unroll
+    for (int e = 0; e < 8; e++) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+    return top;
+}
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o));
+    return v;
+}
+
 // One workgroup codes one row of X: the maximum first, then the codes from a second read (the row is
 // in the cache by then).  K % 16 == 0.
 template <int XT>
@@ -37,26 +61,17 @@ __global__ __launch_bounds__(256) void x_code_kernel(const void* X, int K, int8_
     for (int k = 8 * threadIdx.x; k < K; k += 2048) {
         float v[8];
         x_load8<XT>(X, base + k, v);
-#pragma unroll
-        for (int e = 0; e < 8; e++) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+        top = max8(v, top);
     }
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
+    top = wave_max(top);
     if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = top;
     __syncthreads();
-    top = max(max(sh[0], sh[1]), max(sh[2], sh[3]));
-    const float d = row_scale(top);
-    const float inv = d > 0.f ? fminf(1.0f / d, 3.402823466e+38f) : 0.f;
+    const float d = row_scale(max(max(sh[0], sh[1]), max(sh[2], sh[3]))), inv = inverse(d);
     if (threadIdx.x == 0) scales[blockIdx.x] = d;
     for (int k = 8 * threadIdx.x; k < K; k += 2048) {
         float v[8];
         x_load8<XT>(X, base + k, v);
-        uint32_t w[2];
-#pragma unroll
-        for (int e = 0; e < 2; e++)
-            w[e] = code8(v[4 * e] * inv) | code8(v[4 * e + 1] * inv) << 8 | code8(v[4 * e + 2] * inv) << 16 |
-                   code8(v[4 * e + 3] * inv) << 24;
-        *(uint2*)(codes + base + k) = make_uint2(w[0], w[1]);
+        *(uint2*)(codes + base + k) = code8x8(v, inv);
     }
 }
 
@@ -67,57 +82,336 @@ __device__ __forceinline__ void store_y(void* Y, int64_t i, float v) {
     else
         ((uint16_t*)Y)[i] = f32_to_16<YT>(keep_f32(v));
 }
+__device__ __forceinline__ void store_any(void* Y, int yt, int64_t i, float v) {
+    if (yt == XT_F32)
+        store_y<XT_F32>(Y, i, v);
+    else if (yt == XT_F16)
+        store_y<XT_F16>(Y, i, v);
+    else
+        store_y<XT_BF16>(Y, i, v);
+}
 
-// 32 x 32 outputs a wavefront, operands straight from memory.
-template <int YT>
-__global__ __launch_bounds__(256) void w8a8_kernel(W8A8Params p) {
-    const int lane = threadIdx.x & 63, r = lane & 31, g = lane >> 5;
-    const int wave = threadIdx.x >> 6;
-    const int n0 = blockIdx.x * 128 + 32 * wave, t0 = blockIdx.y * 32;
-    if (n0 >= p.N) return;
-    const int8_t* w = p.w + (int64_t)min(n0 + r, p.N - 1) * p.K + 16 * g;
-    const int8_t* x = p.xq + (int64_t)min(t0 + r, p.T - 1) * p.K + 16 * g;
-    i32x16_t acc = {};
-    for (int k = 0; k < p.K; k += 32) {
-        i32x4_t a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
-        if (k + 16 * g < p.K) {
-            a = *(const i32x4_t*)(w + k);
-            b = *(const i32x4_t*)(x + k);
+// ---- few tokens: the weights stream once -----------------------------------------------------------
+// A workgroup of KS wavefronts takes 16 RN weight rows and all (at most 16 TT) tokens; the wavefronts
+// take 128-byte pieces of K in turn, four of them loaded ahead of their use, and their integer sums are
+// joined at the end.  A lane's 16 bytes of a weight row are its operand of the matrix instruction as
+// they come from memory.  FUSED (few tokens): every workgroup codes X itself into shared memory while
+// its first weights are on their way, which saves a launch.
+constexpr int kAhead = 4;           // pieces a batch
+constexpr int kFusedLds = 64 << 10; // bytes of X codes a workgroup keeps
+
+__host__ __device__ __forceinline__ int fused_pitch(int K) { return (K + 127) / 128 * 128 + 16; }
+
+template <int XT>
+__device__ __forceinline__ void code_rows_lds(const void* X, int K, int T, int threads, int8_t* xs, float* dx,
+                                              uint32_t (*part)[16]) {
+    const int tid = threadIdx.x, pitch = fused_pitch(K);
+    for (int t = 0; t < T; t++) {
+        uint32_t top = 0;
+        for (int k = 8 * tid; k < K; k += 8 * threads) {
+            float v[8];
+            x_load8<XT>(X, (int64_t)t * K + k, v);
+            top = max8(v, top);
         }
-        acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, acc, 0, 0, 0);
+        top = wave_max(top);
+        if ((tid & 63) == 0) part[t][tid >> 6] = top;
     }
-    const int t = t0 + r;
-    if (t >= p.T) return;
-    const float dx = p.xs[t];
+    __syncthreads();
+    for (int t = 0; t < T; t++) {
+        uint32_t top = 0;
+        for (int w = 0; w < threads >> 6; w++) top = max(top, part[t][w]);
+        const float d = row_scale(top), inv = inverse(d);
+        if (tid == 0) dx[t] = d;
+        for (int k = 8 * tid; k < pitch - 16; k += 8 * threads) {
+            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (k < K) x_load8<XT>(X, (int64_t)t * K + k, v);
+            *(uint2*)(xs + t * pitch + k) = code8x8(v, inv);
+        }
+    }
+    __syncthreads();
+}
+
+template <int TT, int RN, int KS, bool FUSED>
+__global__ __launch_bounds__(64 * KS) void w8a8_rows_kernel(W8A8Params p) {
+    constexpr int RP = 16 * RN + 4;  // pitch of the sums
+    constexpr int kRed = KS * 16 * TT * RP * 4;
+    constexpr int kLds = FUSED && kFusedLds > kRed ? kFusedLds : kRed;
+    __shared__ __attribute__((aligned(16))) int8_t lds[kLds];
+    __shared__ float dx[16];
+    __shared__ uint32_t part[16][16];
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n0 = blockIdx.x * 16 * RN, K = p.K;
+    const int8_t* w[RN];
 #pragma unroll
-    for (int i = 0; i < 16; i++) {
-        const int n = n0 + 8 * (i >> 2) + 4 * g + (i & 3);
-        if (n < p.N) store_y<YT>(p.Y, (int64_t)t * p.N + n, (float)acc[i] * dx * p.ws[n]);
+    for (int i = 0; i < RN; i++) w[i] = p.w + (int64_t)min(n0 + 16 * i + r, p.N - 1) * K;
+
+    const int units = (K + 127) / 128, pitch = fused_pitch(K);
+    auto load_w = [&](int u0, i32x4_t (&b)[kAhead][2][RN]) {
+#pragma unroll
+        for (int a = 0; a < kAhead; a++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const int k = 128 * (u0 + KS * a) + 64 * h + 16 * g;
+#pragma unroll
+                for (int i = 0; i < RN; i++) b[a][h][i] = __builtin_nontemporal_load((const i32x4_t*)(w[i] + (k < K ? k : 0)));
+            }
+    };
+    i32x4_t acc[RN][TT] = {}, cur[kAhead][2][RN];
+    load_w(wave, cur);
+    if constexpr (FUSED) {
+        if (p.xt == XT_F32)
+            code_rows_lds<XT_F32>(p.X, K, p.T, 64 * KS, lds, dx, part);
+        else if (p.xt == XT_F16)
+            code_rows_lds<XT_F16>(p.X, K, p.T, 64 * KS, lds, dx, part);
+        else
+            code_rows_lds<XT_BF16>(p.X, K, p.T, 64 * KS, lds, dx, part);
     }
+    for (int u0 = wave; u0 < units; u0 += KS * kAhead) {
+        i32x4_t next[kAhead][2][RN];
+        if (u0 + KS * kAhead < units) load_w(u0 + KS * kAhead, next);
+#pragma unroll
+        for (int a = 0; a < kAhead; a++) {
+            if (u0 + KS * a >= units) break;
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const int k = 128 * (u0 + KS * a) + 64 * h + 16 * g;
+#pragma unroll
+                for (int t = 0; t < TT; t++) {
+                    const int row = min(16 * t + r, p.T - 1);  // columns past T are never stored
+                    i32x4_t x = {0, 0, 0, 0};
+                    if constexpr (FUSED)
+                        x = *(const i32x4_t*)(lds + row * pitch + k);
+                    else if (k < K)
+                        x = *(const i32x4_t*)(p.xq + (int64_t)row * K + k);
+#pragma unroll
+                    for (int i = 0; i < RN; i++)
+                        acc[i][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(cur[a][h][i], x, acc[i][t], 0, 0, 0);
+                }
+            }
+        }
+#pragma unroll
+        for (int a = 0; a < kAhead; a++)
+#pragma unroll
+            for (int h = 0; h < 2; h++)
+#pragma unroll
+                for (int i = 0; i < RN; i++) cur[a][h][i] = next[a][h][i];
+    }
+    if constexpr (FUSED) __syncthreads();  // X's codes make room for the sums
+    int* red = (int*)lds;
+#pragma unroll
+    for (int i = 0; i < RN; i++)
+#pragma unroll
+        for (int t = 0; t < TT; t++)
+            *(i32x4_t*)(red + (wave * 16 * TT + 16 * t + r) * RP + 16 * i + 4 * g) = acc[i][t];
+    __syncthreads();
+    for (int x = threadIdx.x; x < 16 * TT * 16 * RN; x += 64 * KS) {
+        const int t = x / (16 * RN), n = x % (16 * RN);
+        if (t >= p.T || n0 + n >= p.N) continue;
+        int sum = 0;
+#pragma unroll
+        for (int v = 0; v < KS; v++) sum += red[(v * 16 * TT + t) * RP + n];
+        const float d = FUSED ? dx[t] : p.xs[t];
+        store_any(p.Y, p.yt, (int64_t)t * p.N + n0 + n, (float)sum * d * p.ws[n0 + n]);
+    }
+}
+
+// ---- many tokens: tiles ----------------------------------------------------------------------------
+// A workgroup takes BT tokens x BN weight rows; both operands pass through shared memory in stages of
+// 128 k, copied straight from memory while the previous stage is multiplied.  A row's 16-byte chunks
+// lie at slot chunk ^ (row % 8), so the 8 lanes of a read phase meet 8 different bank groups.
+template <int N>
+struct Frags {
+    i32x4_t f[N];
+};
+
+template <int MT, int NT, int WT, int WN>
+__global__ __launch_bounds__(64 * WT * WN) void w8a8_tile_kernel(W8A8Params p, int tiles_t, int tiles_n) {
+    constexpr int BT = 32 * MT * WT, BN = 32 * NT * WN, NW = WT * WN;
+    constexpr int XC = BT / 8 / NW, WC = BN / 8 / NW;  // copies of 8 rows a wavefront and stage
+    static_assert(XC * 8 * NW == BT && WC * 8 * NW == BN && NT % 2 == 0 && NW * 8192 <= (BT + BN) * 128, "tile");
+    __shared__ __attribute__((aligned(16))) int8_t s0[(BT + BN) * 128];
+    __shared__ __attribute__((aligned(16))) int8_t s1[(BT + BN) * 128];
+    const int lane = threadIdx.x & 63, r = lane & 31, g = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wt = wave % WT, wn = wave / WT;
+
+    // consecutive workgroups go to the 8 dies in turn: each die gets a run of tiles, in patches of 4
+    // token tiles, so that its cache holds the operands its workgroups share
+    const int total = tiles_t * tiles_n, per = total / 8, rem = total % 8, die = blockIdx.x & 7;
+    int lin = die * per + min(die, rem) + (blockIdx.x >> 3);
+    const int width = 4 * tiles_n, first = lin / width * 4, tall = min(tiles_t - first, 4);
+    lin %= width;
+    const int t0 = (first + lin % tall) * BT, n0 = lin / tall * BN;
+
+    const int K = p.K, stages = (K + 127) / 128;
+    const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc((void*)(p.xq + (int64_t)t0 * K), 0,
+                                                                        min(BT, p.T - t0) * K, 0x00020000);
+    const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc((void*)(p.w + (int64_t)n0 * K), 0,
+                                                                        min(BN, p.N - n0) * K, 0x00020000);
+    const int chunk = (lane & 7) ^ (lane >> 3);  // of the row, for this lane's slot
+    const int voff = (8 * wave + (lane >> 3)) * K + 16 * chunk;
+    auto copy = [&](int st, int8_t* s) {
+        const int k = 128 * st + 16 * chunk < K ? voff + 128 * st : 0x40000000;  // past K: zeros
+#pragma unroll
+        for (int i = 0; i < XC; i++) buffer_copy16_lds(xr, s + (i * NW + wave) * 1024, k + i * NW * 8 * K);
+#pragma unroll
+        for (int i = 0; i < WC; i++) buffer_copy16_lds(wr, s + BT * 128 + (i * NW + wave) * 1024, k + i * NW * 8 * K);
+    };
+    i32x16_t acc[NT][MT] = {};
+    const int xrow = (32 * MT * wt + r) * 128, wrow = (BT + 32 * NT * wn + r) * 128;
+    auto frags = [&](const int8_t* s, int j, Frags<MT>& x, Frags<NT>& w) {
+        const int slot = 16 * ((2 * j + g) ^ (lane & 7));
+#pragma unroll
+        for (int i = 0; i < MT; i++) x.f[i] = *(const i32x4_t*)(s + xrow + i * 4096 + slot);
+#pragma unroll
+        for (int i = 0; i < NT; i++) w.f[i] = *(const i32x4_t*)(s + wrow + i * 4096 + slot);
+    };
+    auto multiply = [&](const int8_t* s) {
+        Frags<MT> x[2];
+        Frags<NT> w[2];
+        frags(s, 0, x[0], w[0]);
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            if (j < 3) frags(s, j + 1, x[(j + 1) & 1], w[(j + 1) & 1]);
+#pragma unroll
+            for (int a = 0; a < NT; a++)
+#pragma unroll
+                for (int b = 0; b < MT; b++)
+                    acc[a][b] = __builtin_amdgcn_mfma_i32_32x32x32_i8(w[j & 1].f[a], x[j & 1].f[b], acc[a][b], 0, 0, 0);
+            // the next step's reads go between this step's products, and no further ahead
+            if (j < 3) {
+#pragma unroll
+                for (int i = 0; i < MT + NT; i++) {
+                    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    // stages in pairs (two arrays, so that a read of one never waits for the copies into the other); past
+    // the last stage the copies are zeros
+    copy(0, s0);
+    for (int st = 0; st < stages; st += 2) {
+        __syncthreads();
+        copy(st + 1, s1);
+        multiply(s0);
+        __syncthreads();
+        copy(st + 2, s0);
+        multiply(s1);
+    }
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // the last copy has landed before its place is used again
+    __syncthreads();
+
+    // 32 tokens x 64 rows at a time through this wavefront's 8 KiB, so that stores are whole lines
+    float* out = (float*)(s0 + wave * 8192);
+    const bool wide = p.N % 8 == 0 && ((uintptr_t)p.Y & 15) == 0;
+#pragma unroll
+    for (int b = 0; b < MT; b++) {
+        const int tb = t0 + 32 * (MT * wt + b);
+        const float d = p.xs[min(tb + r, p.T - 1)];
+#pragma unroll
+        for (int a = 0; a < NT; a += 2) {
+            const int nb = n0 + 32 * (NT * wn + a);
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const i32x16_t& c = acc[a + (i >> 2)][b];
+                const int q = 4 * (i & 3);
+                f32x4_t v = {(float)c[q] * d, (float)c[q + 1] * d, (float)c[q + 2] * d, (float)c[q + 3] * d};
+                const int at = 2 * i + g;  // which four of the 64 rows
+                *(f32x4_t*)(out + r * 64 + 4 * (at ^ (r & 15))) = v;
+            }
+            __builtin_amdgcn_wave_barrier();
+            if (wide && p.yt != XT_F32) {
+                const int n = nb + 8 * (lane & 7);
+                float s[8];
+#pragma unroll
+                for (int e = 0; e < 8; e++) s[e] = p.ws[min(n + e, p.N - 1)];
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const int t = 8 * i + (lane >> 3);
+                    const f32x4_t lo = *(const f32x4_t*)(out + t * 64 + 4 * ((2 * (lane & 7)) ^ (t & 15)));
+                    const f32x4_t hi = *(const f32x4_t*)(out + t * 64 + 4 * ((2 * (lane & 7) + 1) ^ (t & 15)));
+                    if (tb + t >= p.T || n >= p.N) continue;
+                    uint32_t y[4];
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const float u = keep_f32((e < 2 ? lo[2 * e] : hi[2 * e - 4]) * s[2 * e]);
+                        const float v = keep_f32((e < 2 ? lo[2 * e + 1] : hi[2 * e - 3]) * s[2 * e + 1]);
+                        y[e] = p.yt == XT_F16 ? (uint32_t)f32_to_f16_bits(u) | (uint32_t)f32_to_f16_bits(v) << 16
+                                              : (uint32_t)f32_to_bf16_bits(u) | (uint32_t)f32_to_bf16_bits(v) << 16;
+                    }
+                    *(uint4*)((uint16_t*)p.Y + (int64_t)(tb + t) * p.N + n) = make_uint4(y[0], y[1], y[2], y[3]);
+                }
+            } else {
+                const int n = nb + lane;
+                const float s = p.ws[min(n, p.N - 1)];
+                for (int t = 0; t < 32 && tb + t < p.T; t++) {
+                    const float v = out[t * 64 + 4 * ((lane >> 2) ^ (t & 15)) + (lane & 3)];
+                    if (n < p.N) store_any(p.Y, p.yt, (int64_t)(tb + t) * p.N + n, v * s);
+                }
+            }
+            __builtin_amdgcn_wave_barrier();
+        }
+    }
+}
+
+constexpr int kRowsMax = 128;  // tokens of the streaming kernel
+bool fused(int K, int T) { return T <= 8 && T * fused_pitch(K) <= kFusedLds; }
+
+template <int TT, int RN, int KS>
+void launch_rows(const W8A8Params& p, bool fuse, hipStream_t s) {
+    const uint32_t grid = (p.N + 16 * RN - 1) / (16 * RN);
+    if constexpr (TT == 1) {
+        if (fuse) {
+            w8a8_rows_kernel<TT, RN, KS, true><<<grid, 64 * KS, 0, s>>>(p);
+            return;
+        }
+    }
+    w8a8_rows_kernel<TT, RN, KS, false><<<grid, 64 * KS, 0, s>>>(p);
+}
+
+template <int MT, int NT, int WT, int WN>
+void launch_tile(const W8A8Params& p, hipStream_t s) {
+    const int tt = (p.T + 32 * MT * WT - 1) / (32 * MT * WT), tn = (p.N + 32 * NT * WN - 1) / (32 * NT * WN);
+    w8a8_tile_kernel<MT, NT, WT, WN><<<(uint32_t)(tt * tn), 64 * WT * WN, 0, s>>>(p, tt, tn);
 }
 
 }  // namespace
 
-size_t w8a8_workspace(int N, int K, int T) { return ((size_t)T * K + 255) / 256 * 256 + (size_t)T * 4; }
+size_t w8a8_workspace(int N, int K, int T) {
+    return fused(K, T) ? 0 : ((size_t)T * K + 255) / 256 * 256 + (size_t)T * 4;
+}
 
-hipError_t launch_w8a8(W8A8Params p, const void* X, int xt, int yt, void* ws, hipStream_t s) {
-    p.xq = (const int8_t*)ws;
-    float* xs = (float*)((char*)ws + ((size_t)p.T * p.K + 255) / 256 * 256);
-    p.xs = xs;
-    int8_t* xq = (int8_t*)ws;
-    if (xt == XT_F32)
-        x_code_kernel<XT_F32><<<p.T, 256, 0, s>>>(X, p.K, xq, xs);
-    else if (xt == XT_F16)
-        x_code_kernel<XT_F16><<<p.T, 256, 0, s>>>(X, p.K, xq, xs);
+hipError_t launch_w8a8(W8A8Params p, void* ws, hipStream_t s) {
+    const bool fuse = fused(p.K, p.T);
+    if (!fuse) {
+        float* xs = (float*)((char*)ws + ((size_t)p.T * p.K + 255) / 256 * 256);
+        int8_t* xq = (int8_t*)ws;
+        p.xq = xq;
+        p.xs = xs;
+        if (p.xt == XT_F32)
+            x_code_kernel<XT_F32><<<p.T, 256, 0, s>>>(p.X, p.K, xq, xs);
+        else if (p.xt == XT_F16)
+            x_code_kernel<XT_F16><<<p.T, 256, 0, s>>>(p.X, p.K, xq, xs);
+        else
+            x_code_kernel<XT_BF16><<<p.T, 256, 0, s>>>(p.X, p.K, xq, xs);
+    }
+    if (p.T <= 16)
+        launch_rows<1, 1, 8>(p, fuse, s);
+    else if (p.T <= 32)
+        launch_rows<2, 1, 8>(p, false, s);
+    else if (p.T <= 48)
+        launch_rows<3, 2, 4>(p, false, s);
+    else if (p.T <= 64)
+        launch_rows<4, 2, 4>(p, false, s);
+    else if (p.T <= kRowsMax)
+        launch_rows<8, 2, 4>(p, false, s);
+    else if ((int64_t)((p.T + 255) / 256) * ((p.N + 255) / 256) >= 192)
+        launch_tile<2, 4, 4, 2>(p, s);
     else
-        x_code_kernel<XT_BF16><<<p.T, 256, 0, s>>>(X, p.K, xq, xs);
-    const dim3 grid((p.N + 127) / 128, (p.T + 31) / 32);
-    if (yt == XT_F32)
-        w8a8_kernel<XT_F32><<<grid, 256, 0, s>>>(p);
-    else if (yt == XT_F16)
-        w8a8_kernel<XT_F16><<<grid, 256, 0, s>>>(p);
-    else
-        w8a8_kernel<XT_BF16><<<grid, 256, 0, s>>>(p);
+        launch_tile<2, 2, 2, 2>(p, s);
     return hipGetLastError();
 }
 
