@@ -8,41 +8,10 @@
 // memory.
 #include <hip/hip_runtime.h>
 
-#include "qg_device.hpp"
-#include "qg_internal.hpp"
+#include "qg_attn8.hpp"
 
 namespace qg {
 namespace {
-
-typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kNegInf = -__builtin_inff();
-// A weight enters the second product as f16: p * vs * 2^(kBase - ev), where 2^ev >= the V scales so
-// far.  The running maximum may lag by kLag (in powers of two) before the sums are rescaled, so values
-// stay at or below 2^15 and keep f16's full precision down to 2^-23 of the row's largest.
-constexpr float kLag = 6.f;
-constexpr int kBase = 9;
-
-// Four codes as four f16 values, exactly: byte ^ 0x80 below 0x64 is 1024 + (code + 128).
-__device__ __forceinline__ void codes4_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-    const uint32_t u = w ^ 0x80808080u;
-    const half2_t bias = {(_Float16)1152.f, (_Float16)1152.f};
-    const half2_t a = __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u)) - bias;
-    const half2_t b = __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u)) - bias;
-    lo = __builtin_bit_cast(uint32_t, a);
-    hi = __builtin_bit_cast(uint32_t, b);
-}
-__device__ __forceinline__ half8_t codes8_f16(uint32_t w0, uint32_t w1) {
-    u32x4 r;
-    uint32_t a, b;
-    codes4_f16(w0, a, b);
-    r[0] = a, r[1] = b;
-    codes4_f16(w1, a, b);
-    r[2] = a, r[3] = b;
-    return __builtin_bit_cast(half8_t, r);
-}
 
 // Maximum / sum over the four lane groups of 16 (lanes l, l ^ 16, l ^ 32, l ^ 48).
 __device__ __forceinline__ float groups_max(float v) {
@@ -52,19 +21,6 @@ __device__ __forceinline__ float groups_max(float v) {
 __device__ __forceinline__ float groups_sum(float v) {
     v += __shfl_xor(v, 16);
     return v + __shfl_xor(v, 32);
-}
-
-// What the 16 rows of a tile see together, and how the splits divide it.
-struct TileRange {
-    int lo, hi, nact;  // tokens [lo, hi), lo a multiple of 64; splits that have any of them
-};
-__device__ __forceinline__ TileRange tile_range(const AttnParams& a, const KvSpan& sp, int r0, int rows) {
-    const int i0 = r0 / a.group, i1 = (min(r0 + rows, sp.n * a.group) - 1) / a.group;
-    TileRange t;
-    t.lo = kv8_sight(sp, i0, a.causal, a.window).lo & ~63;
-    t.hi = kv8_sight(sp, i1, a.causal, a.window).hi;
-    t.nact = (t.hi - t.lo + a.chunk - 1) / a.chunk;
-    return t;
 }
 
 // One workgroup takes 16 rows (query rows times the heads that share a K/V head, counted together) and
@@ -130,7 +86,7 @@ __global__ __launch_bounds__(256) void attn8_rows_kernel(AttnParams a) {
         }
         top = max(top, (uint32_t)__shfl_xor((int)top, 16));
         top = max(top, (uint32_t)__shfl_xor((int)top, 32));
-        const int eb = top >> 23, ex = eb == 0 || eb == 255 ? 0 : 141 - eb;
+        const int ex = q_exponent(top);
         qs = ldexpf(a.scale * kLog2e, -ex);
 #pragma unroll
         for (int i = 0; i < NH; i++)
@@ -297,7 +253,7 @@ __global__ __launch_bounds__(256) void attn8_join_kernel(AttnParams a) {
     const KvSpan sp = kv8_span(a.q, s);
     if (i >= sp.n) return;
     const int r = i * a.group + head % a.group;
-    const TileRange tr = tile_range(a, sp, r & ~15, 16);
+    const TileRange tr = tile_range(a, sp, r / a.tile_rows * a.tile_rows, a.tile_rows);
     if (tr.nact <= 1) return;
     const int64_t p0 = ((int64_t)(sp.r0 + i) * a.q_heads + head) * a.splits;
     float mt = kNegInf;
@@ -345,7 +301,12 @@ __global__ __launch_bounds__(256) void attn8_join_kernel(AttnParams a) {
 template <int XT, int D>
 hipError_t launch_one(const AttnParams& a, hipStream_t s) {
     const int64_t grid = (int64_t)a.q.seqs * a.splits * a.c.heads * a.tiles;
-    attn8_rows_kernel<XT, D><<<dim3((uint32_t)grid), 256, 0, s>>>(a);
+    if (a.tile_rows > 16) {
+        const hipError_t e = launch_attn8_tile(a, XT, s);
+        if (e != hipSuccess) return e;
+    } else {
+        attn8_rows_kernel<XT, D><<<dim3((uint32_t)grid), 256, 0, s>>>(a);
+    }
     if (a.splits > 1)
         attn8_join_kernel<XT, D><<<dim3((uint32_t)(a.q.max_new * a.q_heads), a.q.seqs), 256, 0, s>>>(a);
     return hipGetLastError();
@@ -366,25 +327,39 @@ hipError_t launch_dim(const AttnParams& a, hipStream_t s) {
 }  // namespace
 
 namespace {
-constexpr int64_t kMinChunk = 1024, kFill = 2048;
+// Rows a K/V head (query rows times heads of the group) from which the tile kernel takes over.
+constexpr int64_t kTileFrom = 64;
+constexpr int64_t kMinChunk = 1024, kFill = 2048, kFillTile = 512;
 // Splits that fill the card several times over.
 int64_t wanted_splits(const AttnParams& a) {
-    const int64_t base = (int64_t)a.q.seqs * a.c.heads * a.tiles;
-    return (kFill + base - 1) / base;
+    const int64_t base = (int64_t)a.q.seqs * a.c.heads * a.tiles, fill = a.tile_rows > 16 ? kFillTile : kFill;
+    return (fill + base - 1) / base;
+}
+void set_tiles(AttnParams& a, int xt) {
+    const int64_t rows = (int64_t)a.q.max_new * a.group;
+    a.tile_rows = rows >= kTileFrom ? attn8_tile_rows(xt, a.c.dim) : 16;
+    a.tiles = (int)((rows + a.tile_rows - 1) / a.tile_rows);
 }
 }  // namespace
 
-int attn8_max_splits(const AttnParams& a) {
-    const int64_t most = (a.q.max_kv + kMinChunk - 1) / kMinChunk, want = wanted_splits(a);
+int attn8_max_splits(AttnParams a) {
+    const int64_t most = (a.q.max_kv + kMinChunk - 1) / kMinChunk;
+    int64_t want = 1;
+    for (int xt : {XT_F32, XT_F16}) {
+        set_tiles(a, xt);
+        const int64_t w = wanted_splits(a);
+        if (w > want) want = w;
+    }
     return (int)(most < want ? most : want);
 }
 
-// Tiles and splits of a call, from the host's bounds alone.
-void attn8_plan(AttnParams& a) {
-    a.tiles = (int)(((int64_t)a.q.max_new * a.group + 15) / 16);
-    // tokens that a tile of 16 rows may see: all, or its window, started at a multiple of 64
+// Kernel, tiles and splits of a call, from the host's bounds alone.
+void attn8_plan(AttnParams& a, int xt) {
+    set_tiles(a, xt);
+    // tokens that a tile's rows may see: all, or their window, started at a multiple of 64
     int64_t span = a.q.max_kv;
-    if (a.causal && a.window > 0 && (int64_t)a.window + 16 / a.group + 65 < span) span = a.window + 16 / a.group + 65;
+    const int64_t seen = (int64_t)a.window + a.tile_rows / a.group + 65;
+    if (a.causal && a.window > 0 && seen < span) span = seen;
     const int64_t want = wanted_splits(a);
     int64_t chunk = (span + want - 1) / want;
     if (chunk < kMinChunk) chunk = kMinChunk;

@@ -1,0 +1,67 @@
+// qg_attn8.hpp -- what the kernels of the attention over the 8-bit cache share.
+//
+//   o = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale q . k_j) over the tokens j that the row may see.
+//
+// K and V codes are integers of at most 8 bits, exact in f16, so the products run on the f16 matrix
+// instructions with f32 sums: q enters as f16 after an exact power of two per row (f32 q as two such
+// f16 pieces), the weights as f16 after the block's V scale.
+#pragma once
+
+#include "qg_device.hpp"
+#include "qg_internal.hpp"
+
+namespace qg {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNegInf = -__builtin_inff();
+// A weight enters the second product as f16: p * vs * 2^(kBase - ev), where 2^ev >= the V scales so
+// far.  The running maximum may lag by kLag (in powers of two) before the sums are rescaled, so values
+// stay at or below 2^15 and keep f16's full precision down to 2^-23 of the row's largest.
+constexpr float kLag = 6.f;
+constexpr int kBase = 9;
+
+// Four codes as four f16 values, exactly: byte ^ 0x80 below 0x64 is 1024 + (code + 128).
+__device__ __forceinline__ void codes4_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const uint32_t u = w ^ 0x80808080u;
+    const half2_t bias = {(_Float16)1152.f, (_Float16)1152.f};
+    const half2_t a = __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u)) - bias;
+    const half2_t b = __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u)) - bias;
+    lo = __builtin_bit_cast(uint32_t, a);
+    hi = __builtin_bit_cast(uint32_t, b);
+}
+__device__ __forceinline__ half8_t codes8_f16(uint32_t w0, uint32_t w1) {
+    u32x4 r;
+    uint32_t a, b;
+    codes4_f16(w0, a, b);
+    r[0] = a, r[1] = b;
+    codes4_f16(w1, a, b);
+    r[2] = a, r[3] = b;
+    return __builtin_bit_cast(half8_t, r);
+}
+
+// What the rows r0 .. r0 + rows - 1 of a tile see together, and how the splits divide it.
+struct TileRange {
+    int lo, hi, nact;  // tokens [lo, hi), lo a multiple of 64; splits that have any of them
+};
+__device__ __forceinline__ TileRange tile_range(const AttnParams& a, const KvSpan& sp, int r0, int rows) {
+    const int i0 = r0 / a.group, i1 = (min(r0 + rows, sp.n * a.group) - 1) / a.group;
+    TileRange t;
+    t.lo = kv8_sight(sp, i0, a.causal, a.window).lo & ~63;
+    t.hi = kv8_sight(sp, i1, a.causal, a.window).hi;
+    t.nact = (t.hi - t.lo + a.chunk - 1) / a.chunk;
+    return t;
+}
+
+// Power of two that brings the largest of a row's values (its bits without the sign) into [2^14, 2^15).
+__device__ __forceinline__ int q_exponent(uint32_t top) {
+    const int eb = top >> 23;
+    return eb == 0 || eb == 255 ? 0 : 141 - eb;
+}
+
+// The kernel of tiles of 32 .. 256 rows (qg_attn8_tile.hip), and its rows a workgroup for a type and dim.
+int attn8_tile_rows(int xt, int dim);
+hipError_t launch_attn8_tile(const AttnParams& a, int xt, hipStream_t s);
+
+}  // namespace qg

@@ -78,7 +78,7 @@ qg_status run_kv8(bool write, const qg_kv8_cache* cache, const qg_kv8_seqs* seqs
 
 // Shared by qg_attn_kv8 and its workspace query.
 qg_status attn_params(const qg_kv8_cache* cache, const qg_kv8_seqs* seqs, int q_heads, int causal, int window,
-                      AttnParams& a) {
+                      int xt, AttnParams& a) {
     const qg_status st = check_kv8(cache, seqs, a.c, a.q);
     if (st != QG_OK) return st;
     if (q_heads < a.c.heads || q_heads > 65536 || q_heads % a.c.heads != 0) return QG_ESHAPE;
@@ -88,7 +88,7 @@ qg_status attn_params(const qg_kv8_cache* cache, const qg_kv8_seqs* seqs, int q_
     a.window = window > 0 ? window : 0;
     if (empty(a.q)) return QG_OK;
     if ((int64_t)a.q.max_new * q_heads >= ((int64_t)1 << 31)) return QG_ESHAPE;
-    qg::attn8_plan(a);
+    qg::attn8_plan(a, xt);
     if ((int64_t)a.q.seqs * a.splits * a.c.heads * a.tiles >= ((int64_t)1 << 31)) return QG_ESHAPE;
     return QG_OK;
 }
@@ -111,7 +111,7 @@ qg_status qg_kv8_read(const qg_kv8_cache* cache, const qg_kv8_seqs* seqs, void* 
 
 size_t qg_attn_kv8_workspace(const qg_kv8_cache* cache, const qg_kv8_seqs* seqs, int q_heads) {
     AttnParams a{};
-    if (attn_params(cache, seqs, q_heads, 1, 0, a) != QG_OK || empty(a.q)) return 0;
+    if (attn_params(cache, seqs, q_heads, 1, 0, QG_X_F32, a) != QG_OK || empty(a.q)) return 0;
     a.splits = qg::attn8_max_splits(a);
     return qg::attn8_workspace(a);
 }
@@ -121,7 +121,7 @@ qg_status qg_attn_kv8(const qg_kv8_cache* cache, const qg_kv8_seqs* seqs, const 
                       int causal, int window, void* workspace, size_t ws_bytes, hipStream_t stream) {
     if (!xt_ok(xt)) return QG_EINVAL;
     AttnParams a{};
-    qg_status st = attn_params(cache, seqs, q_heads, causal, window, a);
+    qg_status st = attn_params(cache, seqs, q_heads, causal, window, xt, a);
     if (st != QG_OK || empty(a.q)) return st;
     st = check_rows(q, xt, q_row, q_head, a.q.T, q_heads, a.c.dim, false);
     if (st != QG_OK) return st;

@@ -123,11 +123,11 @@ struct AttnParams {
     int q_heads, group;
     float scale;
     int causal, window;
-    int tiles, splits, chunk;              // row tiles a K/V head, splits of the tokens, tokens a split
+    int tile_rows, tiles, splits, chunk;   // rows a tile, tiles a K/V head, splits of the tokens, tokens a split
     float *part_o, *part_ml;               // splits > 1: sums [row][head][split][dim], (maximum, weight sum)
 };
-void attn8_plan(AttnParams& a);
-int attn8_max_splits(const AttnParams& a);  // of any window
+void attn8_plan(AttnParams& a, int xt);
+int attn8_max_splits(AttnParams a);  // of any window and type
 size_t attn8_workspace(const AttnParams& a);
 hipError_t launch_attn8(AttnParams a, int xt, float* ws, hipStream_t s);
 
