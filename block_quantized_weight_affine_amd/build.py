@@ -25,10 +25,14 @@ FLAGS = [
     "-I", os.path.join(ROOT, "include"), "-I", CSRC,
 ]
 
+# the attention kernels' sums stay in vector registers, where the softmax works on them
+_SUMS = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+EXTRA = {"qg_attn8.hip": _SUMS, "qg_attn8_tile.hip": _SUMS}
+
 
 def _compile(src: str) -> str:
     obj = os.path.join(OBJ, os.path.splitext(src)[0] + ".o")
-    cmd = ["hipcc", *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
+    cmd = ["hipcc", *FLAGS, *EXTRA.get(src, []), "-c", os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"hipcc failed for {src}:\n{r.stdout}\n{r.stderr}")

@@ -8,6 +8,8 @@
 // memory.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "qg_attn8.hpp"
 
 namespace qg {
@@ -23,6 +25,11 @@ __device__ __forceinline__ float groups_sum(float v) {
     return v + __shfl_xor(v, 32);
 }
 
+// Wavefronts a SIMD of the rows kernel: q, two loads and the sums take (3 + pieces) dim / 4 registers a lane.
+constexpr int rows_waves(int pieces, int dim) {
+    return (3 + pieces) * dim / 4 <= 128 ? 3 : (3 + pieces) * dim / 4 <= 200 ? 2 : 1;
+}
+
 // One workgroup takes 16 rows (query rows times the heads that share a K/V head, counted together) and
 // one split of the tokens they see; its wavefronts take 64 tokens in turn and are joined at the end.
 //
@@ -30,13 +37,15 @@ __device__ __forceinline__ float groups_sum(float v) {
 // m-th instruction = token 4m + r % 4 of block r / 4, so result lane (row l % 16, group g = l / 16)
 // holds all 16 tokens of block g.  That is what the second product V^T P^T wants as its B operand, so
 // the weights never move between lanes, every lane has one K and one V scale, and both code loads are
-// 16 bytes a lane as the cache holds them.
+// 16 bytes a lane as the cache holds them.  The next tokens' K is loaded as soon as the first product is
+// done with this one's registers, V after the second, the table's entry one turn earlier.
 template <int XT, int D>
-__global__ __launch_bounds__(256) void attn8_rows_kernel(AttnParams a) {
+__global__ __launch_bounds__(256, rows_waves(XT == XT_F32 ? 2 : 1, D)) void attn8_rows_kernel(AttnParams a) {
     constexpr int NP = XT == XT_F32 ? 2 : 1;  // f16 pieces of a q value and of a weight
     constexpr int NH = (D + 63) / 64;         // 16-byte K loads a token
     constexpr int NT = D / 16;
     constexpr int DH = D > 128 ? D / 2 : D;   // dims joined at a time
+    constexpr bool kTight = NP * D > 128;
     __shared__ float sh_o[4][16][DH + 4];
     __shared__ float sh_m[4][16], sh_l[4][16];
 
@@ -58,32 +67,68 @@ __global__ __launch_bounds__(256) void attn8_rows_kernel(AttnParams a) {
     // this lane's row
     const int r = tile * 16 + col, ri = min(r, rows - 1) / a.group;
     const int head = h * a.group + min(r, rows - 1) % a.group;
-    KvSight see = kv8_sight(sp, ri, a.causal, a.window);
-    if (r >= rows) see.hi = see.lo;
+    const KvSight see = kv8_sight(sp, ri, a.causal, a.window);
+    const int lo_any = kv8_sight(sp, tile * 16 / a.group, a.causal, a.window).lo;
+    const int lo_all = kv8_sight(sp, (min(tile * 16 + 16, rows) - 1) / a.group, a.causal, a.window).lo;
+    const int hi_all = kv8_sight(sp, tile * 16 / a.group, a.causal, a.window).hi;
+
+    // block of this lane's group in the 64 tokens from tb, and of the group whose K it loads
+    auto entry = [&](int tb) {
+        const uint32_t pi = kv8_div((uint32_t)((tb >> 4) + g), a.c.nb, a.c.magic);
+        return a.q.table[(int64_t)s * a.q.width + min(pi, (uint32_t)a.q.width - 1)];
+    };
+    auto index = [&](int tb, int page) {
+        const int blk = (tb >> 4) + g;
+        const uint32_t pi = kv8_div((uint32_t)blk, a.c.nb, a.c.magic);
+        const bool ok = (16 * blk < t1) & (16 * blk + 16 > lo_any) & (pi < (uint32_t)a.q.width) &
+                        ((uint32_t)page < (uint32_t)a.c.pages);
+        return ok ? (int)(((uint32_t)page * a.c.heads + h) * a.c.nb + ((uint32_t)blk - pi * (uint32_t)a.c.nb)) : -1;
+    };
+    uint4 kw[4][NH], vw[NT];
+    auto load_k = [&](int bi) {
+        const int kbi = max(0, __shfl(bi, (lane & 12) * 4));
+        const int8_t* kp = a.c.kc + (int64_t)kbi * (16 * D) + (lane & 3) * 16;
+#pragma unroll
+        for (int mi = 0; mi < 4; mi++)
+#pragma unroll
+            for (int i = 0; i < NH; i++)
+                kw[mi][i] = *(const uint4*)(kp + ((min(4 * i + g, NT - 1) * 16) + 4 * mi) * 16);
+    };
+    auto load_v = [&](int bi) {
+        const int8_t* vp = a.c.vc + (int64_t)max(bi, 0) * (16 * D) + col * 16;
+#pragma unroll
+        for (int i = 0; i < NT; i++) vw[i] = *(const uint4*)(vp + i * 256);
+    };
+    const int first = t0 + 64 * wave;
+    const int page0 = entry(first), page1 = entry(first + 256);
+
+    float x[NH][16];
+    const int64_t at = (int64_t)(sp.r0 + ri) * a.q_row + head * a.q_head;
+#pragma unroll
+    for (int i = 0; i < NH; i++) {
+        const int ch = 4 * i + g;
+        float lo[8] = {}, hi[8] = {};
+        if (ch < NT) {
+            x_load8<XT>(a.Q, at + 16 * ch, lo);
+            x_load8<XT>(a.Q, at + 16 * ch + 8, hi);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; e++) x[i][e] = lo[e], x[i][8 + e] = hi[e];
+    }
+    int bi = index(first, page0), page = page1;
+    load_k(bi);
+    if (!kTight) load_v(bi);
+    float ks = a.c.ks[max(bi, 0)], vs = a.c.vs[max(bi, 0)];
 
     // q as f16 pieces, scaled so that the row's largest lies in [2^14, 2^15)
     half8_t qf[NP][NH][2];
     float qs;
     {
-        float x[NH][16];
-        const int64_t at = (int64_t)(sp.r0 + ri) * a.q_row + head * a.q_head;
         uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < NH; i++) {
-            const int ch = 4 * i + g;
-            if (ch < NT) {
-                float lo[8], hi[8];
-                x_load8<XT>(a.Q, at + 16 * ch, lo);
-                x_load8<XT>(a.Q, at + 16 * ch + 8, hi);
-#pragma unroll
-                for (int e = 0; e < 8; e++) x[i][e] = lo[e], x[i][8 + e] = hi[e];
-            } else {
-#pragma unroll
-                for (int e = 0; e < 16; e++) x[i][e] = 0.f;
-            }
+        for (int i = 0; i < NH; i++)
 #pragma unroll
             for (int e = 0; e < 16; e++) top = max(top, __float_as_uint(x[i][e]) & 0x7fffffffu);
-        }
         top = max(top, (uint32_t)__shfl_xor((int)top, 16));
         top = max(top, (uint32_t)__shfl_xor((int)top, 32));
         const int ex = q_exponent(top);
@@ -99,91 +144,92 @@ __global__ __launch_bounds__(256) void attn8_rows_kernel(AttnParams a) {
             }
     }
 
+    if (kTight) {  // q's values make room for V's
+        __builtin_amdgcn_sched_barrier(0);
+        load_v(bi);
+    }
+
     f32x4_t o[NT];
 #pragma unroll
     for (int i = 0; i < NT; i++) o[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    float m = kNegInf, l = 0.f;
-    int ev = -1000;  // exponent that the V scales are taken relative to
+    float m = kNegInf, limit = kNegInf, mu = (float)kBase, l = 0.f;
+    int e0 = bi < 0 ? -1000 : v_exponent(vs);
+    e0 = max(e0, __shfl_xor(e0, 16));
+    e0 = __builtin_amdgcn_readfirstlane(max(e0, __shfl_xor(e0, 32)));
+    if (e0 < -500) e0 = 0;
 
-    const int krow = (lane & 15) >> 2;  // block of the four that this lane loads K of
-    for (int tb = t0 + 64 * wave; tb < t1; tb += 256) {
-        const int blk = (tb >> 4) + g;
-        const int bi = 16 * blk < tr.hi ? kv8_block(a.c, a.q, s, h, blk) : -1;
-        const int kbi = max(0, __shfl(bi, krow * 16));
-        const int8_t* kp = a.c.kc + (int64_t)kbi * (16 * D) + (lane & 3) * 16;
-        const int8_t* vp = a.c.vc + (int64_t)max(bi, 0) * (16 * D) + col * 16;
-        // tokens of this lane's block that its row sees: [jl, jh)
-        const int jl = see.lo - 16 * blk, jh = bi < 0 ? 0 : see.hi - 16 * blk;
-        const bool any = jl < 16 && jh > 0 && jl < jh;
-        const float ks = any ? a.c.ks[max(bi, 0)] * qs : 0.f;
-        const float vb = bi < 0 ? 0.f : a.c.vs[bi], vs = any ? vb : 0.f;
-
-        uint4 kw[4][NH];
-#pragma unroll
-        for (int mi = 0; mi < 4; mi++)
-#pragma unroll
-            for (int i = 0; i < NH; i++)
-                kw[mi][i] = *(const uint4*)(kp + ((min(4 * i + g, NT - 1) * 16) + 4 * mi) * 16);
-        uint4 vw[NT];
-#pragma unroll
-        for (int i = 0; i < NT; i++) vw[i] = *(const uint4*)(vp + i * 256);
-
-        float p[16];
+    for (int tb = first; tb < t1; tb += 256) {
+        f32x4_t acc[4];
 #pragma unroll
         for (int mi = 0; mi < 4; mi++) {
-            f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+            acc[mi] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < NH; i++) {
                 const half8_t k0 = codes8_f16(kw[mi][i].x, kw[mi][i].y), k1 = codes8_f16(kw[mi][i].z, kw[mi][i].w);
 #pragma unroll
                 for (int n = 0; n < NP; n++) {
-                    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, qf[n][i][0], acc, 0, 0, 0);
-                    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, qf[n][i][1], acc, 0, 0, 0);
+                    acc[mi] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, qf[n][i][0], acc[mi], 0, 0, 0);
+                    acc[mi] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, qf[n][i][1], acc[mi], 0, 0, 0);
                 }
             }
+        }
+        const int was = bi;
+        const float vnow = vs, kf = vs - vs == 0.f ? ks * qs : __builtin_nanf("");
+        const bool more = tb + 256 < t1;
+        if (more) {
+            bi = index(tb + 256, page);
+            load_k(bi);
+            ks = a.c.ks[max(bi, 0)];
+            vs = a.c.vs[max(bi, 0)];
+            page = entry(tb + 512);
+        }
+        const float lv = v_power(vnow, e0);
+        float p[16];
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const int j = 4 * mi + e;
-                p[j] = j >= jl && j < jh ? acc[e] * ks : kNegInf;
-            }
+        for (int j = 0; j < 16; j++) p[j] = acc[j >> 2][j & 3] * kf;
+        if (tb < lo_all || tb + 64 > hi_all || __any(was < 0)) {
+            // tokens of this lane's block that its row sees: [jl, jh)
+            const int jl = see.lo - tb - 16 * g, jh = was < 0 ? 0 : see.hi - tb - 16 * g;
+#pragma unroll
+            for (int j = 0; j < 16; j++) p[j] = ((j >= jl) & (j < jh)) ? p[j] : kNegInf;
         }
         float top = p[0];
 #pragma unroll
         for (int j = 1; j < 16; j++) top = fmaxf(top, p[j]);
-        top = groups_max(top);
-        // the largest V scale's exponent, the same in the whole wavefront
-        const int eb = __builtin_amdgcn_readfirstlane((int)(__float_as_uint(groups_max(fabsf(vb))) >> 23)) - 126;
-        if (eb > ev || __any(top > m + kLag)) {
-            const float mn = fmaxf(m, top);
-            const int en = max(ev, eb);
-            const float f = m == kNegInf ? 0.f : ldexpf(__builtin_amdgcn_exp2f(m - mn), ev - en);
-            l *= m == kNegInf ? 0.f : __builtin_amdgcn_exp2f(m - mn);
+        top += lv;
+        if (__any(top > limit)) {
+            const float mn = fmaxf(m, groups_max(top));
+            const float f = m == kNegInf ? 0.f : __builtin_amdgcn_exp2f(m - mn);
+            l *= f;
 #pragma unroll
             for (int i = 0; i < NT; i++) o[i] *= f;
             m = mn;
-            ev = en;
+            limit = mn + kLag;
+            mu = mn == kNegInf ? (float)kBase : (float)kBase - mn;
         }
-        const float mu = m == kNegInf ? 0.f : m;
-        const float vn = ldexpf(vs, kBase - ev);
+        const float c = lv + mu;
         half8_t pf[NP][2];
+        float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < 16; j++) {
-            const float w = __builtin_amdgcn_exp2f(p[j] - mu);
-            l += w;
-            const float wv = w * vn;
-            const _Float16 hi = (_Float16)wv;
+            const float w = __builtin_amdgcn_exp2f(p[j] + c);
+            sum += w;
+            const _Float16 hi = (_Float16)w;
             pf[0][j >> 3][j & 7] = hi;
-            if constexpr (NP == 2) pf[1][j >> 3][j & 7] = (_Float16)(wv - (float)hi);
+            if constexpr (NP == 2) pf[1][j >> 3][j & 7] = (_Float16)(w - (float)hi);
         }
+        l = fmaf(sum, __builtin_amdgcn_exp2f(-lv), l);
+        const half2_t f = __builtin_bit_cast(half2_t, v_sign(vnow)), fc = f * (half2_t){(_Float16)-1152.f, (_Float16)-1152.f};
 #pragma unroll
         for (int i = 0; i < NT; i++) {
-            const half8_t v0 = codes8_f16(vw[i].x, vw[i].y), v1 = codes8_f16(vw[i].z, vw[i].w);
+            const half8_t v0 = codes8_f16(vw[i].x, vw[i].y, f, fc), v1 = codes8_f16(vw[i].z, vw[i].w, f, fc);
 #pragma unroll
             for (int n = 0; n < NP; n++) {
                 o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pf[n][0], o[i], 0, 0, 0);
                 o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pf[n][1], o[i], 0, 0, 0);
             }
         }
+        if (more) load_v(bi);
     }
 
     // join the wavefronts
@@ -194,7 +240,7 @@ __global__ __launch_bounds__(256) void attn8_rows_kernel(AttnParams a) {
     }
     __syncthreads();
     const float mt = fmaxf(fmaxf(sh_m[0][col], sh_m[1][col]), fmaxf(sh_m[2][col], sh_m[3][col]));
-    const float f = m == kNegInf ? 0.f : ldexpf(__builtin_amdgcn_exp2f(m - mt), ev - kBase);
+    const float f = m == kNegInf ? 0.f : ldexpf(__builtin_amdgcn_exp2f(m - mt), e0);
 #pragma unroll
     for (int d0 = 0; d0 < D; d0 += DH) {
         if (d0) __syncthreads();
@@ -240,16 +286,25 @@ __global__ __launch_bounds__(256) void attn8_rows_kernel(AttnParams a) {
     }
 }
 
-// Joins the splits of one row and head, one workgroup each: its wavefronts take the splits in turn.
-// The order of the sums is fixed, so results repeat bit for bit.
-template <int XT, int D>
+template <int XT>
+__device__ __forceinline__ void store2(void* o, int64_t at, float a, float b) {
+    if constexpr (XT == XT_F32)
+        *(float2*)((float*)o + at) = make_float2(a, b);
+    else
+        *(uint32_t*)((uint16_t*)o + at) = (uint32_t)f32_to_16<XT>(keep_f32(a)) | (uint32_t)f32_to_16<XT>(keep_f32(b)) << 16;
+}
+
+// Joins the splits of a row and head: W wavefronts take the splits in turn, 4 / W rows a workgroup.  The
+// order of the sums is fixed, so results repeat bit for bit.
+template <int XT, int D, int W>
 __global__ __launch_bounds__(256) void attn8_join_kernel(AttnParams a) {
     constexpr int NV = (D + 127) / 128;  // pairs of dims a lane
-    __shared__ float sh_l[4];
-    __shared__ float sh_o[4][D];
+    __shared__ float sh_o[W > 1 ? 4 : 1][D];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int s = blockIdx.y, i = blockIdx.x / a.q_heads, head = blockIdx.x % a.q_heads;
+    const int s = blockIdx.y;
+    const uint32_t x = W > 1 ? blockIdx.x : 4 * blockIdx.x + wave;
+    const int i = x / (uint32_t)a.q_heads, head = x % (uint32_t)a.q_heads;
     const KvSpan sp = kv8_span(a.q, s);
     if (i >= sp.n) return;
     const int r = i * a.group + head % a.group;
@@ -265,38 +320,60 @@ __global__ __launch_bounds__(256) void attn8_join_kernel(AttnParams a) {
     float2 o[NV];
 #pragma unroll
     for (int e = 0; e < NV; e++) o[e] = make_float2(0.f, 0.f);
-    for (int x = wave; x < tr.nact; x += 4) {
-        const float2 ml = *(const float2*)(a.part_ml + (p0 + x) * 2);
+    for (int x0 = 0; x0 < tr.nact; x0 += 64) {
+        // a lane has a split's factor; the sums take eight splits' loads at a time
+        float2 ml = make_float2(kNegInf, 0.f);
+        if (x0 + lane < tr.nact) ml = *(const float2*)(a.part_ml + (p0 + x0 + lane) * 2);
         const float w = __builtin_amdgcn_exp2f(ml.x - mu);
-        l += ml.y * w;
+        l += ml.y == 0.f ? 0.f : ml.y * w;
+        const int n = min(tr.nact - x0, 64);
+        for (int y = W > 1 ? wave : 0; y < n; y += 8 * W) {
+            float2 v[8][NV];
 #pragma unroll
-        for (int e = 0; e < NV; e++) {
-            const int d = 2 * lane + 128 * e;
-            if (d < D) {
-                const float2 v = *(const float2*)(a.part_o + (p0 + x) * D + d);
-                o[e].x += v.x * w;
-                o[e].y += v.y * w;
+            for (int k = 0; k < 8; k++)
+#pragma unroll
+                for (int e = 0; e < NV; e++) {
+                    const int d = 2 * lane + 128 * e;
+                    v[k][e] = *(const float2*)(a.part_o + (p0 + x0 + min(y + k * W, n - 1)) * D + (d < D ? d : 0));
+                }
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+                const float f = y + k * W < n ? __shfl(w, y + k * W) : 0.f;
+#pragma unroll
+                for (int e = 0; e < NV; e++)
+                    if (y + k * W < n) o[e].x = fmaf(v[k][e].x, f, o[e].x), o[e].y = fmaf(v[k][e].y, f, o[e].y);
             }
         }
     }
-    if (lane == 0) sh_l[wave] = l;
+#pragma unroll
+    for (int e = 1; e < 64; e <<= 1) l += __shfl_xor(l, e);
+    const int64_t at = (int64_t)(sp.r0 + i) * a.o_row + head * a.o_head;
+    if constexpr (W == 1) {
+#pragma unroll
+        for (int e = 0; e < NV; e++) {
+            const int d = 2 * lane + 128 * e;
+            if (d < D) store2<XT>(a.O, at + d, l == 0.f ? 0.f : o[e].x / l, l == 0.f ? 0.f : o[e].y / l);
+        }
+        return;
+    }
 #pragma unroll
     for (int e = 0; e < NV; e++) {
         const int d = 2 * lane + 128 * e;
         if (d < D) *(float2*)&sh_o[wave][d] = o[e];
     }
     __syncthreads();
-    const int d = threadIdx.x;
+    const int d = 2 * threadIdx.x;
     if (d >= D) return;
-    const float lt = sh_l[0] + sh_l[1] + sh_l[2] + sh_l[3];
-    const float v = sh_o[0][d] + sh_o[1][d] + sh_o[2][d] + sh_o[3][d];
-    const float y = lt == 0.f ? 0.f : v / lt;
-    const int64_t at = (int64_t)(sp.r0 + i) * a.o_row + head * a.o_head + d;
-    if constexpr (XT == XT_F32)
-        ((float*)a.O)[at] = y;
-    else
-        ((uint16_t*)a.O)[at] = f32_to_16<XT>(keep_f32(y));
+    float y[2];
+#pragma unroll
+    for (int e = 0; e < 2; e++) {
+        const float v = sh_o[0][d + e] + sh_o[W > 1 ? 1 : 0][d + e] + sh_o[W > 1 ? 2 : 0][d + e] + sh_o[W > 1 ? 3 : 0][d + e];
+        y[e] = l == 0.f ? 0.f : v / l;
+    }
+    store2<XT>(a.O, at + d, y[0], y[1]);
 }
+
+constexpr int64_t kJoinWide = 2048;  // rows that are joined by a workgroup each
 
 template <int XT, int D>
 hipError_t launch_one(const AttnParams& a, hipStream_t s) {
@@ -307,8 +384,13 @@ hipError_t launch_one(const AttnParams& a, hipStream_t s) {
     } else {
         attn8_rows_kernel<XT, D><<<dim3((uint32_t)grid), 256, 0, s>>>(a);
     }
-    if (a.splits > 1)
-        attn8_join_kernel<XT, D><<<dim3((uint32_t)(a.q.max_new * a.q_heads), a.q.seqs), 256, 0, s>>>(a);
+    if (a.splits > 1) {
+        const uint32_t rows = (uint32_t)a.q.max_new * (uint32_t)a.q_heads;
+        if ((int64_t)rows * a.q.seqs <= kJoinWide)
+            attn8_join_kernel<XT, D, 4><<<dim3(rows, a.q.seqs), 256, 0, s>>>(a);
+        else
+            attn8_join_kernel<XT, D, 1><<<dim3((rows + 3) / 4, a.q.seqs), 256, 0, s>>>(a);
+    }
     return hipGetLastError();
 }
 
@@ -329,16 +411,20 @@ hipError_t launch_dim(const AttnParams& a, hipStream_t s) {
 namespace {
 // Rows a K/V head (query rows times heads of the group) from which the tile kernel takes over.
 constexpr int64_t kTileFrom = 64;
-constexpr int64_t kMinChunk = 1024, kFill = 2048, kFillTile = 512;
-// Splits that fill the card several times over.
-int64_t wanted_splits(const AttnParams& a) {
-    const int64_t base = (int64_t)a.q.seqs * a.c.heads * a.tiles, fill = a.tile_rows > 16 ? kFillTile : kFill;
-    return (fill + base - 1) / base;
-}
+constexpr int64_t kMinChunk = 256;
 void set_tiles(AttnParams& a, int xt) {
     const int64_t rows = (int64_t)a.q.max_new * a.group;
     a.tile_rows = rows >= kTileFrom ? attn8_tile_rows(xt, a.c.dim) : 16;
     a.tiles = (int)((rows + a.tile_rows - 1) / a.tile_rows);
+}
+// Splits that fill the card (a CU holds 2 or 3 workgroups of the rows kernel, or one of the larger ones),
+// and of the longest sequence always a few, so that sequences of different lengths even out.
+int64_t wanted_splits(const AttnParams& a, int xt) {
+    const int64_t base = (int64_t)a.q.seqs * a.c.heads * a.tiles;
+    if (a.tile_rows > 16) return base < 256 ? 256 / base : 1;
+    const bool one = rows_waves(xt == XT_F32 ? 2 : 1, a.c.dim) == 1;
+    const int64_t fill = one ? 256 : 1024, least = one ? 3 : 6;
+    return std::max((fill + base - 1) / base, least);
 }
 }  // namespace
 
@@ -347,7 +433,7 @@ int attn8_max_splits(AttnParams a) {
     int64_t want = 1;
     for (int xt : {XT_F32, XT_F16}) {
         set_tiles(a, xt);
-        const int64_t w = wanted_splits(a);
+        const int64_t w = wanted_splits(a, xt);
         if (w > want) want = w;
     }
     return (int)(most < want ? most : want);
@@ -360,10 +446,11 @@ void attn8_plan(AttnParams& a, int xt) {
     int64_t span = a.q.max_kv;
     const int64_t seen = (int64_t)a.window + a.tile_rows / a.group + 65;
     if (a.causal && a.window > 0 && seen < span) span = seen;
-    const int64_t want = wanted_splits(a);
+    const int64_t want = wanted_splits(a, xt);
     int64_t chunk = (span + want - 1) / want;
+    const int64_t unit = a.tile_rows > 16 ? 64 : 256;
     if (chunk < kMinChunk) chunk = kMinChunk;
-    a.chunk = (int)((chunk + 255) / 256 * 256);
+    a.chunk = (int)((chunk + unit - 1) / unit * unit);
     a.splits = (int)((span + a.chunk - 1) / a.chunk);
     if (a.splits < 1) a.splits = 1;
 }

@@ -16,9 +16,11 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNegInf = -__builtin_inff();
-// A weight enters the second product as f16: p * vs * 2^(kBase - ev), where 2^ev >= the V scales so
-// far.  The running maximum may lag by kLag (in powers of two) before the sums are rescaled, so values
-// stay at or below 2^15 and keep f16's full precision down to 2^-23 of the row's largest.
+// A weight enters the second product as f16 with the block's V scale in it:
+//   w = exp2(s + log2(vs 2^-e0) - m + kBase),  m a running maximum of what stands before it in the row,
+// and the denominator takes w times the reciprocal, so a row's precision is set by the blocks that it sees
+// and by no others.  m may lag by kLag before the sums are rescaled: weights stay at or below 2^15 and keep
+// f16's full precision down to 2^-23 of the row's largest.  e0 only keeps the powers in f32's range.
 constexpr float kLag = 6.f;
 constexpr int kBase = 9;
 
@@ -39,6 +41,37 @@ __device__ __forceinline__ half8_t codes8_f16(uint32_t w0, uint32_t w1) {
     codes4_f16(w1, a, b);
     r[2] = a, r[3] = b;
     return __builtin_bit_cast(half8_t, r);
+}
+
+// Four codes times f (0, 1 or -1; c = -1152 f) as f16.
+__device__ __forceinline__ void codes4_f16(uint32_t w, half2_t f, half2_t c, uint32_t& lo, uint32_t& hi) {
+    const uint32_t u = w ^ 0x80808080u;
+    const half2_t a = __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u));
+    const half2_t b = __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u));
+    lo = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(a, f, c));
+    hi = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(b, f, c));
+}
+__device__ __forceinline__ half8_t codes8_f16(uint32_t w0, uint32_t w1, half2_t f, half2_t c) {
+    u32x4 r;
+    uint32_t a, b;
+    codes4_f16(w0, f, c, a, b);
+    r[0] = a, r[1] = b;
+    codes4_f16(w1, f, c, a, b);
+    r[2] = a, r[3] = b;
+    return __builtin_bit_cast(half8_t, r);
+}
+// The factor of a block's V codes: the V scale's sign.
+__device__ __forceinline__ uint32_t v_sign(float vs) { return vs == 0.f ? 0u : vs < 0.f ? 0xbc00bc00u : 0x3c003c00u; }
+// log2(|vs| 2^-e0), 0 where the scale is 0 (its codes count as 0) or not finite (its K scale becomes NaN).
+__device__ __forceinline__ float v_power(float vs, int e0) {
+    const float va = fabsf(vs);
+    if (va == 0.f || !(va < __builtin_inff())) return 0.f;
+    return fminf(fmaxf(__builtin_amdgcn_logf(ldexpf(va, -e0)), -100.f), 100.f);
+}
+// Exponent of |vs|, -1000 where it is 0 or not finite.
+__device__ __forceinline__ int v_exponent(float vs) {
+    const float va = fabsf(vs);
+    return va > 0.f && va < __builtin_inff() ? (int)(__float_as_uint(va) >> 23) - 126 : -1000;
 }
 
 // What the rows r0 .. r0 + rows - 1 of a tile see together, and how the splits divide it.

@@ -6,6 +6,11 @@
 namespace qg {
 namespace {
 
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+
+constexpr int kInfo = 256;  // blocks looked up at a time
+
 // All lanes' LDS reads and writes so far are done, in every wavefront; loads from memory stay in flight.
 __device__ __forceinline__ void lds_barrier() {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
@@ -13,17 +18,20 @@ __device__ __forceinline__ void lds_barrier() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-__device__ __forceinline__ float lane_value(float v, int l) {
-    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), l));
+// Keeps a value's computation where it stands.
+__device__ __forceinline__ half2_t stay(half2_t v) {
+    asm volatile("" : "+v"(v));
+    return v;
 }
 
-// Four codes times f (0, 1 or -1; c = -1152 f) as f16.
-__device__ __forceinline__ void codes4_f16(uint32_t w, half2_t f, half2_t c, uint32_t& lo, uint32_t& hi) {
-    const uint32_t u = w ^ 0x80808080u;
-    const half2_t a = __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u));
-    const half2_t b = __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u));
-    lo = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(a, f, c));
-    hi = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(b, f, c));
+__device__ __forceinline__ float stay(float v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
 }
 
 // A workgroup of NW wavefronts takes 32 CT NW rows (query rows times the heads that share a K/V head,
@@ -40,7 +48,13 @@ __global__ __launch_bounds__(64 * NW) void attn8_tile_kernel(AttnParams a) {
     constexpr int NK = D / 16, NT = D / 32;
     constexpr int UN = (D / 16 + NW - 1) / NW;  // 1 KiB pieces of K, and of V, that a wavefront decodes
     constexpr int BR = 32 * CT * NW;
-    __shared__ __attribute__((aligned(16))) uint4 sk[2][8 * D], sv[2][8 * D];
+    constexpr int KB = D > 192 ? 2 : 3;         // stages of K in shared memory
+    constexpr bool kEven = NK % NW == 0;
+    __shared__ __attribute__((aligned(16))) uint4 sk[KB * 8 * D], sv[2][8 * D];
+    __shared__ __attribute__((aligned(16))) int in_bi[2 * kInfo];
+    __shared__ __attribute__((aligned(16))) float in_ks[2 * kInfo], in_lv[2 * kInfo], in_rv[2 * kInfo];
+    __shared__ uint32_t in_sg[2 * kInfo];
+    __shared__ int in_top[NW];
 
     const int lane = threadIdx.x & 63, col = lane & 31, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -64,6 +78,28 @@ __global__ __launch_bounds__(64 * NW) void attn8_tile_kernel(AttnParams a) {
     const int lo_all = kv8_sight(sp, min(w0 + 32 * CT, rows) <= w0 ? 0 : (min(w0 + 32 * CT, rows) - 1) / a.group, a.causal, a.window).lo;
     const int hi_all = kv8_sight(sp, min(w0, rows - 1) / a.group, a.causal, a.window).hi;
     const int lo_any = kv8_sight(sp, tile * BR / a.group, a.causal, a.window).lo;
+
+    // What the kernel has to know of each block, looked up by a thread each for 64 stages at a time: its
+    // index (-1: hidden from all), the K scale, and the V scale relative to 2^e0 as a power of two, its
+    // reciprocal and its sign.  A NaN or infinite V scale becomes a K scale of NaN: rows that see the
+    // block are NaN, others whole.
+    const int tid = threadIdx.x;
+    auto page_of = [&](int blk) {
+        const uint32_t pi = kv8_div((uint32_t)blk, a.c.nb, a.c.magic);
+        return a.q.table[(int64_t)s * a.q.width + min(pi, (uint32_t)a.q.width - 1)];
+    };
+    auto index_of = [&](int blk, int page) {
+        const uint32_t pi = kv8_div((uint32_t)blk, a.c.nb, a.c.magic);
+        const bool ok = (16 * blk < t1) & (16 * blk + 16 > lo_any) & (pi < (uint32_t)a.q.width) &
+                        ((uint32_t)page < (uint32_t)a.c.pages);
+        return ok ? (int)(((uint32_t)page * a.c.heads + h) * a.c.nb + ((uint32_t)blk - pi * (uint32_t)a.c.nb)) : -1;
+    };
+    const int my_blk = (t0 >> 4) + tid;  // plus kInfo a segment
+    // the first stages' codes set out before anything waits for their scales
+    int page0 = 0, first[KB + 1];
+    if (tid < kInfo) page0 = page_of(my_blk);
+#pragma unroll
+    for (int i = 0; i <= KB; i++) first[i] = page_of((t0 >> 4) + 4 * i + (lane >> 4));
 
     half8_t qf[CT][NP][NK];
     float qs[CT];
@@ -99,273 +135,346 @@ __global__ __launch_bounds__(64 * NW) void attn8_tile_kernel(AttnParams a) {
         qs[c] = fabsf(qs[c]);
     }
 
-    // the table's entry of this lane's block of a stage, and the block's index (-1: hidden from all)
-    auto blk_of = [&](int st) { return ((t0 + 64 * st) >> 4) + (lane >> 4); };
-    auto entry = [&](int st) {
-        const uint32_t pi = kv8_div((uint32_t)blk_of(st), a.c.nb, a.c.magic);
-        return a.q.table[(int64_t)s * a.q.width + min(pi, (uint32_t)a.q.width - 1)];
+    int bi0 = -1, e0 = 0, eb = -1000;
+    float ks0 = 0.f, vs0 = 0.f;
+    if (tid < kInfo) {
+        bi0 = index_of(my_blk, page0);
+        ks0 = a.c.ks[max(bi0, 0)];
+        vs0 = a.c.vs[max(bi0, 0)];
+    }
+#pragma unroll
+    for (int i = 0; i <= KB; i++) first[i] = index_of((t0 >> 4) + 4 * i + (lane >> 4), first[i]);
+    auto note = [&](int seg, int bi, float ks, float vs) {
+        const int x = (kInfo * seg + tid) & (2 * kInfo - 1);
+        const float lv = v_power(vs, e0);
+        in_bi[x] = bi;
+        in_ks[x] = bi < 0 ? -1.f : vs - vs == 0.f ? ks : __builtin_nanf("");
+        in_lv[x] = lv;
+        in_rv[x] = __builtin_amdgcn_exp2f(-lv);
+        in_sg[x] = v_sign(vs);
     };
-    auto index = [&](int st, int page) {
-        const int blk = blk_of(st);
-        const uint32_t pi = kv8_div((uint32_t)blk, a.c.nb, a.c.magic);
-        const bool ok = (st < stages) & (16 * blk < tr.hi) & (16 * blk + 16 > lo_any) & (pi < (uint32_t)a.q.width) &
-                        ((uint32_t)page < (uint32_t)a.c.pages);
-        return ok ? (int)(((uint32_t)page * a.c.heads + h) * a.c.nb + ((uint32_t)blk - pi * (uint32_t)a.c.nb)) : -1;
-    };
+
+    auto block_k = [&](int st) { return max(in_bi[(4 * st + (lane >> 4)) & (2 * kInfo - 1)], 0); };
     auto load_k = [&](int bi, uint4 (&raw)[UN]) {
-        const int8_t* p = a.c.kc + (int64_t)max(bi, 0) * (16 * D) + (lane & 15) * 16;
+        const int8_t* p = a.c.kc + (int64_t)bi * (16 * D) + (lane & 15) * 16;
 #pragma unroll
         for (int i = 0; i < UN; i++)
-            if (NK % NW == 0 || wave + NW * i < NK) raw[i] = *(const uint4*)(p + (wave + NW * i) * 256);
+            if (kEven || wave + NW * i < NK) raw[i] = *(const uint4*)(p + (wave + NW * i) * 256);
     };
-    auto store_k = [&](const uint4 (&raw)[UN], uint4* to) {
-#pragma unroll
-        for (int i = 0; i < UN; i++)
-            if (NK % NW == 0 || wave + NW * i < NK) {
-                uint4* p = to + (wave + NW * i) * 128 + lane;
-                p[0] = __builtin_bit_cast(uint4, codes8_f16(raw[i].x, raw[i].y));
-                p[64] = __builtin_bit_cast(uint4, codes8_f16(raw[i].z, raw[i].w));
-            }
+    // half x % 2 of piece x / 2, of K or V
+    auto store_k = [&](int x, const uint4 (&raw)[UN], uint4* to) {
+        const int i = x >> 1;
+        if (kEven || wave + NW * i < NK)
+            to[(wave + NW * i) * 128 + 64 * (x & 1) + lane] =
+                __builtin_bit_cast(uint4, x & 1 ? codes8_f16(raw[i].z, raw[i].w) : codes8_f16(raw[i].x, raw[i].y));
     };
     // V piece u: the 64 (block, dim) pairs from 64 u
     auto piece_v = [&](int i) { return NW - 1 - wave + NW * i; };
-    auto load_v = [&](int bi, uint4 (&raw)[UN]) {
+    auto place_v = [&](int i, int& j, int& d) {
+        const int x = 64 * piece_v(i) + lane;
+        j = x / D;
+        d = x - j * D;
+    };
+    auto load_v = [&](int st, uint4 (&raw)[UN]) {
 #pragma unroll
         for (int i = 0; i < UN; i++)
-            if (NK % NW == 0 || piece_v(i) < NK) {
-                const int x = 64 * piece_v(i) + lane, j = x / D;
-                const int vb = D % 64 == 0 ? __builtin_amdgcn_readlane(bi, 16 * (64 * piece_v(i) / D)) : __shfl(bi, 16 * j);
-                raw[i] = *(const uint4*)(a.c.vc + (int64_t)max(vb, 0) * (16 * D) + (x - j * D) * 16);
+            if (kEven || piece_v(i) < NK) {
+                int j, d;
+                place_v(i, j, d);
+                const int bi = in_bi[(4 * st + j) & (2 * kInfo - 1)];
+                raw[i] = *(const uint4*)(a.c.vc + (int64_t)max(bi, 0) * (16 * D) + d * 16);
             }
     };
-    auto store_v = [&](const uint4 (&raw)[UN], float vs, uint4* to) {
+    auto sign_v = [&](int st, half2_t (&sign)[UN]) {
 #pragma unroll
         for (int i = 0; i < UN; i++)
-            if (NK % NW == 0 || piece_v(i) < NK) {
-                const int x = 64 * piece_v(i) + lane, j = x / D, d = x - j * D;
-                const float sc = D % 64 == 0 ? lane_value(vs, 16 * (64 * piece_v(i) / D)) : __shfl(vs, 16 * j);
-                const float sg = sc == 0.f ? 0.f : sc < 0.f ? -1.f : 1.f;
-                const half2_t f = {(_Float16)sg, (_Float16)sg}, c = {(_Float16)(-1152.f * sg), (_Float16)(-1152.f * sg)};
-                u32x4 lo, hi;
-                uint32_t p, q;
-                codes4_f16(raw[i].x, f, c, p, q);
-                lo[0] = p, lo[1] = q;
-                codes4_f16(raw[i].z, f, c, p, q);
-                lo[2] = p, lo[3] = q;
-                codes4_f16(raw[i].y, f, c, p, q);
-                hi[0] = p, hi[1] = q;
-                codes4_f16(raw[i].w, f, c, p, q);
-                hi[2] = p, hi[3] = q;
-                to[2 * j * D + d] = __builtin_bit_cast(uint4, lo);
-                to[2 * j * D + D + d] = __builtin_bit_cast(uint4, hi);
+            if (kEven || piece_v(i) < NK) {
+                int j, d;
+                place_v(i, j, d);
+                sign[i] = __builtin_bit_cast(half2_t, in_sg[(4 * st + j) & (2 * kInfo - 1)]);
             }
+    };
+    auto store_v = [&](int x, const uint4 (&raw)[UN], const half2_t (&sign)[UN], uint4* to) {
+        const int i = x >> 1;
+        if (kEven || piece_v(i) < NK) {
+            int j, d;
+            place_v(i, j, d);
+            const half2_t f = sign[i], c = f * (half2_t){(_Float16)-1152.f, (_Float16)-1152.f};
+            u32x4 w;
+            uint32_t p, q;
+            codes4_f16(x & 1 ? raw[i].y : raw[i].x, f, c, p, q);
+            w[0] = p, w[1] = q;
+            codes4_f16(x & 1 ? raw[i].w : raw[i].z, f, c, p, q);
+            w[2] = p, w[3] = q;
+            to[2 * j * D + (x & 1) * D + d] = __builtin_bit_cast(uint4, w);
+        }
     };
 
+    // A weight is exp2(score + V scale's power - m + kBase), m the running maximum of what comes before
+    // it: it has the V scale in it, and its sum for the denominator is taken times the reciprocal.
     f32x16_t o[CT][NT] = {};
-    float m[CT], l[CT];
+    float m[CT], l[CT], limit[CT], mu[CT];  // mu: kBase - m
 #pragma unroll
-    for (int c = 0; c < CT; c++) m[c] = kNegInf, l[c] = 0.f;
-    int ev = -1000;           // exponent that the V scales are taken relative to
-    float kf[CT][4], cf[CT][4], rv[4];  // factor and addend of a score in powers of two, 1 / V scale
+    for (int c = 0; c < CT; c++) m[c] = limit[c] = kNegInf, l[c] = 0.f, mu[c] = (float)kBase;
+    float kf[CT][4], cf[CT][4];  // factor and addend of a score
 
-    auto scores = [&](const uint4* k, f32x16_t (&s)[CT][2]) {
+    // Stage st's scales; where a row does not see all of it, or a scale is negative, NaN or infinite, the
+    // scores are scaled and hidden one by one.
+    f32x4_t kb, lv, rv, rn;
+    auto read_scales = [&](int st) {
+        const int x = (4 * st) & (2 * kInfo - 1);
+        kb = *(const f32x4_t*)&in_ks[x];
+        lv = *(const f32x4_t*)&in_lv[x];
+        rn = *(const f32x4_t*)&in_rv[x];
+    };
+    auto scale_and_hide = [&](int st, f32x16_t (&sc)[CT][2]) {
+        const int tb = t0 + 64 * st, x = (4 * st) & (2 * kInfo - 1);
+        uint32_t odd = 0;
+#pragma unroll
+        for (int q = 0; q < 4; q++) odd = max(odd, __float_as_uint(kb[q]));
 #pragma unroll
         for (int c = 0; c < CT; c++)
 #pragma unroll
-            for (int t = 0; t < 2; t++)
-#pragma unroll
-                for (int e = 0; e < 16; e++) s[c][t][e] = 0.f;
-#pragma unroll
-        for (int i = 0; i < NK; i++)
-#pragma unroll
-            for (int t = 0; t < 2; t++) {
-                const half8_t kk = __builtin_bit_cast(half8_t, k[(2 * i + g) * 64 + 32 * t + col]);
-#pragma unroll
-                for (int c = 0; c < CT; c++)
-#pragma unroll
-                    for (int n = 0; n < NP; n++)
-                        s[c][t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kk, qf[c][n][i], s[c][t], 0, 0, 0);
-            }
-    };
-    // Stage st's maxima; the sums are rescaled where a maximum or the V scales' exponent grew.
-    auto maxima = [&](int st, int bi, float ks, float vs, f32x16_t (&sc)[CT][2]) {
-        const int tb = t0 + 64 * st;
-        // what a row sees of a block with a NaN or infinite V scale is NaN
-        if (bi < 0) vs = 0.f;
-        const bool odd = !(fabsf(vs) < __builtin_inff());
-        if (odd) ks = __builtin_nanf("");
-        const uint64_t there = __ballot(bi >= 0);
-        const bool whole = tb >= lo_all && tb + 64 <= hi_all && !__any(bi < 0 || !(ks >= 0.f));
-        const float va = odd ? 0.f : fabsf(vs);
-        float kb[4];
-#pragma unroll
-        for (int q = 0; q < 4; q++) kb[q] = lane_value(ks, 16 * q);
-        float top[CT];
-        if (whole) {
+            for (int q = 0; q < 4; q++) kf[c][q] = kb[q] * qs[c];
+        if ((tb < lo_all) | (tb + 64 > hi_all) | (__builtin_amdgcn_readfirstlane((int)(odd >> 23)) >= 255)) {
+            const i32x4_t bi = *(const i32x4_t*)&in_bi[x];
 #pragma unroll
             for (int c = 0; c < CT; c++) {
-                float best = kNegInf;
-#pragma unroll
-                for (int q = 0; q < 4; q++) {
-                    kf[c][q] = kb[q] * qs[c];
-                    float t = sc[c][q >> 1][8 * (q & 1)];
-#pragma unroll
-                    for (int e = 1; e < 8; e++) t = fmaxf(t, sc[c][q >> 1][8 * (q & 1) + e]);
-                    best = fmaxf(best, t * kf[c][q]);
-                }
-                top[c] = best;
-            }
-        } else {
-#pragma unroll
-            for (int c = 0; c < CT; c++) {
-                float best = kNegInf;
                 const int jl = see[c].lo - tb - 4 * g, jh = see[c].hi - tb - 4 * g;
 #pragma unroll
                 for (int q = 0; q < 4; q++) {
-                    const float f = kb[q] * qs[c];
-                    const bool here = (there >> (16 * q)) & 1;
-                    kf[c][q] = 1.f;
 #pragma unroll
                     for (int e = 0; e < 8; e++) {
                         const int j = 16 * q + 8 * (e >> 2) + (e & 3);
-                        const float v = here && j >= jl && j < jh ? sc[c][q >> 1][8 * (q & 1) + e] * f : kNegInf;
-                        sc[c][q >> 1][8 * (q & 1) + e] = v;
-                        best = fmaxf(best, v);
+                        const bool on = (bi[q] >= 0) & (j >= jl) & (j < jh);
+                        sc[c][q >> 1][8 * (q & 1) + e] = on ? sc[c][q >> 1][8 * (q & 1) + e] * kf[c][q] : kNegInf;
                     }
+                    kf[c][q] = 1.f;
                 }
-                top[c] = best;
             }
         }
-        bool grew = false;
+    };
+    float top[CT], part[CT];
+    auto top_pair = [&](int x, const f32x16_t (&sc)[CT][2]) {  // scores 2x, 2x + 1 of the 32 of a column
+        const int q = x >> 2;
 #pragma unroll
         for (int c = 0; c < CT; c++) {
-            top[c] = fmaxf(top[c], __shfl_xor(top[c], 32));
-            grew |= top[c] > m[c] + kLag;
+            const float u = sc[c][x >> 3][2 * x & 15], v = sc[c][x >> 3][(2 * x & 15) + 1];
+            part[c] = x & 3 ? max3(part[c], u, v) : max3(u, v, v);
+            if ((x & 3) == 3) {
+                const float t = fmaf(part[c], kf[c][q], lv[q]);
+                top[c] = q ? fmaxf(top[c], t) : t;
+            }
         }
-        float vm = va;
-        vm = fmaxf(vm, __shfl_xor(vm, 16));
-        vm = fmaxf(vm, __shfl_xor(vm, 32));
-        const int eb = __builtin_amdgcn_readfirstlane((int)(__float_as_uint(vm) >> 23)) - 126;
-        if (eb > ev || __any(grew)) {
-            const int en = max(ev, eb);
+    };
+    // The sums are rescaled where a maximum grew by more than kLag.
+    auto settle = [&]() {
+        bool grew = false;
+#pragma unroll
+        for (int c = 0; c < CT; c++) grew |= top[c] > limit[c];
+        if (__any(grew)) {
 #pragma unroll
             for (int c = 0; c < CT; c++) {
-                const float mn = fmaxf(m[c], top[c]);
+                const float mn = fmaxf(m[c], fmaxf(top[c], __shfl_xor(top[c], 32)));
                 const float f = m[c] == kNegInf ? 0.f : __builtin_amdgcn_exp2f(m[c] - mn);
                 l[c] *= f;
-                const float fo = ldexpf(f, ev - en);
 #pragma unroll
                 for (int i = 0; i < NT; i++)
 #pragma unroll
-                    for (int e = 0; e < 16; e++) o[c][i][e] *= fo;
+                    for (int e = 0; e < 16; e++) o[c][i][e] *= f;
                 m[c] = mn;
+                limit[c] = mn + kLag;
+                mu[c] = mn == kNegInf ? (float)kBase : (float)kBase - mn;
             }
-            ev = en;
         }
-        // the block's V scale relative to 2^(ev - kBase), as a power of two; 0: its codes count as 0
-        const float lv = va == 0.f ? 0.f : fmaxf(__builtin_amdgcn_logf(ldexpf(va, kBase - ev)), -60.f);
-        const float iv = __builtin_amdgcn_exp2f(-lv);
-#pragma unroll
-        for (int q = 0; q < 4; q++) {
-            const float lq = lane_value(lv, 16 * q);
-            rv[q] = lane_value(iv, 16 * q);
-#pragma unroll
-            for (int c = 0; c < CT; c++) cf[c][q] = lq - (m[c] == kNegInf ? 0.f : m[c]);
-        }
-    };
-    half8_t pf[CT][NP][4];
-    auto weights = [&](const f32x16_t (&sc)[CT][2]) {
+        rv = rn;
 #pragma unroll
         for (int c = 0; c < CT; c++)
 #pragma unroll
-            for (int q = 0; q < 4; q++) {
-                float sum = 0.f;
-#pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    float w[2];
-#pragma unroll
-                    for (int x = 0; x < 2; x++)
-                        w[x] = __builtin_amdgcn_exp2f(fmaf(sc[c][q >> 1][8 * (q & 1) + e + x], kf[c][q], cf[c][q]));
-                    sum += w[0] + w[1];
-                    const half2_t hi = __builtin_convertvector((__attribute__((ext_vector_type(2))) float){w[0], w[1]}, half2_t);
-                    pf[c][0][q][e] = hi[0];
-                    pf[c][0][q][e + 1] = hi[1];
-                    if constexpr (NP == 2) {
-                        pf[c][1][q][e] = (_Float16)(w[0] - (float)hi[0]);
-                        pf[c][1][q][e + 1] = (_Float16)(w[1] - (float)hi[1]);
-                    }
-                }
-                l[c] = fmaf(sum, rv[q], l[c]);
-            }
+            for (int q = 0; q < 4; q++) cf[c][q] = lv[q] + mu[c];
     };
-    auto values = [&](const uint4* v) {
+    // The weights of scores 2x, 2x + 1 in three steps that different pairs take at the same time, so that no
+    // instruction waits for the one before it.
+    half8_t pf[CT][NP][4];
+    float sum[CT], arg[CT][16][2], wt[CT][16][2];
+    auto weigh_1 = [&](int x, const f32x16_t (&sc)[CT][2]) {
+        const int q = x >> 2;
 #pragma unroll
-        for (int q = 0; q < 4; q++)
+        for (int c = 0; c < CT; c++)
 #pragma unroll
-            for (int i = 0; i < NT; i++) {
-                const half8_t vv = __builtin_bit_cast(half8_t, v[(2 * q + g) * D + 32 * i + col]);
+            for (int e = 0; e < 2; e++) arg[c][x][e] = stay(fmaf(sc[c][x >> 3][(2 * x & 15) + e], kf[c][q], cf[c][q]));
+    };
+    auto weigh_2 = [&](int x) {
 #pragma unroll
-                for (int c = 0; c < CT; c++)
+        for (int c = 0; c < CT; c++)
 #pragma unroll
-                    for (int n = 0; n < NP; n++)
-                        o[c][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vv, pf[c][n][q], o[c][i], 0, 0, 0);
+            for (int e = 0; e < 2; e++) wt[c][x][e] = stay(__builtin_amdgcn_exp2f(arg[c][x][e]));
+    };
+    auto weigh_3 = [&](int x) {
+        const int q = x >> 2, e = 2 * x & 7;
+#pragma unroll
+        for (int c = 0; c < CT; c++) {
+            const float u = wt[c][x][0], v = wt[c][x][1];
+            sum[c] = x & 3 ? sum[c] + u + v : u + v;
+            if ((x & 3) == 3) l[c] = stay(fmaf(sum[c], rv[q], l[c]));
+            const half2_t hi = stay(__builtin_convertvector((f32x2_t){u, v}, half2_t));
+            pf[c][0][q][e] = hi[0];
+            pf[c][0][q][e + 1] = hi[1];
+            if constexpr (NP == 2) {
+                const half2_t lo = stay(__builtin_convertvector((f32x2_t){u - (float)hi[0], v - (float)hi[1]}, half2_t));
+                pf[c][1][q][e] = lo[0];
+                pf[c][1][q][e + 1] = lo[1];
+            }
+        }
+    };
+    auto weigh = [&](int step, const f32x16_t (&sc)[CT][2], int steps) {
+#pragma unroll
+        for (int y = 0; y < 16; y++) {
+            if (y >= 16 * step / steps && y < 16 * (step + 1) / steps) weigh_1(y, sc);
+            if (y >= 16 * (step - 1) / steps && y < 16 * step / steps) weigh_2(y);
+            if (y >= 16 * (step - 2) / steps && y < 16 * (step - 1) / steps) weigh_3(y);
+        }
+    };
+
+    constexpr int P1 = 2 * NK, P2 = 4 * NT, kDeep = 4;  // operands of a stage's two products, read kDeep ahead
+    auto operand = [&](int x, const uint4* k, const uint4* v) {
+        const int y = x - P1;
+        return __builtin_bit_cast(half8_t, x < P1 ? k[(2 * (x >> 1) + g) * 64 + 32 * (x & 1) + col]
+                                                  : v[(2 * (y / NT) + g) * D + 32 * (y % NT) + col]);
+    };
+    auto score = [&](int x, half8_t k, f32x16_t (&sc)[CT][2]) {
+#pragma unroll
+        for (int c = 0; c < CT; c++)
+#pragma unroll
+            for (int n = 0; n < NP; n++) {
+                f32x16_t& to = sc[c][x & 1];
+                if (x < 2 && n == 0)
+                    to = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, qf[c][n][x >> 1], f32x16_t{}, 0, 0, 0);
+                else
+                    to = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, qf[c][n][x >> 1], to, 0, 0, 0);
             }
     };
 
-    // ids and scales of stages t + 1, t + 2, t + 3 (t: the loop's stage), the entry of stage t + 4
-    int b1, b2, b3, e4;
-    float k1, v1, k2, v2, k3, v3;
     uint4 rk[UN], rw[UN];
-    auto load_scales = [&](int bi, float& ks, float& vs) {
-        ks = a.c.ks[max(bi, 0)];
-        vs = a.c.vs[max(bi, 0)];
-    };
+    half2_t sign[UN];
     f32x16_t s0[CT][2], s1[CT][2];
     {
-        const int e0 = entry(0), e1 = entry(1), e2 = entry(2), e3 = entry(3);
-        const int b0 = index(0, e0);
-        float k0, v0;
-        load_scales(b0, k0, v0);
-        load_k(b0, rk);
-        load_v(b0, rw);
-        b1 = index(1, e1);
-        b2 = index(2, e2);
-        b3 = index(3, e3);
-        e4 = entry(4);
-        load_scales(b1, k1, v1);
-        load_scales(b2, k2, v2);
-        store_k(rk, sk[0]);
-        store_v(rw, v0, sv[0]);
-        load_k(b1, rk);
-        store_k(rk, sk[1]);
-        load_k(b2, rk);
-        load_v(b1, rw);
+        uint4 fk[KB][UN], fv[UN];
+#pragma unroll
+        for (int i = 0; i < KB; i++) load_k(max(first[i], 0), fk[i]);
+        load_k(max(first[KB], 0), rk);
+#pragma unroll
+        for (int i = 0; i < UN; i++)
+            if (kEven || piece_v(i) < NK) {
+                int j, d;
+                place_v(i, j, d);
+                fv[i] = *(const uint4*)(a.c.vc + (int64_t)max(__shfl(first[0], 16 * j), 0) * (16 * D) + d * 16);
+                rw[i] = *(const uint4*)(a.c.vc + (int64_t)max(__shfl(first[1], 16 * j), 0) * (16 * D) + d * 16);
+            }
+        if (bi0 >= 0) eb = v_exponent(vs0);
+#pragma unroll
+        for (int x = 1; x < 64; x <<= 1) eb = max(eb, __shfl_xor(eb, x));
+        if (lane == 0) in_top[wave] = eb;
         lds_barrier();
-        scores(sk[0], s0);
-        maxima(0, b0, k0, v0, s0);
+        eb = in_top[0];
+#pragma unroll
+        for (int w = 1; w < NW; w++) eb = max(eb, in_top[w]);
+        e0 = eb < -500 ? 0 : __builtin_amdgcn_readfirstlane(eb);
+        if (tid < kInfo) note(0, bi0, ks0, vs0);
+        lds_barrier();
+        sign_v(0, sign);
+#pragma unroll
+        for (int x = 0; x < 2 * UN; x++) {
+#pragma unroll
+            for (int i = 0; i < KB; i++) store_k(x, fk[i], sk + i * 8 * D);
+            store_v(x, fv, sign, sv[0]);
+        }
+        sign_v(1, sign);
+        lds_barrier();
     }
-    // Iteration t: S of stage t + 1 and the weights of stage t; then O of stage t, while stage t + 2's K
-    // and stage t + 1's V are decoded and the loads after those set out.
-    auto body = [&](int t, f32x16_t (&now)[CT][2], f32x16_t (&next)[CT][2], uint4* kn, uint4* ko, uint4* vo, uint4* vn) {
-        scores(kn, next);
-        weights(now);
-        values(vo);
-        store_k(rk, ko);
-        store_v(rw, v1, vn);
-        load_k(b3, rk);
-        load_v(b2, rw);
-        load_scales(b3, k3, v3);
-        if (t + 1 < stages) maxima(t + 1, b1, k1, v1, next);
-        b1 = b2, k1 = k2, v1 = v2;
-        b2 = b3, k2 = k3, v2 = v3;
-        b3 = index(t + 4, e4);
-        e4 = entry(t + 5);
+#pragma unroll
+    for (int x = 0; x < P1; x++) score(x, operand(x, sk, sv[0]), s0);
+    read_scales(0);
+    scale_and_hide(0, s0);
+#pragma unroll
+    for (int x = 0; x < 16; x++) top_pair(x, s0);
+    settle();
+    // Iteration t: S of stage t + 1 between the weights of stage t; then O of stage t between the maxima
+    // of stage t + 1 and the decoding of stage t + KB's K and stage t + 1's V, whose successors' loads set
+    // out as soon as their registers are free.  Stages past the last are hidden.
+    int page = 0, nbi = -1;
+    float nks = 0.f, nvs = 0.f;
+    half8_t f[kDeep];
+    if constexpr (KB == 3) {
+#pragma unroll
+        for (int x = 0; x < kDeep; x++) f[x] = operand(x, sk + 8 * D, sv[0]);
+    }
+    const uint4 *kr = sk + 8 * D, *kr2 = sk + (KB - 1) * 8 * D;  // K of stages t + 1 and (of three buffers) t + 2
+    uint4* kw = sk;
+    auto body = [&](int t, f32x16_t (&now)[CT][2], f32x16_t (&next)[CT][2], uint4* vr, uint4* vw) {
+        if constexpr (KB == 2) {
+#pragma unroll
+            for (int x = 0; x < kDeep; x++) f[x] = operand(x, kr, vr);
+        }
+        const int bk = block_k(t + KB + 1);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int x = 0; x < P1; x++) {
+            score(x, f[x % kDeep], next);
+            f[x % kDeep] = operand(x + kDeep, kr, vr);
+            if (x == P1 - 4) read_scales(t + 1);
+            weigh(x, now, P1);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        scale_and_hide(t + 1, next);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int x = 0; x < P2; x++) {
+#pragma unroll
+            for (int c = 0; c < CT; c++)
+#pragma unroll
+                for (int n = 0; n < NP; n++)
+                    o[c][x % NT] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[(P1 + x) % kDeep], pf[c][n][x / NT], o[c][x % NT], 0, 0, 0);
+            if (x + kDeep < P2)
+                f[(P1 + x) % kDeep] = operand(P1 + x + kDeep, kr, vr);
+            else if (KB == 3)
+                f[(P1 + x) % kDeep] = operand(x + kDeep - P2, kr2, vr);
+            if (x < 2) weigh(P1 + x, now, P1);
+#pragma unroll
+            for (int y = 8 * UN * x / P2; y < 8 * UN * (x + 1) / P2; y++) {
+                if (y < 2 * UN) store_k(y, rk, kw);
+                if (y == 2 * UN - 1) load_k(bk, rk);
+                if (y >= 2 * UN && y < 4 * UN) store_v(y - 2 * UN, rw, sign, vw);
+                if (y == 4 * UN - 1) {
+                    load_v(t + 2, rw);
+                    sign_v(t + 2, sign);
+                }
+            }
+#pragma unroll
+            for (int y = 16 * x / P2; y < 16 * (x + 1) / P2; y++) top_pair(y, next);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        settle();
+        uint4* k = kw;
+        kw = (uint4*)kr;
+        kr = KB == 3 ? kr2 : k;
+        kr2 = k;
         lds_barrier();
     };
     for (int t = 0; t < stages; t += 2) {
-        body(t, s0, s1, sk[1], sk[0], sv[0], sv[1]);
-        if (t + 1 >= stages) break;
-        body(t + 1, s1, s0, sk[0], sk[1], sv[1], sv[0]);
+        body(t, s0, s1, sv[0], sv[1]);
+        body(t + 1, s1, s0, sv[1], sv[0]);
+        // the next 64 stages' blocks, in three steps so that no load is waited for
+        const int seg = t / 64 + 1, at = t & 63;
+        if (at >= 8 && at < 26 && seg * 64 < stages + 6 && tid < kInfo) {
+            if (at == 8) page = page_of(my_blk + kInfo * seg);
+            if (at == 16) {
+                nbi = index_of(my_blk + kInfo * seg, page);
+                nks = a.c.ks[max(nbi, 0)];
+                nvs = a.c.vs[max(nbi, 0)];
+            }
+            if (at == 24) note(seg, nbi, nks, nvs);
+        }
     }
 
 #pragma unroll
@@ -376,7 +485,7 @@ __global__ __launch_bounds__(64 * NW) void attn8_tile_kernel(AttnParams a) {
         const int64_t trow = sp.r0 + r / a.group;
         const int hd = h * a.group + r % a.group;
         if (tr.nact > 1) {
-            const float un = m[c] == kNegInf ? 0.f : ldexpf(1.f, ev - kBase);
+            const float un = ldexpf(1.f, e0);
             const int64_t pi = (trow * a.q_heads + hd) * a.splits + split;
             float* to = a.part_o + pi * D + 4 * g;
 #pragma unroll
@@ -395,7 +504,7 @@ __global__ __launch_bounds__(64 * NW) void attn8_tile_kernel(AttnParams a) {
                 for (int e = 0; e < 4; e++) {
                     float y[4];
 #pragma unroll
-                    for (int x = 0; x < 4; x++) y[x] = ldexpf(o[c][i][4 * e + x] * inv, ev - kBase);
+                    for (int x = 0; x < 4; x++) y[x] = ldexpf(o[c][i][4 * e + x] * inv, e0);
                     if constexpr (XT == XT_F32)
                         *(f32x4_t*)((float*)a.O + at + 32 * i + 8 * e) = f32x4_t{y[0], y[1], y[2], y[3]};
                     else {
