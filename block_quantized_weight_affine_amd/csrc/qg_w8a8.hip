@@ -51,27 +51,44 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
     return v;
 }
 
-// One workgroup codes one row of X: the maximum first, then the codes from a second read (the row is
-// in the cache by then).  K % 16 == 0.
+// One workgroup codes one row of X, held in registers up to K = 16384 (longer rows are read again for
+// their codes).  K % 16 == 0.
 template <int XT>
-__global__ __launch_bounds__(256) void x_code_kernel(const void* X, int K, int8_t* codes, float* scales) {
-    __shared__ uint32_t sh[4];
+__global__ __launch_bounds__(512) void x_code_kernel(const void* X, int K, int8_t* codes, float* scales) {
+    constexpr int kHeld = 4;
+    __shared__ uint32_t sh[8];
     const int64_t base = (int64_t)blockIdx.x * K;
+    float v[kHeld][8];
     uint32_t top = 0;
-    for (int k = 8 * threadIdx.x; k < K; k += 2048) {
-        float v[8];
-        x_load8<XT>(X, base + k, v);
-        top = max8(v, top);
+#pragma unroll
+    for (int i = 0; i < kHeld; i++) {
+        const int k = 8 * threadIdx.x + 4096 * i;
+        if (k < K) {
+            x_load8<XT>(X, base + k, v[i]);
+            top = max8(v[i], top);
+        }
+    }
+    for (int k = 8 * threadIdx.x + 4096 * kHeld; k < K; k += 4096) {
+        float x[8];
+        x_load8<XT>(X, base + k, x);
+        top = max8(x, top);
     }
     top = wave_max(top);
     if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = top;
     __syncthreads();
-    const float d = row_scale(max(max(sh[0], sh[1]), max(sh[2], sh[3]))), inv = inverse(d);
+#pragma unroll
+    for (int w = 0; w < 8; w++) top = max(top, sh[w]);
+    const float d = row_scale(top), inv = inverse(d);
     if (threadIdx.x == 0) scales[blockIdx.x] = d;
-    for (int k = 8 * threadIdx.x; k < K; k += 2048) {
-        float v[8];
-        x_load8<XT>(X, base + k, v);
-        *(uint2*)(codes + base + k) = code8x8(v, inv);
+#pragma unroll
+    for (int i = 0; i < kHeld; i++) {
+        const int k = 8 * threadIdx.x + 4096 * i;
+        if (k < K) *(uint2*)(codes + base + k) = code8x8(v[i], inv);
+    }
+    for (int k = 8 * threadIdx.x + 4096 * kHeld; k < K; k += 4096) {
+        float x[8];
+        x_load8<XT>(X, base + k, x);
+        *(uint2*)(codes + base + k) = code8x8(x, inv);
     }
 }
 
@@ -93,112 +110,149 @@ __device__ __forceinline__ void store_any(void* Y, int yt, int64_t i, float v) {
 
 // ---- few tokens: the weights stream once -----------------------------------------------------------
 // A workgroup of KS wavefronts takes 16 RN weight rows and all (at most 16 TT) tokens; the wavefronts
-// take 128-byte pieces of K in turn, four of them loaded ahead of their use, and their integer sums are
-// joined at the end.  A lane's 16 bytes of a weight row are its operand of the matrix instruction as
-// they come from memory.  FUSED (few tokens): every workgroup codes X itself into shared memory while
-// its first weights are on their way, which saves a launch.
-constexpr int kAhead = 4;           // pieces a batch
-constexpr int kFusedLds = 64 << 10; // bytes of X codes a workgroup keeps
+// take 128-byte pieces of K in turn and their integer sums are joined at the end.  A wavefront copies its
+// pieces of both operands straight into its own part of shared memory, AHEAD of them on their way, 8 rows
+// of whole 128-byte lines a copy: loads into registers in the operands' layout (16 rows of 64 bytes) are
+// bound by the lines that a load touches.  A row's 16-byte chunks lie at slot chunk ^ (row % 8), so that
+// reads meet all banks.  CODES > 0 (at most 8 tokens): every workgroup codes X itself into CODES bytes of
+// shared memory while its first weights are on their way, which saves a launch.
+constexpr int kFusedLds = 64 << 10, kFusedSmall = 16 << 10;  // bytes of X codes a workgroup keeps
 
 __host__ __device__ __forceinline__ int fused_pitch(int K) { return (K + 127) / 128 * 128 + 16; }
 
-template <int XT>
-__device__ __forceinline__ void code_rows_lds(const void* X, int K, int T, int threads, int8_t* xs, float* dx,
-                                              uint32_t (*part)[16]) {
-    const int tid = threadIdx.x, pitch = fused_pitch(K);
-    for (int t = 0; t < T; t++) {
+// The KS wavefronts share the rows out evenly (one row: all on it); a wavefront's part of a row stays in
+// registers up to 4096 values.
+template <int XT, int KS>
+__device__ __forceinline__ void code_rows_lds(const void* X, int K, int T, int8_t* xs, float* dx, uint32_t* part) {
+    constexpr int kHeld = 8;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), pitch = fused_pitch(K);
+    const int split = T <= 1 ? KS : T <= 2 ? KS / 2 : T <= 4 ? KS / 4 : KS >= 8 ? KS / 8 : 1;  // wavefronts a row
+    const int rows = KS / split;                                                              // rows at a time
+    for (int t0 = 0; t0 < T; t0 += rows) {
+        const int t = t0 + wave / split, sub = wave % split;
+        const int64_t base = (int64_t)min(t, T - 1) * K;
+        const int k0 = 8 * (64 * sub + lane), step = 512 * split;
+        float v[kHeld][8];
         uint32_t top = 0;
-        for (int k = 8 * tid; k < K; k += 8 * threads) {
-            float v[8];
-            x_load8<XT>(X, (int64_t)t * K + k, v);
-            top = max8(v, top);
+#pragma unroll
+        for (int i = 0; i < kHeld; i++) {
+            if (512 * sub + step * i >= K) break;
+            const int k = k0 + step * i;
+#pragma unroll
+            for (int e = 0; e < 8; e++) v[i][e] = 0.f;
+            if (k < K) x_load8<XT>(X, base + k, v[i]);
+            top = max8(v[i], top);
+        }
+        for (int k = k0 + step * kHeld; k < K; k += step) {
+            float x[8];
+            x_load8<XT>(X, base + k, x);
+            top = max8(x, top);
         }
         top = wave_max(top);
-        if ((tid & 63) == 0) part[t][tid >> 6] = top;
-    }
-    __syncthreads();
-    for (int t = 0; t < T; t++) {
-        uint32_t top = 0;
-        for (int w = 0; w < threads >> 6; w++) top = max(top, part[t][w]);
+        if (lane == 0) part[wave] = top;
+        __syncthreads();
+        for (int w = 0; w < split; w++) top = max(top, part[wave / split * split + w]);
         const float d = row_scale(top), inv = inverse(d);
-        if (tid == 0) dx[t] = d;
-        for (int k = 8 * tid; k < pitch - 16; k += 8 * threads) {
-            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (k < K) x_load8<XT>(X, (int64_t)t * K + k, v);
-            *(uint2*)(xs + t * pitch + k) = code8x8(v, inv);
+        if (t < T) {
+            if (lane == 0 && sub == 0) dx[t] = d;
+#pragma unroll
+            for (int i = 0; i < kHeld; i++) {
+                if (512 * sub + step * i >= K) break;
+                const int k = k0 + step * i;
+                if (k < pitch - 16) *(uint2*)(xs + t * pitch + k) = code8x8(v[i], inv);
+            }
+            for (int k = k0 + step * kHeld; k < pitch - 16; k += step) {
+                float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                if (k < K) x_load8<XT>(X, base + k, x);
+                *(uint2*)(xs + t * pitch + k) = code8x8(x, inv);
+            }
         }
+        __syncthreads();
     }
-    __syncthreads();
 }
 
-template <int TT, int RN, int KS, bool FUSED>
+template <int TT, int RN, int KS, int AHEAD, int CODES>
 __global__ __launch_bounds__(64 * KS) void w8a8_rows_kernel(W8A8Params p) {
-    constexpr int RP = 16 * RN + 4;  // pitch of the sums
+    constexpr bool FUSED = CODES > 0;
+    constexpr int RP = 16 * RN + 4;                    // pitch of the sums
+    constexpr int kPiece = (RN + (FUSED ? 0 : TT)) * 2048, kRing = KS * kPiece;
+    static_assert(AHEAD == 1 || AHEAD == 2, "ring");
     constexpr int kRed = KS * 16 * TT * RP * 4;
-    constexpr int kLds = FUSED && kFusedLds > kRed ? kFusedLds : kRed;
-    __shared__ __attribute__((aligned(16))) int8_t lds[kLds];
+    // one array a place in the ring, so that a read of one never waits for copies into another
+    __shared__ __attribute__((aligned(16))) int8_t s0[kRing > kRed ? kRing : kRed];
+    __shared__ __attribute__((aligned(16))) int8_t s1[AHEAD > 1 ? kRing : 16];
+    __shared__ __attribute__((aligned(16))) int8_t codes[FUSED ? CODES : 16];
     __shared__ float dx[16];
-    __shared__ uint32_t part[16][16];
+    __shared__ uint32_t part[KS];
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n0 = blockIdx.x * 16 * RN, K = p.K;
-    const int8_t* w[RN];
-#pragma unroll
-    for (int i = 0; i < RN; i++) w[i] = p.w + (int64_t)min(n0 + 16 * i + r, p.N - 1) * K;
-
     const int units = (K + 127) / 128, pitch = fused_pitch(K);
-    auto load_w = [&](int u0, i32x4_t (&b)[kAhead][2][RN]) {
+    const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc((void*)(p.w + (int64_t)n0 * K), 0,
+                                                                        min(16 * RN, p.N - n0) * K, 0x00020000);
+    const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc((void*)p.xq, 0, FUSED ? 0 : p.T * K, 0x00020000);
+    const int chunk = 16 * ((lane & 7) ^ (lane >> 3)), from = (lane >> 3) * K + chunk;
+    auto copy = [&](int8_t* s, int u) {
+        const int at = 128 * u + chunk < K ? from + 128 * u : 0x40000000;
+        int8_t* to = s + wave * kPiece;
 #pragma unroll
-        for (int a = 0; a < kAhead; a++)
+        for (int i = 0; i < 2 * RN; i++) buffer_copy16_lds(wr, to + i * 1024, at + 8 * i * K);
+        if constexpr (!FUSED) {
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
-                const int k = 128 * (u0 + KS * a) + 64 * h + 16 * g;
-#pragma unroll
-                for (int i = 0; i < RN; i++) b[a][h][i] = __builtin_nontemporal_load((const i32x4_t*)(w[i] + (k < K ? k : 0)));
-            }
+            for (int i = 0; i < 2 * TT; i++) buffer_copy16_lds(xr, to + (2 * RN + i) * 1024, at + 8 * i * K);
+        }
     };
-    i32x4_t acc[RN][TT] = {}, cur[kAhead][2][RN];
-    load_w(wave, cur);
+    i32x4_t acc[RN][TT] = {};
+    auto multiply = [&](const int8_t* s, int u) {
+        const int8_t* at = s + wave * kPiece + r * 128;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const int slot = 16 * ((4 * h + g) ^ (lane & 7));
+            i32x4_t w[RN], x[TT];
+#pragma unroll
+            for (int i = 0; i < RN; i++) w[i] = *(const i32x4_t*)(at + i * 2048 + slot);
+#pragma unroll
+            for (int t = 0; t < TT; t++) {
+                if constexpr (FUSED)
+                    x[t] = *(const i32x4_t*)(codes + min(16 * t + r, p.T - 1) * pitch + (u < units ? 128 * u + 64 * h + 16 * g : 0));
+                else
+                    x[t] = *(const i32x4_t*)(at + (RN + t) * 2048 + slot);
+            }
+#pragma unroll
+            for (int t = 0; t < TT; t++)
+#pragma unroll
+                for (int i = 0; i < RN; i++) acc[i][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[i], x[t], acc[i][t], 0, 0, 0);
+        }
+    };
+    copy(s0, wave);
+    if constexpr (AHEAD > 1) copy(s1, wave + KS);
     if constexpr (FUSED) {
         if (p.xt == XT_F32)
-            code_rows_lds<XT_F32>(p.X, K, p.T, 64 * KS, lds, dx, part);
+            code_rows_lds<XT_F32, KS>(p.X, K, p.T, codes, dx, part);
         else if (p.xt == XT_F16)
-            code_rows_lds<XT_F16>(p.X, K, p.T, 64 * KS, lds, dx, part);
+            code_rows_lds<XT_F16, KS>(p.X, K, p.T, codes, dx, part);
         else
-            code_rows_lds<XT_BF16>(p.X, K, p.T, 64 * KS, lds, dx, part);
+            code_rows_lds<XT_BF16, KS>(p.X, K, p.T, codes, dx, part);
     }
-    for (int u0 = wave; u0 < units; u0 += KS * kAhead) {
-        i32x4_t next[kAhead][2][RN];
-        if (u0 + KS * kAhead < units) load_w(u0 + KS * kAhead, next);
-#pragma unroll
-        for (int a = 0; a < kAhead; a++) {
-            if (u0 + KS * a >= units) break;
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-                const int k = 128 * (u0 + KS * a) + 64 * h + 16 * g;
-#pragma unroll
-                for (int t = 0; t < TT; t++) {
-                    const int row = min(16 * t + r, p.T - 1);  // columns past T are never stored
-                    i32x4_t x = {0, 0, 0, 0};
-                    if constexpr (FUSED)
-                        x = *(const i32x4_t*)(lds + row * pitch + k);
-                    else if (k < K)
-                        x = *(const i32x4_t*)(p.xq + (int64_t)row * K + k);
-#pragma unroll
-                    for (int i = 0; i < RN; i++)
-                        acc[i][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(cur[a][h][i], x, acc[i][t], 0, 0, 0);
-                }
-            }
-        }
-#pragma unroll
-        for (int a = 0; a < kAhead; a++)
-#pragma unroll
-            for (int h = 0; h < 2; h++)
-#pragma unroll
-                for (int i = 0; i < RN; i++) cur[a][h][i] = next[a][h][i];
+    // a wavefront keeps to its own pieces, so nothing is waited for but its own copies; a place is copied
+    // to again only when what was read from it has arrived
+    constexpr int kYounger = (AHEAD - 1) * 2 * (RN + (FUSED ? 0 : TT));  // copies after the piece's own
+    static_assert(kYounger < 64, "ring");
+    auto turn = [&](int8_t* s, int u) {
+        __builtin_amdgcn_s_waitcnt(0x0f70 | (kYounger & 15) | (kYounger >> 4) << 14);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(s, u);
+        __builtin_amdgcn_s_waitcnt(0xc07f);
+        __builtin_amdgcn_sched_barrier(0);
+        copy(s, u + KS * AHEAD);
+    };
+    for (int u0 = wave; u0 < units; u0 += KS * AHEAD) {
+        turn(s0, u0);
+        if constexpr (AHEAD > 1) turn(s1, u0 + KS);
     }
-    if constexpr (FUSED) __syncthreads();  // X's codes make room for the sums
-    int* red = (int*)lds;
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // the last copies have landed before their place is used again
+    __syncthreads();
+    int* red = (int*)s0;
 #pragma unroll
     for (int i = 0; i < RN; i++)
 #pragma unroll
@@ -360,16 +414,42 @@ __global__ __launch_bounds__(64 * WT * WN) void w8a8_tile_kernel(W8A8Params p, i
 constexpr int kRowsMax = 128;  // tokens of the streaming kernel
 bool fused(int K, int T) { return T <= 8 && T * fused_pitch(K) <= kFusedLds; }
 
-template <int TT, int RN, int KS>
-void launch_rows(const W8A8Params& p, bool fuse, hipStream_t s) {
-    const uint32_t grid = (p.N + 16 * RN - 1) / (16 * RN);
-    if constexpr (TT == 1) {
-        if (fuse) {
-            w8a8_rows_kernel<TT, RN, KS, true><<<grid, 64 * KS, 0, s>>>(p);
-            return;
-        }
+template <int TT, int RN, int KS, int CODES>
+void launch_rows(const W8A8Params& p, hipStream_t s) {
+    constexpr int kRing = KS * (RN + (CODES ? 0 : TT)) * 2048, kRed = KS * 16 * TT * (16 * RN + 4) * 4;
+    constexpr int AHEAD = (kRed > kRing ? kRed : kRing) + kRing + CODES + 2048 <= 160 << 10 ? 2 : 1;
+    w8a8_rows_kernel<TT, RN, KS, AHEAD, CODES><<<(uint32_t)((p.N + 16 * RN - 1) / (16 * RN)), 64 * KS, 0, s>>>(p);
+}
+
+// Weight rows a workgroup: the fullest CU reads (16 RN + 16 TT) rows for each workgroup that it gets, and
+// that bounds the kernel (45 tokens, 11009 x 4112: RN 1, 2, 3, 4: 28.8, 26.1, 21.5, 23.2 us).
+int rows_of(int N, int TT) {
+    int best = 1;
+    int64_t least = 0;
+    for (int rn = 1; rn <= 4; rn++) {
+        const int64_t groups = (N + 16 * rn - 1) / (16 * rn), cost = (groups + 255) / 256 * (rn + TT);
+        if (rn == 1 || cost < least) best = rn, least = cost;
     }
-    w8a8_rows_kernel<TT, RN, KS, false><<<grid, 64 * KS, 0, s>>>(p);
+    return best;
+}
+
+template <int TT, int KS>
+void launch_few(const W8A8Params& p, hipStream_t s) {
+    switch (rows_of(p.N, TT)) {
+        case 1: return launch_rows<TT, 1, KS, 0>(p, s);
+        case 2: return launch_rows<TT, 2, KS, 0>(p, s);
+        case 3: return launch_rows<TT, 3, KS, 0>(p, s);
+        default: return launch_rows<TT, 4, KS, 0>(p, s);
+    }
+}
+
+// One launch: X's codes in the least shared memory that holds them, so that CUs hold several workgroups.
+template <int KS>
+void launch_fused(const W8A8Params& p, hipStream_t s) {
+    if (p.T * fused_pitch(p.K) <= kFusedSmall)
+        launch_rows<1, 1, KS, kFusedSmall>(p, s);
+    else
+        launch_rows<1, 1, KS, kFusedLds>(p, s);
 }
 
 template <int MT, int NT, int WT, int WN>
@@ -392,22 +472,26 @@ hipError_t launch_w8a8(W8A8Params p, void* ws, hipStream_t s) {
         p.xq = xq;
         p.xs = xs;
         if (p.xt == XT_F32)
-            x_code_kernel<XT_F32><<<p.T, 256, 0, s>>>(p.X, p.K, xq, xs);
+            x_code_kernel<XT_F32><<<p.T, 512, 0, s>>>(p.X, p.K, xq, xs);
         else if (p.xt == XT_F16)
-            x_code_kernel<XT_F16><<<p.T, 256, 0, s>>>(p.X, p.K, xq, xs);
+            x_code_kernel<XT_F16><<<p.T, 512, 0, s>>>(p.X, p.K, xq, xs);
         else
-            x_code_kernel<XT_BF16><<<p.T, 256, 0, s>>>(p.X, p.K, xq, xs);
+            x_code_kernel<XT_BF16><<<p.T, 512, 0, s>>>(p.X, p.K, xq, xs);
     }
-    if (p.T <= 16)
-        launch_rows<1, 1, 8>(p, fuse, s);
+    if (fuse)
+        p.N <= 8192 ? launch_fused<16>(p, s) : launch_fused<4>(p, s);
+    else if (p.T <= 16)
+        launch_few<1, 8>(p, s);
     else if (p.T <= 32)
-        launch_rows<2, 1, 8>(p, false, s);
+        launch_few<2, 4>(p, s);
     else if (p.T <= 48)
-        launch_rows<3, 2, 4>(p, false, s);
+        launch_few<3, 4>(p, s);
     else if (p.T <= 64)
-        launch_rows<4, 2, 4>(p, false, s);
+        launch_few<4, 4>(p, s);
+    else if (p.T <= 96)
+        launch_few<6, 4>(p, s);
     else if (p.T <= kRowsMax)
-        launch_rows<8, 2, 4>(p, false, s);
+        launch_few<8, 4>(p, s);
     else if ((int64_t)((p.T + 255) / 256) * ((p.N + 255) / 256) >= 192)
         launch_tile<2, 4, 4, 2>(p, s);
     else
