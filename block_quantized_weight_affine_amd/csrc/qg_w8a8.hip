@@ -113,8 +113,8 @@ __device__ __forceinline__ void store_any(void* Y, int yt, int64_t i, float v) {
 // take 128-byte pieces of K in turn and their integer sums are joined at the end.  A wavefront copies its
 // pieces of both operands straight into its own part of shared memory, AHEAD of them on their way, 8 rows
 // of whole 128-byte lines a copy: loads into registers in the operands' layout (16 rows of 64 bytes) are
-// bound by the lines that a load touches.  A row's 16-byte chunks lie at slot chunk ^ (row % 8), so that
-// reads meet all banks.  CODES > 0 (at most 8 tokens): every workgroup codes X itself into CODES bytes of
+// bound by the lines that a load touches.  A row's 16-byte chunks lie at slot chunk ^ (row / 2 % 8), so
+// that reads meet all banks.  CODES > 0 (at most 8 tokens): every workgroup codes X itself into CODES bytes of
 // shared memory while its first weights are on their way, which saves a launch.
 constexpr int kFusedLds = 64 << 10, kFusedSmall = 16 << 10;  // bytes of X codes a workgroup keeps
 
@@ -191,15 +191,17 @@ __global__ __launch_bounds__(64 * KS) void w8a8_rows_kernel(W8A8Params p) {
     const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc((void*)(p.w + (int64_t)n0 * K), 0,
                                                                         min(16 * RN, p.N - n0) * K, 0x00020000);
     const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc((void*)p.xq, 0, FUSED ? 0 : p.T * K, 0x00020000);
-    const int chunk = 16 * ((lane & 7) ^ (lane >> 3)), from = (lane >> 3) * K + chunk;
+    // copy i has rows 8 i .. 8 i + 7
+    const int even = 16 * ((lane & 7) ^ (lane >> 4)), odd = even ^ 64, from = (lane >> 3) * K;
     auto copy = [&](int8_t* s, int u) {
-        const int at = 128 * u + chunk < K ? from + 128 * u : 0x40000000;
+        const int at[2] = {128 * u + even < K ? from + even + 128 * u : 0x40000000,
+                           128 * u + odd < K ? from + odd + 128 * u : 0x40000000};
         int8_t* to = s + wave * kPiece;
 #pragma unroll
-        for (int i = 0; i < 2 * RN; i++) buffer_copy16_lds(wr, to + i * 1024, at + 8 * i * K);
+        for (int i = 0; i < 2 * RN; i++) buffer_copy16_lds(wr, to + i * 1024, at[i & 1] + 8 * i * K);
         if constexpr (!FUSED) {
 #pragma unroll
-            for (int i = 0; i < 2 * TT; i++) buffer_copy16_lds(xr, to + (2 * RN + i) * 1024, at + 8 * i * K);
+            for (int i = 0; i < 2 * TT; i++) buffer_copy16_lds(xr, to + (2 * RN + i) * 1024, at[i & 1] + 8 * i * K);
         }
     };
     i32x4_t acc[RN][TT] = {};
@@ -207,7 +209,7 @@ __global__ __launch_bounds__(64 * KS) void w8a8_rows_kernel(W8A8Params p) {
         const int8_t* at = s + wave * kPiece + r * 128;
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-            const int slot = 16 * ((4 * h + g) ^ (lane & 7));
+            const int slot = 16 * ((4 * h + g) ^ (lane >> 1 & 7));
             i32x4_t w[RN], x[TT];
 #pragma unroll
             for (int i = 0; i < RN; i++) w[i] = *(const i32x4_t*)(at + i * 2048 + slot);
@@ -273,7 +275,10 @@ __global__ __launch_bounds__(64 * KS) void w8a8_rows_kernel(W8A8Params p) {
 // ---- many tokens: tiles ----------------------------------------------------------------------------
 // A workgroup takes BT tokens x BN weight rows; both operands pass through shared memory in stages of
 // 128 k, copied straight from memory while the previous stage is multiplied.  A row's 16-byte chunks
-// lie at slot chunk ^ (row % 8), so the 8 lanes of a read phase meet 8 different bank groups.
+// lie at slot chunk ^ (row / 2 % 8): the 16 lanes that are read at a time meet all 64 banks (with
+// chunk ^ (row % 8) every bank met two of them: 22 % of the kernel's cycles).  The one barrier of a stage
+// stands before its last products: by then every wavefront holds their operands, so the stage's place is
+// free for the copies of the stage after next, and the next stage's first operands are read during them.
 template <int N>
 struct Frags {
     i32x4_t f[N];
@@ -303,7 +308,7 @@ __global__ __launch_bounds__(64 * WT * WN) void w8a8_tile_kernel(W8A8Params p, i
                                                                         min(BT, p.T - t0) * K, 0x00020000);
     const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc((void*)(p.w + (int64_t)n0 * K), 0,
                                                                         min(BN, p.N - n0) * K, 0x00020000);
-    const int chunk = (lane & 7) ^ (lane >> 3);  // of the row, for this lane's slot
+    const int chunk = (lane & 7) ^ ((lane >> 4) + 4 * (wave & 1));  // of the row, for this lane's slot
     const int voff = (8 * wave + (lane >> 3)) * K + 16 * chunk;
     auto copy = [&](int st, int8_t* s) {
         const int k = 128 * st + 16 * chunk < K ? voff + 128 * st : 0x40000000;  // past K: zeros
@@ -315,45 +320,52 @@ __global__ __launch_bounds__(64 * WT * WN) void w8a8_tile_kernel(W8A8Params p, i
     i32x16_t acc[NT][MT] = {};
     const int xrow = (32 * MT * wt + r) * 128, wrow = (BT + 32 * NT * wn + r) * 128;
     auto frags = [&](const int8_t* s, int j, Frags<MT>& x, Frags<NT>& w) {
-        const int slot = 16 * ((2 * j + g) ^ (lane & 7));
+        const int slot = 16 * ((2 * j + g) ^ (lane >> 1 & 7));
 #pragma unroll
         for (int i = 0; i < MT; i++) x.f[i] = *(const i32x4_t*)(s + xrow + i * 4096 + slot);
 #pragma unroll
         for (int i = 0; i < NT; i++) w.f[i] = *(const i32x4_t*)(s + wrow + i * 4096 + slot);
     };
-    auto multiply = [&](const int8_t* s) {
-        Frags<MT> x[2];
-        Frags<NT> w[2];
-        frags(s, 0, x[0], w[0]);
+    Frags<MT> x[2];
+    Frags<NT> w[2];
+    auto multiply = [&](int j) {
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-            if (j < 3) frags(s, j + 1, x[(j + 1) & 1], w[(j + 1) & 1]);
+        for (int a = 0; a < NT; a++)
 #pragma unroll
-            for (int a = 0; a < NT; a++)
+            for (int b = 0; b < MT; b++)
+                acc[a][b] = __builtin_amdgcn_mfma_i32_32x32x32_i8(w[j].f[a], x[j].f[b], acc[a][b], 0, 0, 0);
+        // the next step's reads go between this step's products, and no further ahead
 #pragma unroll
-                for (int b = 0; b < MT; b++)
-                    acc[a][b] = __builtin_amdgcn_mfma_i32_32x32x32_i8(w[j & 1].f[a], x[j & 1].f[b], acc[a][b], 0, 0, 0);
-            // the next step's reads go between this step's products, and no further ahead
-            if (j < 3) {
-#pragma unroll
-                for (int i = 0; i < MT + NT; i++) {
-                    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                }
-            }
-            __builtin_amdgcn_sched_barrier(0);
+        for (int i = 0; i < MT + NT; i++) {
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
         }
+        __builtin_amdgcn_sched_barrier(0);
     };
-    // stages in pairs (two arrays, so that a read of one never waits for the copies into the other); past
-    // the last stage the copies are zeros
+    auto stage = [&](int st, int8_t* s, const int8_t* next) {
+#pragma unroll
+        for (int j = 0; j < 3; j++) {
+            frags(s, j + 1, x[(j + 1) & 1], w[(j + 1) & 1]);
+            multiply(j & 1);
+        }
+        __builtin_amdgcn_s_waitcnt(0x0070);  // own copies have landed, own reads have arrived
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        copy(st + 2, s);
+        __builtin_amdgcn_sched_barrier(0);
+        frags(next, 0, x[0], w[0]);
+        multiply(1);
+    };
+    // two arrays, so that a read of one never waits for the copies into the other; past the last stage the
+    // copies are zeros
     copy(0, s0);
+    copy(1, s1);
+    __syncthreads();
+    frags(s0, 0, x[0], w[0]);
+    __builtin_amdgcn_sched_barrier(0);
     for (int st = 0; st < stages; st += 2) {
-        __syncthreads();
-        copy(st + 1, s1);
-        multiply(s0);
-        __syncthreads();
-        copy(st + 2, s0);
-        multiply(s1);
+        stage(st, s0, s1);
+        stage(st + 1, s1, s0);
     }
     __builtin_amdgcn_s_waitcnt(0x0f70);  // the last copy has landed before its place is used again
     __syncthreads();
