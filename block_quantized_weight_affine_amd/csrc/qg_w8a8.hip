@@ -274,7 +274,7 @@ __global__ __launch_bounds__(64 * KS) void w8a8_rows_kernel(W8A8Params p) {
 
 // ---- many tokens: tiles ----------------------------------------------------------------------------
 // A workgroup takes BT tokens x BN weight rows; both operands pass through shared memory in stages of
-// 128 k, copied straight from memory while the previous stage is multiplied.  A row's 16-byte chunks
+// 128 k, copied straight from memory while the R - 1 stages before are multiplied.  A row's 16-byte chunks
 // lie at slot chunk ^ (row / 2 % 8): the 16 lanes that are read at a time meet all 64 banks (with
 // chunk ^ (row % 8) every bank met two of them: 22 % of the kernel's cycles).  The one barrier of a stage
 // stands before its last products: by then every wavefront holds their operands, so the stage's place is
@@ -284,13 +284,15 @@ struct Frags {
     i32x4_t f[N];
 };
 
-template <int MT, int NT, int WT, int WN>
+template <int MT, int NT, int WT, int WN, int R>
 __global__ __launch_bounds__(64 * WT * WN) void w8a8_tile_kernel(W8A8Params p, int tiles_t, int tiles_n) {
     constexpr int BT = 32 * MT * WT, BN = 32 * NT * WN, NW = WT * WN;
     constexpr int XC = BT / 8 / NW, WC = BN / 8 / NW;  // copies of 8 rows a wavefront and stage
     static_assert(XC * 8 * NW == BT && WC * 8 * NW == BN && NT % 2 == 0 && NW * 8192 <= (BT + BN) * 128, "tile");
     __shared__ __attribute__((aligned(16))) int8_t s0[(BT + BN) * 128];
     __shared__ __attribute__((aligned(16))) int8_t s1[(BT + BN) * 128];
+    __shared__ __attribute__((aligned(16))) int8_t s2[R > 2 ? (BT + BN) * 128 : 16];
+    __shared__ __attribute__((aligned(16))) int8_t s3[R > 2 ? (BT + BN) * 128 : 16];
     const int lane = threadIdx.x & 63, r = lane & 31, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wt = wave % WT, wn = wave / WT;
@@ -342,16 +344,19 @@ __global__ __launch_bounds__(64 * WT * WN) void w8a8_tile_kernel(W8A8Params p, i
         }
         __builtin_amdgcn_sched_barrier(0);
     };
+    constexpr int kYounger = (R - 2) * (XC + WC);  // copies of later stages than the next
+    static_assert((R == 2 || R == 4) && kYounger < 64, "ring");
     auto stage = [&](int st, int8_t* s, const int8_t* next) {
 #pragma unroll
         for (int j = 0; j < 3; j++) {
             frags(s, j + 1, x[(j + 1) & 1], w[(j + 1) & 1]);
             multiply(j & 1);
         }
-        __builtin_amdgcn_s_waitcnt(0x0070);  // own copies have landed, own reads have arrived
+        // own copies of the next stage have landed, own reads have arrived
+        __builtin_amdgcn_s_waitcnt(0x0070 | (kYounger & 15) | (kYounger >> 4) << 14);
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
-        copy(st + 2, s);
+        copy(st + R, s);
         __builtin_amdgcn_sched_barrier(0);
         frags(next, 0, x[0], w[0]);
         multiply(1);
@@ -360,12 +365,21 @@ __global__ __launch_bounds__(64 * WT * WN) void w8a8_tile_kernel(W8A8Params p, i
     // copies are zeros
     copy(0, s0);
     copy(1, s1);
+    if constexpr (R > 2) {
+        copy(2, s2);
+        copy(3, s3);
+    }
     __syncthreads();
     frags(s0, 0, x[0], w[0]);
     __builtin_amdgcn_sched_barrier(0);
-    for (int st = 0; st < stages; st += 2) {
+    for (int st = 0; st < stages; st += R) {
         stage(st, s0, s1);
-        stage(st + 1, s1, s0);
+        stage(st + 1, s1, R > 2 ? s2 : s0);
+        if constexpr (R > 2) {
+            if (st + 2 >= stages) break;
+            stage(st + 2, s2, s3);
+            stage(st + 3, s3, s0);
+        }
     }
     __builtin_amdgcn_s_waitcnt(0x0f70);  // the last copy has landed before its place is used again
     __syncthreads();
@@ -464,10 +478,10 @@ void launch_fused(const W8A8Params& p, hipStream_t s) {
         launch_rows<1, 1, KS, kFusedLds>(p, s);
 }
 
-template <int MT, int NT, int WT, int WN>
+template <int MT, int NT, int WT, int WN, int R>
 void launch_tile(const W8A8Params& p, hipStream_t s) {
     const int tt = (p.T + 32 * MT * WT - 1) / (32 * MT * WT), tn = (p.N + 32 * NT * WN - 1) / (32 * NT * WN);
-    w8a8_tile_kernel<MT, NT, WT, WN><<<(uint32_t)(tt * tn), 64 * WT * WN, 0, s>>>(p, tt, tn);
+    w8a8_tile_kernel<MT, NT, WT, WN, R><<<(uint32_t)(tt * tn), 64 * WT * WN, 0, s>>>(p, tt, tn);
 }
 
 }  // namespace
@@ -505,9 +519,11 @@ hipError_t launch_w8a8(W8A8Params p, void* ws, hipStream_t s) {
     else if (p.T <= kRowsMax)
         launch_few<8, 4>(p, s);
     else if ((int64_t)((p.T + 255) / 256) * ((p.N + 255) / 256) >= 192)
-        launch_tile<2, 4, 4, 2>(p, s);
+        launch_tile<2, 4, 4, 2, 2>(p, s);
+    else if ((int64_t)((p.T + 127) / 128) * ((p.N + 127) / 128) > 160)
+        launch_tile<2, 2, 2, 2, 4>(p, s);
     else
-        launch_tile<2, 2, 2, 2>(p, s);
+        launch_tile<1, 2, 2, 1, 4>(p, s);
     return hipGetLastError();
 }
 
