@@ -414,14 +414,20 @@ constexpr int64_t kTileFrom = 64;
 constexpr int64_t kMinChunk = 256;
 void set_tiles(AttnParams& a, int xt) {
     const int64_t rows = (int64_t)a.q.max_new * a.group;
-    a.tile_rows = rows >= kTileFrom ? attn8_tile_rows(xt, a.c.dim) : 16;
+    a.tile_rows = rows >= kTileFrom ? attn8_tile_rows(a, xt) : 16;
     a.tiles = (int)((rows + a.tile_rows - 1) / a.tile_rows);
 }
-// Splits that fill the card (a CU holds 2 or 3 workgroups of the rows kernel, or one of the larger ones),
-// and of the longest sequence always a few, so that sequences of different lengths even out.
-int64_t wanted_splits(const AttnParams& a, int xt) {
+// Splits of `span` tokens.  Rows kernel: enough to fill the card (a CU holds 2 or 3 of its workgroups, or
+// one of the larger ones), and of the longest sequence always a few, so that sequences of different lengths
+// even out.  Tile kernel: a stage of 64 tokens takes about 24 times as long as a tile's part in writing
+// and joining the sums of one more split, so at most sqrt(24 stages / workgroups); none once the card is full.
+int64_t wanted_splits(const AttnParams& a, int xt, int64_t span) {
     const int64_t base = (int64_t)a.q.seqs * a.c.heads * a.tiles;
-    if (a.tile_rows > 16) return base < 256 ? 256 / base : 1;
+    if (a.tile_rows > 16) {
+        int64_t k = 1;
+        while ((k + 1) * base <= 256 && (k + 1) * (k + 1) * base <= 24 * (span / 64)) k++;
+        return k;
+    }
     const bool one = rows_waves(xt == XT_F32 ? 2 : 1, a.c.dim) == 1;
     const int64_t fill = one ? 256 : 1024, least = one ? 3 : 6;
     return std::max((fill + base - 1) / base, least);
@@ -433,7 +439,7 @@ int attn8_max_splits(AttnParams a) {
     int64_t want = 1;
     for (int xt : {XT_F32, XT_F16}) {
         set_tiles(a, xt);
-        const int64_t w = wanted_splits(a, xt);
+        const int64_t w = wanted_splits(a, xt, a.q.max_kv);
         if (w > want) want = w;
     }
     return (int)(most < want ? most : want);
@@ -446,7 +452,7 @@ void attn8_plan(AttnParams& a, int xt) {
     int64_t span = a.q.max_kv;
     const int64_t seen = (int64_t)a.window + a.tile_rows / a.group + 65;
     if (a.causal && a.window > 0 && seen < span) span = seen;
-    const int64_t want = wanted_splits(a, xt);
+    const int64_t want = wanted_splits(a, xt, span);
     int64_t chunk = (span + want - 1) / want;
     const int64_t unit = a.tile_rows > 16 ? 64 : 256;
     if (chunk < kMinChunk) chunk = kMinChunk;

@@ -93,8 +93,8 @@ __device__ __forceinline__ int q_exponent(uint32_t top) {
     return eb == 0 || eb == 255 ? 0 : 141 - eb;
 }
 
-// The kernel of tiles of 32 .. 256 rows (qg_attn8_tile.hip), and its rows a workgroup for a type and dim.
-int attn8_tile_rows(int xt, int dim);
+// The kernel of tiles of 128 or 256 rows (qg_attn8_tile.hip), and which of them a call takes.
+int attn8_tile_rows(const AttnParams& a, int xt);
 hipError_t launch_attn8_tile(const AttnParams& a, int xt, hipStream_t s);
 
 }  // namespace qg

@@ -43,12 +43,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // which is the order in which lane (row l % 32, half g = l / 32) holds its weights after S, so they
 // never move between lanes.  Stage t + 1's S is multiplied while stage t's weights are computed.
 template <int XT, int D, int NW, int CT>
-__global__ __launch_bounds__(64 * NW) void attn8_tile_kernel(AttnParams a) {
+__global__ __launch_bounds__(64 * NW, NW == 4 && XT != XT_F32 && D <= 128 ? 2 : 1) void attn8_tile_kernel(AttnParams a) {
     constexpr int NP = XT == XT_F32 ? 2 : 1;  // f16 pieces of a q value and of a weight
     constexpr int NK = D / 16, NT = D / 32;
     constexpr int UN = (D / 16 + NW - 1) / NW;  // 1 KiB pieces of K, and of V, that a wavefront decodes
     constexpr int BR = 32 * CT * NW;
-    constexpr int KB = D > 192 ? 2 : 3;         // stages of K in shared memory
+    constexpr int KB = D > 192 || (D == 128 && NW == 4) ? 2 : 3;  // stages of K in shared memory
     constexpr bool kEven = NK % NW == 0;
     __shared__ __attribute__((aligned(16))) uint4 sk[KB * 8 * D], sv[2][8 * D];
     __shared__ __attribute__((aligned(16))) int in_bi[2 * kInfo];
@@ -518,17 +518,16 @@ __global__ __launch_bounds__(64 * NW) void attn8_tile_kernel(AttnParams a) {
     }
 }
 
-// Rows a wavefront (32 CT) and wavefronts for a type and dim.
-template <int XT, int D>
-struct Shape {
-    static constexpr int NW = XT == XT_F32 || D > 128 ? 4 : 8, CT = 1;
-};
-
 template <int XT, int D>
 hipError_t launch_one(const AttnParams& a, hipStream_t s) {
-    using S = Shape<XT, D>;
-    const int64_t grid = (int64_t)a.q.seqs * a.splits * a.c.heads * a.tiles;
-    attn8_tile_kernel<XT, D, S::NW, S::CT><<<dim3((uint32_t)grid), 64 * S::NW, 0, s>>>(a);
+    const uint32_t grid = (uint32_t)((int64_t)a.q.seqs * a.splits * a.c.heads * a.tiles);
+    if constexpr (XT != XT_F32 && D <= 128) {
+        if (a.tile_rows == 256) {
+            attn8_tile_kernel<XT, D, 8, 1><<<grid, 512, 0, s>>>(a);
+            return hipGetLastError();
+        }
+    }
+    attn8_tile_kernel<XT, D, 4, 1><<<grid, 256, 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -546,8 +545,13 @@ hipError_t launch_dim(const AttnParams& a, hipStream_t s) {
 
 }  // namespace
 
-int attn8_tile_rows(int xt, int dim) {
-    return xt == XT_F32 || dim > 128 ? 128 : 256;
+// 256 rows share a stage's decoding where their sums fit the registers and such tiles are enough for all
+// CUs; with fewer, tiles of 128 rows, of which a CU takes two (5 chunks of 129 to 384 rows, 6 heads of 64 a
+// group, window 1024: 34.7 and 32.2 us; 2 x 4096 prompt tokens, 32 heads of 128: 325 and 415 us).
+int attn8_tile_rows(const AttnParams& a, int xt) {
+    if (xt == XT_F32 || a.c.dim > 128) return 128;
+    const int64_t tiles = ((int64_t)a.q.max_new * a.group + 255) / 256;
+    return a.q.seqs * tiles * a.c.heads < 256 ? 128 : 256;
 }
 
 hipError_t launch_attn8_tile(const AttnParams& a, int xt, hipStream_t s) {
