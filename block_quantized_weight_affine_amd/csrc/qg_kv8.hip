@@ -15,18 +15,42 @@ namespace {
 constexpr float kPer127 = 1.0f / 127.0f;
 constexpr int kWaves = 4;
 
-// Two adjacent elements.
+// Four adjacent elements.
 template <int XT>
-__device__ __forceinline__ void load2(const void* x, int64_t i, float& a, float& b) {
+__device__ __forceinline__ void load4(const void* x, int64_t i, float (&v)[4]) {
     if constexpr (XT == XT_F32) {
-        const float2 t = *(const float2*)((const float*)x + i);
-        a = t.x;
-        b = t.y;
+        const float4 t = *(const float4*)((const float*)x + i);
+        v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
     } else {
-        const uint32_t t = *(const uint32_t*)((const uint16_t*)x + i);
-        a = XT == XT_F16 ? f16_to_f32((uint16_t)t) : bf16_to_f32((uint16_t)t);
-        b = XT == XT_F16 ? f16_to_f32((uint16_t)(t >> 16)) : bf16_to_f32((uint16_t)(t >> 16));
+        const uint2 t = *(const uint2*)((const uint16_t*)x + i);
+        const uint32_t w[2] = {t.x, t.y};
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            const uint16_t u = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+            v[e] = XT == XT_F16 ? f16_to_f32(u) : bf16_to_f32(u);
+        }
     }
+}
+
+// How a wavefront shares a V block out: a lane takes four dims of TOK tokens.
+template <int D>
+struct VShare {
+    static constexpr int groups = D / 4, parts = groups <= 16 ? 4 : groups <= 32 ? 2 : 1, TOK = 16 / parts;
+};
+// TOK codes of a dim, as the cache holds them.
+template <int TOK>
+__device__ __forceinline__ void load_run(const int8_t* p, uint32_t (&w)[TOK / 4]) {
+#pragma unroll
+    for (int i = 0; i < TOK / 4; i++) w[i] = ((const uint32_t*)p)[i];
+}
+template <int TOK>
+__device__ __forceinline__ void store_run(int8_t* p, const uint32_t (&w)[TOK / 4]) {
+    if constexpr (TOK == 16)
+        *(uint4*)p = make_uint4(w[0], w[1], w[2], w[3]);
+    else if constexpr (TOK == 8)
+        *(uint2*)p = make_uint2(w[0], w[1]);
+    else
+        *(uint32_t*)p = w[0];
 }
 
 // |x| as bits: an unsigned maximum of these carries a NaN through to the scale.
@@ -64,67 +88,91 @@ __device__ __forceinline__ Coding coding(uint32_t amax_bits, float d_old, bool b
     return c;
 }
 
+// Where a wavefront's block lies: the block of the item-th that the sequence's rows touch.
+struct Item {
+    int h, blk, j0, j1;  // tokens j0 .. j1 - 1 of the block are the sequence's rows
+    bool is_v, none;
+    int64_t row;         // row of the block's token 0
+};
+__device__ __forceinline__ Item kv8_item(const KvCache& c, const KvSpan& sp, int item) {
+    Item t;
+    t.h = item % c.heads;
+    item /= c.heads;
+    t.is_v = item & 1;
+    const int p0 = sp.len - sp.n;  // first new position
+    t.blk = (p0 >> 4) + (item >> 1);
+    t.none = sp.n == 0 || 16 * t.blk >= sp.len;
+    t.j0 = p0 > 16 * t.blk ? p0 - 16 * t.blk : 0;
+    t.j1 = sp.len - 16 * t.blk < 16 ? sp.len - 16 * t.blk : 16;
+    t.row = (int64_t)sp.r0 + 16 * t.blk - p0;
+    return t;
+}
+
 // One wavefront codes one block of one head, K or V.  It holds the block in registers (16 dim values),
 // so the new tokens are read once and nothing goes through shared memory:
 //   K  a lane takes 16 dims of a token (16 codes = the 16 bytes that lie together in the cache);
-//   V  a lane takes two dims of all 16 tokens (two 16-byte runs of the cache).
-// Bound by memory traffic for prompts and by latency for single tokens.
+//   V  a lane takes four dims of 4, 8 or 16 tokens (a run of the cache for each dim).
+// The rows are read before the table's answer is there, the earlier scale and codes together: bound by
+// memory traffic for prompts and by three loads' latency for single tokens.
 template <int XT, int D>
 __global__ __launch_bounds__(64 * kWaves) void kv8_write_kernel(KvCache c, KvSeqs q, const void* k, const void* v,
                                                                 KvStrides st) {
-    const int lane = threadIdx.x & 63;
-    int item = blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int s = blockIdx.y;
-    const KvSpan sp = kv8_span(q, s);
-    const int h = item % c.heads;
-    item /= c.heads;
-    const bool is_v = item & 1;
-    const int p0 = sp.len - sp.n;                    // first new position
-    const int blk = (p0 >> 4) + (item >> 1);
-    if (sp.n == 0 || 16 * blk >= sp.len) return;
-    const int bi = kv8_block(c, q, s, h, blk);
-    if (bi < 0) return;
-    const int j0 = p0 > 16 * blk ? p0 - 16 * blk : 0;                      // new tokens of the block: j0 .. j1 - 1
-    const int j1 = sp.len - 16 * blk < 16 ? sp.len - 16 * blk : 16;
-    const bool begun = j0 > 0;
-    const int64_t row = (int64_t)sp.r0 + 16 * blk - p0;                    // row of the block's token 0
-    float* scale = (is_v ? c.vs : c.ks) + bi;
-    const float d_old = begun ? *scale : 0.f;
-    int8_t* out = (is_v ? c.vc : c.kc) + (int64_t)bi * (16 * D);
-    if (!is_v) {
+    const int lane = threadIdx.x & 63, s = blockIdx.y;
+    const Item t = kv8_item(c, kv8_span(q, s), blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
+    if (t.none) return;
+    const bool begun = t.j0 > 0;
+    if (!t.is_v) {
         constexpr int CH = D / 16, NI = (D + 63) / 64;
         float x[NI][16];
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < NI; i++) {
             const int it = lane + 64 * i, tok = it / CH, ch = it % CH;
-            if (it < D && tok >= j0 && tok < j1) {
-                const int64_t at = (row + tok) * st.k_row + h * st.k_head + 16 * ch;
+            if (it < D && tok >= t.j0 && tok < t.j1) {
+                const int64_t at = (t.row + tok) * st.k_row + t.h * st.k_head + 16 * ch;
                 float a[8], b[8];
                 x_load8<XT>(k, at, a);
                 x_load8<XT>(k, at + 8, b);
 #pragma unroll
                 for (int e = 0; e < 8; e++) x[i][e] = a[e], x[i][8 + e] = b[e];
+            }
+        }
+        const int bi = kv8_block(c, q, s, t.h, t.blk);
+        if (bi < 0) return;
+        uint4* out = (uint4*)(c.kc + (int64_t)bi * (16 * D));
+        float d_old = 0.f;
+        uint4 old[NI];
+        if (begun) {
+            d_old = c.ks[bi];
+#pragma unroll
+            for (int i = 0; i < NI; i++) {
+                const int it = min(lane + 64 * i, D - 1);
+                old[i] = out[(it % CH) * 16 + it / CH];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NI; i++) {
+            const int it = lane + 64 * i, tok = it / CH;
+            if (it < D && tok >= t.j0 && tok < t.j1) {
 #pragma unroll
                 for (int e = 0; e < 16; e++) top = max(top, abs_bits(x[i][e]));
             }
         }
         const Coding cd = coding(wave_max(top), d_old, begun);
-        if (lane == 0) *scale = cd.d;
+        if (lane == 0) c.ks[bi] = cd.d;
 #pragma unroll
         for (int i = 0; i < NI; i++) {
             const int it = lane + 64 * i, tok = it / CH, ch = it % CH;
-            uint4* dst = (uint4*)(out + (ch * 16 + tok) * 16);
-            if (it < D && tok >= j0 && tok < j1) {
+            uint4* dst = out + ch * 16 + tok;
+            if (it < D && tok >= t.j0 && tok < t.j1) {
                 uint32_t w[4];
 #pragma unroll
                 for (int e = 0; e < 4; e++)
                     w[e] = code8(x[i][4 * e] * cd.inv) | code8(x[i][4 * e + 1] * cd.inv) << 8 |
                            code8(x[i][4 * e + 2] * cd.inv) << 16 | code8(x[i][4 * e + 3] * cd.inv) << 24;
                 *dst = make_uint4(w[0], w[1], w[2], w[3]);
-            } else if (it < D && tok < j0 && cd.ratio != 1.f) {
-                const uint4 o = *dst;
-                uint32_t w[4] = {o.x, o.y, o.z, o.w};
+            } else if (it < D && tok < t.j0 && cd.ratio != 1.f) {
+                uint32_t w[4] = {old[i].x, old[i].y, old[i].z, old[i].w};
 #pragma unroll
                 for (int e = 0; e < 4; e++)
                     w[e] = code8(byte_s8(w[e], 0) * cd.ratio) | code8(byte_s8(w[e], 1) * cd.ratio) << 8 |
@@ -133,42 +181,48 @@ __global__ __launch_bounds__(64 * kWaves) void kv8_write_kernel(KvCache c, KvSeq
             }
         }
     } else {
-        constexpr int NI = (D / 2 + 63) / 64;
-        float x[NI][2][16];
+        using Share = VShare<D>;
+        constexpr int TOK = Share::TOK;
+        const int dim = 4 * (lane % Share::groups), first = lane / Share::groups * TOK;
+        const bool on = lane < Share::groups * Share::parts;
+        float x[TOK][4];
+#pragma unroll
+        for (int j = 0; j < TOK; j++) {
+#pragma unroll
+            for (int e = 0; e < 4; e++) x[j][e] = 0.f;
+            if (on && first + j >= t.j0 && first + j < t.j1)
+                load4<XT>(v, (t.row + first + j) * st.v_row + t.h * st.v_head + dim, x[j]);
+        }
+        const int bi = kv8_block(c, q, s, t.h, t.blk);
+        if (bi < 0) return;
+        int8_t* out = c.vc + (int64_t)bi * (16 * D) + dim * 16 + first;
+        float d_old = 0.f;
+        uint32_t old[4][TOK / 4] = {};
+        if (begun) {
+            d_old = c.vs[bi];
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                if (on) load_run<TOK>(out + 16 * e, old[e]);
+        }
         uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < NI; i++) {
-            const int dim = 2 * (lane + 64 * i);
+        for (int j = 0; j < TOK; j++)
 #pragma unroll
-            for (int t = 0; t < 16; t++) {
-                x[i][0][t] = x[i][1][t] = 0.f;
-                if (dim < D && t >= j0 && t < j1)
-                    load2<XT>(v, (row + t) * st.v_row + h * st.v_head + dim, x[i][0][t], x[i][1][t]);
-                top = max(top, max(abs_bits(x[i][0][t]), abs_bits(x[i][1][t])));
-            }
-        }
+            for (int e = 0; e < 4; e++) top = max(top, abs_bits(x[j][e]));
         const Coding cd = coding(wave_max(top), d_old, begun);
-        if (lane == 0) *scale = cd.d;
+        if (lane == 0) c.vs[bi] = cd.d;
+        if (!on) return;
+        // earlier tokens, the new ones, and zeros past the sequence's end
 #pragma unroll
-        for (int i = 0; i < NI; i++) {
-            const int dim = 2 * (lane + 64 * i);
-            if (dim >= D) continue;
+        for (int e = 0; e < 4; e++) {
+            uint32_t w[TOK / 4] = {};
 #pragma unroll
-            for (int u = 0; u < 2; u++) {
-                uint4* dst = (uint4*)(out + (dim + u) * 16);
-                uint32_t w[4] = {0, 0, 0, 0}, old[4] = {0, 0, 0, 0};
-                if (begun) {
-                    const uint4 o = *dst;
-                    old[0] = o.x, old[1] = o.y, old[2] = o.z, old[3] = o.w;
-                }
-                // earlier tokens, the new ones, and zeros past the sequence's end
-#pragma unroll
-                for (int t = 0; t < 16; t++) {
-                    const uint32_t was = code8(byte_s8(old[t >> 2], t & 3) * cd.ratio);
-                    w[t >> 2] |= (t < j0 ? was : code8(x[i][u][t] * cd.inv)) << (8 * (t & 3));
-                }
-                *dst = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int j = 0; j < TOK; j++) {
+                uint32_t code = code8(x[j][e] * cd.inv);
+                if (begun && first + j < t.j0) code = code8(byte_s8(old[e][j >> 2], j & 3) * cd.ratio);
+                w[j >> 2] |= code << (8 * (j & 3));
             }
+            store_run<TOK>(out + 16 * e, w);
         }
     }
 }
@@ -182,31 +236,21 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 // layout of the write kernel, so the stores of a token are one contiguous run.
 template <int YT, int D>
 __global__ __launch_bounds__(64 * kWaves) void kv8_read_kernel(KvCache c, KvSeqs q, void* k, void* v, KvStrides st) {
-    const int lane = threadIdx.x & 63;
-    int item = blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int s = blockIdx.y;
-    const KvSpan sp = kv8_span(q, s);
-    const int h = item % c.heads;
-    item /= c.heads;
-    const bool is_v = item & 1;
-    const int p0 = sp.len - sp.n;
-    const int blk = (p0 >> 4) + (item >> 1);
-    if (sp.n == 0 || 16 * blk >= sp.len) return;
-    const int bi = kv8_block(c, q, s, h, blk);
-    const int j0 = p0 > 16 * blk ? p0 - 16 * blk : 0;
-    const int j1 = sp.len - 16 * blk < 16 ? sp.len - 16 * blk : 16;
-    const int64_t row = (int64_t)sp.r0 + 16 * blk - p0;
-    const float d = bi < 0 ? 0.f : (is_v ? c.vs : c.ks)[bi];               // no page: zeros
-    const int8_t* in = (is_v ? c.vc : c.kc) + (int64_t)(bi < 0 ? 0 : bi) * (16 * D);
-    if (!is_v) {
+    const int lane = threadIdx.x & 63, s = blockIdx.y;
+    const Item t = kv8_item(c, kv8_span(q, s), blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
+    if (t.none) return;
+    const int bi = kv8_block(c, q, s, t.h, t.blk);
+    const float d = bi < 0 ? 0.f : (t.is_v ? c.vs : c.ks)[bi];  // no page: zeros
+    const int8_t* in = (t.is_v ? c.vc : c.kc) + (int64_t)(bi < 0 ? 0 : bi) * (16 * D);
+    if (!t.is_v) {
         constexpr int CH = D / 16, NI = (D + 63) / 64;
 #pragma unroll
         for (int i = 0; i < NI; i++) {
             const int it = lane + 64 * i, tok = it / CH, ch = it % CH;
-            if (it >= D || tok < j0 || tok >= j1) continue;
+            if (it >= D || tok < t.j0 || tok >= t.j1) continue;
             const uint4 o = *(const uint4*)(in + (ch * 16 + tok) * 16);
             const uint32_t w[4] = {o.x, o.y, o.z, o.w};
-            const int64_t at = (row + tok) * st.k_row + h * st.k_head + 16 * ch;
+            const int64_t at = (t.row + tok) * st.k_row + t.h * st.k_head + 16 * ch;
             if constexpr (YT == XT_F32) {
                 float4* y = (float4*)((float*)k + at);
 #pragma unroll
@@ -226,23 +270,25 @@ __global__ __launch_bounds__(64 * kWaves) void kv8_read_kernel(KvCache c, KvSeqs
             }
         }
     } else {
-        constexpr int NI = (D / 2 + 63) / 64;
+        using Share = VShare<D>;
+        constexpr int TOK = Share::TOK;
+        const int dim = 4 * (lane % Share::groups), first = lane / Share::groups * TOK;
+        if (lane >= Share::groups * Share::parts) return;
+        uint32_t w[4][TOK / 4];
 #pragma unroll
-        for (int i = 0; i < NI; i++) {
-            const int dim = 2 * (lane + 64 * i);
-            if (dim >= D) continue;
-            const uint4 o = *(const uint4*)(in + dim * 16), o2 = *(const uint4*)(in + dim * 16 + 16);
-            const uint32_t a[4] = {o.x, o.y, o.z, o.w}, b[4] = {o2.x, o2.y, o2.z, o2.w};
+        for (int e = 0; e < 4; e++) load_run<TOK>(in + dim * 16 + first + 16 * e, w[e]);
 #pragma unroll
-            for (int t = 0; t < 16; t++) {
-                if (t < j0 || t >= j1) continue;
-                const float x0 = byte_s8(a[t >> 2], t & 3) * d, x1 = byte_s8(b[t >> 2], t & 3) * d;
-                const int64_t at = (row + t) * st.v_row + h * st.v_head + dim;
-                if constexpr (YT == XT_F32)
-                    *(float2*)((float*)v + at) = make_float2(x0, x1);
-                else
-                    *(uint32_t*)((uint16_t*)v + at) = pack2<YT>(keep_f32(x0), keep_f32(x1));
-            }
+        for (int j = 0; j < TOK; j++) {
+            if (first + j < t.j0 || first + j >= t.j1) continue;
+            float x[4];
+#pragma unroll
+            for (int e = 0; e < 4; e++) x[e] = byte_s8(w[e][j >> 2], j & 3) * d;
+            const int64_t at = (t.row + first + j) * st.v_row + t.h * st.v_head + dim;
+            if constexpr (YT == XT_F32)
+                *(float4*)((float*)v + at) = make_float4(x[0], x[1], x[2], x[3]);
+            else
+                *(uint2*)((uint16_t*)v + at) = make_uint2(pack2<YT>(keep_f32(x[0]), keep_f32(x[1])),
+                                                          pack2<YT>(keep_f32(x[2]), keep_f32(x[3])));
         }
     }
 }
