@@ -459,32 +459,40 @@ def kv8_seqs(table, rows, kv_len, T, max_new, max_kv):
     return _Desc(QgKv8Seqs(*(x.data_ptr() for x in t), table.shape[0], table.shape[1], T, max_new, max_kv), t, T=T)
 
 
-def _rows3(x, shape, where):
-    """(address, row stride, head stride) of a tensor of this [T][heads][dim] shape."""
-    if x.shape != shape:
-        raise QGError(QG_ESHAPE, where)
-    row, head, one = x.stride()
-    if one != 1:
-        raise QGError(QG_EALIGN, where)
-    return x.data_ptr(), row, head
+_entries = {}
+
+
+def _entry(name):
+    """An entry point, looked up once: these calls are made a few at a time for microseconds of work."""
+    import torch
+    _XT.update({torch.float32: QG_X_F32, torch.float16: QG_X_F16, torch.bfloat16: QG_X_BF16})
+    _entries[name] = call = getattr(lib(), name)
+    return call
 
 
 def qg_kv8_write(cache, seqs, k, v, stream=None):
     """Codes k, v [T][heads][dim] (any row and head strides) into the cache as their sequences' last tokens."""
-    _kv8(lib().qg_kv8_write, "qg_kv8_write", cache, seqs, k, v, stream)
+    _kv8("qg_kv8_write", cache, seqs, k, v, stream)
 
 
 def qg_kv8_read(cache, seqs, k_out, v_out, stream=None):
     """Reads the sequences' last tokens back into k_out, v_out [T][heads][dim]."""
-    _kv8(lib().qg_kv8_read, "qg_kv8_read", cache, seqs, k_out, v_out, stream)
+    _kv8("qg_kv8_read", cache, seqs, k_out, v_out, stream)
 
 
-def _kv8(call, where, cache, seqs, k, v, stream):
-    _expect(k.dtype == v.dtype, where)
-    shape = (seqs.T, cache.heads, cache.dim)
-    kp, kr, kh = _rows3(k, shape, where)
-    vp, vr, vh = _rows3(v, shape, where)
-    status = call(cache.ptr, seqs.ptr, kp, kr, kh, vp, vr, vh, _xt(k), _stream(stream))
+def _kv8(where, cache, seqs, k, v, stream):
+    call = _entries.get(where) or _entry(where)
+    xt, shape = k.dtype, (seqs.T, cache.heads, cache.dim)
+    if xt is not v.dtype or xt not in _XT:
+        raise QGError(QG_EINVAL, where)
+    if k.shape != shape or v.shape != shape:
+        raise QGError(QG_ESHAPE, where)
+    k_row, k_head, k_one = k.stride()
+    v_row, v_head, v_one = v.stride()
+    if k_one != 1 or v_one != 1:
+        raise QGError(QG_EALIGN, where)
+    status = call(cache.ptr, seqs.ptr, k.data_ptr(), k_row, k_head, v.data_ptr(), v_row, v_head, _XT[xt],
+                  _stream(stream))
     if status:
         raise QGError(status, where)
 
@@ -496,13 +504,19 @@ def qg_attn_kv8_workspace(cache, seqs, q_heads) -> int:
 def qg_attn_kv8(cache, seqs, q, o, q_heads, scale, causal=True, window=0, workspace=None, stream=None):
     """Attention of q [T][q_heads][dim] over the cache into o (same shape and type); workspace: a device
     tensor of at least qg_attn_kv8_workspace bytes."""
-    _expect(q.dtype == o.dtype, "qg_attn_kv8")
-    shape = (seqs.T, q_heads, cache.dim)
-    qp, qr, qh = _rows3(q, shape, "qg_attn_kv8")
-    op, orow, oh = _rows3(o, shape, "qg_attn_kv8")
+    call = _entries.get("qg_attn_kv8") or _entry("qg_attn_kv8")
+    xt, shape = q.dtype, (seqs.T, q_heads, cache.dim)
+    if xt is not o.dtype or xt not in _XT:
+        raise QGError(QG_EINVAL, "qg_attn_kv8")
+    if q.shape != shape or o.shape != shape:
+        raise QGError(QG_ESHAPE, "qg_attn_kv8")
+    q_row, q_head, q_one = q.stride()
+    o_row, o_head, o_one = o.stride()
+    if q_one != 1 or o_one != 1:
+        raise QGError(QG_EALIGN, "qg_attn_kv8")
     wp, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
-    status = lib().qg_attn_kv8(cache.ptr, seqs.ptr, qp, qr, qh, op, orow, oh, _xt(q), q_heads, scale, 1 if causal else 0,
-                               window, wp, size, _stream(stream))
+    status = call(cache.ptr, seqs.ptr, q.data_ptr(), q_row, q_head, o.data_ptr(), o_row, o_head, _XT[xt], q_heads, scale,
+                  1 if causal else 0, window, wp, size, _stream(stream))
     if status:
         raise QGError(status, "qg_attn_kv8")
 
@@ -515,9 +529,17 @@ def qgemm_w8a8(w_codes, w_scales, X, Y, N, K, T, workspace=None, stream=None):
     """Y [T][N] = X [T][K] times int8 weights [N][K] with a scale an output channel, X coded in 8 bits with a
     scale a token on the way; types from the tensors' dtypes; workspace: a device tensor of at least
     qgemm_w8a8_workspace bytes."""
+    call = _entries.get("qgemm_w8a8") or _entry("qgemm_w8a8")
+    xt, yt = _XT.get(X.dtype), _XT.get(Y.dtype)
+    if xt is None or yt is None or w_codes.itemsize != 1 or w_scales.itemsize != 4:
+        raise QGError(QG_EINVAL, "qgemm_w8a8")
+    if X.numel() < T * K or Y.numel() < T * N or w_codes.numel() < N * K or w_scales.numel() < N:
+        raise QGError(QG_ESHAPE, "qgemm_w8a8")
+    if not (X.is_contiguous() and Y.is_contiguous() and w_codes.is_contiguous() and w_scales.is_contiguous()):
+        raise QGError(QG_EALIGN, "qgemm_w8a8")
     wp, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
-    status = lib().qgemm_w8a8(w_codes.data_ptr(), w_scales.data_ptr(), X.data_ptr(), _xt(X), Y.data_ptr(), _xt(Y), N, K, T,
-                              wp, size, _stream(stream))
+    status = call(w_codes.data_ptr(), w_scales.data_ptr(), X.data_ptr(), xt, Y.data_ptr(), yt, N, K, T, wp, size,
+                  _stream(stream))
     if status:
         raise QGError(status, "qgemm_w8a8")
 
