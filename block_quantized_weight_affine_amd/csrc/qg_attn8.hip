@@ -25,13 +25,13 @@ __device__ __forceinline__ float groups_sum(float v) {
     return v + __shfl_xor(v, 32);
 }
 
-// Wavefronts a SIMD of the rows kernel: q, two loads and the sums take (3 + pieces) dim / 4 registers a lane.
-constexpr int rows_waves(int pieces, int dim) {
-    return (3 + pieces) * dim / 4 <= 128 ? 3 : (3 + pieces) * dim / 4 <= 200 ? 2 : 1;
-}
+// Registers a lane that q, two loads and the sums of the rows kernel take; in its largest forms the two loads
+// share theirs, and a CU takes one workgroup, of 8 wavefronts.
+constexpr int rows_registers(int pieces, int dim) { return (3 + pieces) * dim / 4; }
+constexpr bool rows_late(int pieces, int dim) { return rows_registers(pieces, dim) > 200; }
 
 // One workgroup takes 16 rows (query rows times the heads that share a K/V head, counted together) and
-// one split of the tokens they see; its wavefronts take 64 tokens in turn and are joined at the end.
+// one split of the tokens they see; its W wavefronts take 64 tokens in turn and are joined at the end.
 //
 // Layout of a wavefront's 64 tokens (four blocks): the first product is K Q^T with A row r of its
 // m-th instruction = token 4m + r % 4 of block r / 4, so result lane (row l % 16, group g = l / 16)
@@ -39,15 +39,15 @@ constexpr int rows_waves(int pieces, int dim) {
 // the weights never move between lanes, every lane has one K and one V scale, and both code loads are
 // 16 bytes a lane as the cache holds them.  The next tokens' K is loaded as soon as the first product is
 // done with this one's registers, V after the second, the table's entry one turn earlier.
-template <int XT, int D>
-__global__ __launch_bounds__(256, rows_waves(XT == XT_F32 ? 2 : 1, D)) void attn8_rows_kernel(AttnParams a) {
+template <int XT, int D, int W>
+__global__ __launch_bounds__(64 * W, W == 4 && rows_registers(XT == XT_F32 ? 2 : 1, D) <= 128 ? 3 : 2) void attn8_rows_kernel(AttnParams a) {
     constexpr int NP = XT == XT_F32 ? 2 : 1;  // f16 pieces of a q value and of a weight
     constexpr int NH = (D + 63) / 64;         // 16-byte K loads a token
     constexpr int NT = D / 16;
     constexpr int DH = D > 128 ? D / 2 : D;   // dims joined at a time
-    constexpr bool kTight = NP * D > 128;
-    __shared__ float sh_o[4][16][DH + 4];
-    __shared__ float sh_m[4][16], sh_l[4][16];
+    constexpr bool kLate = rows_late(NP, D);
+    __shared__ float sh_o[W][16][DH + 4];
+    __shared__ float sh_m[W][16], sh_l[W][16];
 
     const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -100,7 +100,7 @@ __global__ __launch_bounds__(256, rows_waves(XT == XT_F32 ? 2 : 1, D)) void attn
         for (int i = 0; i < NT; i++) vw[i] = *(const uint4*)(vp + i * 256);
     };
     const int first = t0 + 64 * wave;
-    const int page0 = entry(first), page1 = entry(first + 256);
+    const int page0 = entry(first), page1 = entry(first + 64 * W);
 
     float x[NH][16];
     const int64_t at = (int64_t)(sp.r0 + ri) * a.q_row + head * a.q_head;
@@ -117,7 +117,7 @@ __global__ __launch_bounds__(256, rows_waves(XT == XT_F32 ? 2 : 1, D)) void attn
     }
     int bi = index(first, page0), page = page1;
     load_k(bi);
-    if (!kTight) load_v(bi);
+    if (!kLate) load_v(bi);
     float ks = a.c.ks[max(bi, 0)], vs = a.c.vs[max(bi, 0)];
 
     // q as f16 pieces, scaled so that the row's largest lies in [2^14, 2^15)
@@ -144,11 +144,6 @@ __global__ __launch_bounds__(256, rows_waves(XT == XT_F32 ? 2 : 1, D)) void attn
             }
     }
 
-    if (kTight) {  // q's values make room for V's
-        __builtin_amdgcn_sched_barrier(0);
-        load_v(bi);
-    }
-
     f32x4_t o[NT];
 #pragma unroll
     for (int i = 0; i < NT; i++) o[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -158,7 +153,7 @@ __global__ __launch_bounds__(256, rows_waves(XT == XT_F32 ? 2 : 1, D)) void attn
     e0 = __builtin_amdgcn_readfirstlane(max(e0, __shfl_xor(e0, 32)));
     if (e0 < -500) e0 = 0;
 
-    for (int tb = first; tb < t1; tb += 256) {
+    for (int tb = first; tb < t1; tb += 64 * W) {
         f32x4_t acc[4];
 #pragma unroll
         for (int mi = 0; mi < 4; mi++) {
@@ -175,13 +170,17 @@ __global__ __launch_bounds__(256, rows_waves(XT == XT_F32 ? 2 : 1, D)) void attn
         }
         const int was = bi;
         const float vnow = vs, kf = vs - vs == 0.f ? ks * qs : __builtin_nanf("");
-        const bool more = tb + 256 < t1;
+        const bool more = tb + 64 * W < t1;
+        if (kLate) {
+            __builtin_amdgcn_sched_barrier(0);
+            load_v(bi);
+        }
         if (more) {
-            bi = index(tb + 256, page);
-            load_k(bi);
+            bi = index(tb + 64 * W, page);
+            if (!kLate) load_k(bi);
             ks = a.c.ks[max(bi, 0)];
             vs = a.c.vs[max(bi, 0)];
-            page = entry(tb + 512);
+            page = entry(tb + 128 * W);
         }
         const float lv = v_power(vnow, e0);
         float p[16];
@@ -229,7 +228,14 @@ __global__ __launch_bounds__(256, rows_waves(XT == XT_F32 ? 2 : 1, D)) void attn
                 o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pf[n][1], o[i], 0, 0, 0);
             }
         }
-        if (more) load_v(bi);
+        if (more) {
+            if (kLate) {
+                __builtin_amdgcn_sched_barrier(0);
+                load_k(bi);
+            } else {
+                load_v(bi);
+            }
+        }
     }
 
     // join the wavefronts
@@ -239,7 +245,9 @@ __global__ __launch_bounds__(256, rows_waves(XT == XT_F32 ? 2 : 1, D)) void attn
         sh_l[wave][col] = l;
     }
     __syncthreads();
-    const float mt = fmaxf(fmaxf(sh_m[0][col], sh_m[1][col]), fmaxf(sh_m[2][col], sh_m[3][col]));
+    float mt = kNegInf;
+#pragma unroll
+    for (int w = 0; w < W; w++) mt = fmaxf(mt, sh_m[w][col]);
     const float f = m == kNegInf ? 0.f : ldexpf(__builtin_amdgcn_exp2f(m - mt), e0);
 #pragma unroll
     for (int d0 = 0; d0 < D; d0 += DH) {
@@ -250,20 +258,20 @@ __global__ __launch_bounds__(256, rows_waves(XT == XT_F32 ? 2 : 1, D)) void attn
             *(f32x4_t*)&sh_o[wave][col][16 * i + 4 * g] = v;
         }
         __syncthreads();
-        for (int x = threadIdx.x; x < 16 * (DH / 4); x += 256) {
+        for (int x = threadIdx.x; x < 16 * (DH / 4); x += 64 * W) {
             const int row = x / (DH / 4), d = 4 * (x % (DH / 4));
             const int rr = tile * 16 + row;
             if (rr >= rows) continue;
             float mr = kNegInf;
 #pragma unroll
-            for (int w = 0; w < 4; w++) mr = fmaxf(mr, sh_m[w][row]);
+            for (int w = 0; w < W; w++) mr = fmaxf(mr, sh_m[w][row]);
             float lr = 0.f;
 #pragma unroll
-            for (int w = 0; w < 4; w++)
+            for (int w = 0; w < W; w++)
                 lr += sh_l[w][row] * (sh_m[w][row] == kNegInf ? 1.f : __builtin_amdgcn_exp2f(sh_m[w][row] - mr));
             f32x4_t v = *(const f32x4_t*)&sh_o[0][row][d];
 #pragma unroll
-            for (int w = 1; w < 4; w++) v += *(const f32x4_t*)&sh_o[w][row][d];
+            for (int w = 1; w < W; w++) v += *(const f32x4_t*)&sh_o[w][row][d];
             const int64_t trow = sp.r0 + rr / a.group;
             const int hd = h * a.group + rr % a.group;
             if (tr.nact > 1) {
@@ -373,7 +381,7 @@ __global__ __launch_bounds__(256) void attn8_join_kernel(AttnParams a) {
     store2<XT>(a.O, at + d, y[0], y[1]);
 }
 
-constexpr int64_t kJoinWide = 2048;  // rows that are joined by a workgroup each
+constexpr int64_t kJoinWide = 2048;  // rows that are joined by a workgroup each, where a wavefront has more than 8 splits to read
 
 template <int XT, int D>
 hipError_t launch_one(const AttnParams& a, hipStream_t s) {
@@ -382,11 +390,14 @@ hipError_t launch_one(const AttnParams& a, hipStream_t s) {
         const hipError_t e = launch_attn8_tile(a, XT, s);
         if (e != hipSuccess) return e;
     } else {
-        attn8_rows_kernel<XT, D><<<dim3((uint32_t)grid), 256, 0, s>>>(a);
+        if (a.row_waves == 8)
+            attn8_rows_kernel<XT, D, 8><<<dim3((uint32_t)grid), 512, 0, s>>>(a);
+        else if constexpr (!rows_late(XT == XT_F32 ? 2 : 1, D))
+            attn8_rows_kernel<XT, D, 4><<<dim3((uint32_t)grid), 256, 0, s>>>(a);
     }
     if (a.splits > 1) {
         const uint32_t rows = (uint32_t)a.q.max_new * (uint32_t)a.q_heads;
-        if ((int64_t)rows * a.q.seqs <= kJoinWide)
+        if (a.splits > 8 && (int64_t)rows * a.q.seqs <= kJoinWide)
             attn8_join_kernel<XT, D, 4><<<dim3(rows, a.q.seqs), 256, 0, s>>>(a);
         else
             attn8_join_kernel<XT, D, 1><<<dim3((rows + 3) / 4, a.q.seqs), 256, 0, s>>>(a);
@@ -411,7 +422,7 @@ hipError_t launch_dim(const AttnParams& a, hipStream_t s) {
 namespace {
 // Rows a K/V head (query rows times heads of the group) from which the tile kernel takes over.
 constexpr int64_t kTileFrom = 64;
-constexpr int64_t kMinChunk = 256;
+constexpr int64_t kMinChunk = 256, kAlone = 1024;
 void set_tiles(AttnParams& a, int xt) {
     const int64_t rows = (int64_t)a.q.max_new * a.group;
     a.tile_rows = rows >= kTileFrom ? attn8_tile_rows(a, xt) : 16;
@@ -419,7 +430,7 @@ void set_tiles(AttnParams& a, int xt) {
 }
 // Splits of `span` tokens.  Rows kernel: enough to fill the card (a CU holds 2 or 3 of its workgroups, or
 // one of the larger ones), and of the longest sequence always a few, so that sequences of different lengths
-// even out.  Tile kernel: a stage of 64 tokens takes about 24 times as long as a tile's part in writing
+// even out; one where 8 wavefronts are through sooner than a second kernel would join.  Tile kernel: a stage of 64 tokens takes about 24 times as long as a tile's part in writing
 // and joining the sums of one more split, so at most sqrt(24 stages / workgroups); none once the card is full.
 int64_t wanted_splits(const AttnParams& a, int xt, int64_t span) {
     const int64_t base = (int64_t)a.q.seqs * a.c.heads * a.tiles;
@@ -428,9 +439,9 @@ int64_t wanted_splits(const AttnParams& a, int xt, int64_t span) {
         while ((k + 1) * base <= 256 && (k + 1) * (k + 1) * base <= 24 * (span / 64)) k++;
         return k;
     }
-    const bool one = rows_waves(xt == XT_F32 ? 2 : 1, a.c.dim) == 1;
-    const int64_t fill = one ? 256 : 1024, least = one ? 3 : 6;
-    return std::max((fill + base - 1) / base, least);
+    if (rows_late(xt == XT_F32 ? 2 : 1, a.c.dim)) return std::max((256 + base - 1) / base, (int64_t)3);
+    if (span <= kAlone && base <= 128) return 1;
+    return std::max((1024 + base - 1) / base, (int64_t)6);
 }
 }  // namespace
 
@@ -454,7 +465,8 @@ void attn8_plan(AttnParams& a, int xt) {
     if (a.causal && a.window > 0 && seen < span) span = seen;
     const int64_t want = wanted_splits(a, xt, span);
     int64_t chunk = (span + want - 1) / want;
-    const int64_t unit = a.tile_rows > 16 ? 64 : 256;
+    a.row_waves = rows_late(xt == XT_F32 ? 2 : 1, a.c.dim) || (want == 1 && a.tile_rows == 16) ? 8 : 4;
+    const int64_t unit = a.tile_rows > 16 ? 64 : 64 * a.row_waves;
     if (chunk < kMinChunk) chunk = kMinChunk;
     a.chunk = (int)((chunk + unit - 1) / unit * unit);
     a.splits = (int)((span + a.chunk - 1) / a.chunk);
