@@ -151,3 +151,43 @@ def test_w8a8_streams_and_refusals():
         with pytest.raises(qg.QGError):
             qg.qgemm_w8a8(**args)
     assert torch.all(y == 3)
+
+
+def test_pages_past_4_gib():
+    """The same tokens in the first pages of a small cache and in the last of one whose codes pass 2^32 bytes: the
+    same bits."""
+    print("pages past 4 GiB", flush=True)
+    heads, dim, page, lens = 8, 128, 256, [(70, 600), (1, 300)]
+    pages = 2 ** 32 // (heads * dim * page) + 40
+    got = []
+    for total, first in ((40, 0), (pages, pages - 5)):
+        need = [-(-t // page) for _, t in lens]
+        table = torch.full((2, max(need)), -1, dtype=torch.int32)
+        at = first
+        for s, n in enumerate(need):
+            table[s, :n] = torch.arange(at, at + n)
+            at += n
+        tensors = qg.kv8_pages(total, page, heads, dim)
+        cache = qg.kv8_cache(*tensors, page, heads, dim)
+        rng = np.random.default_rng(3)
+        all_rows = _values(rng, (900, 2, heads, dim), "bf16").cuda()
+        ints = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+        seqs = qg.kv8_seqs(table.cuda(), ints(0, 600, 900), ints(600, 300), 900, 600, 600)
+        qg.qg_kv8_write(cache, seqs, all_rows[:, 0], all_rows[:, 1])
+        k, v = torch.empty(900, heads, dim, device="cuda"), torch.empty(900, heads, dim, device="cuda")
+        qg.qg_kv8_read(cache, seqs, k, v)
+        seqs = qg.kv8_seqs(table.cuda(), ints(0, 70, 71), ints(600, 300), 71, 70, 600)
+        q = _values(rng, (71, 16, dim), "bf16").cuda()
+        many = torch.empty_like(q)
+        work = torch.empty(max(16, qg.qg_attn_kv8_workspace(cache, seqs, 16)), dtype=torch.uint8, device="cuda")
+        qg.qg_attn_kv8(cache, seqs, q, many, 16, 0.09, True, 0, work)
+        seqs = qg.kv8_seqs(table.cuda(), ints(0, 1, 2), ints(600, 300), 2, 1, 600)
+        single = torch.empty_like(q[:2])
+        work = torch.empty(max(16, qg.qg_attn_kv8_workspace(cache, seqs, 16)), dtype=torch.uint8, device="cuda")
+        qg.qg_attn_kv8(cache, seqs, q[:2], single, 16, 0.09, True, 0, work)
+        torch.cuda.synchronize()
+        got.append([x.cpu() for x in (k, v, many, single)])
+        del cache, tensors
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert torch.isfinite(got[0][2]).all() and got[0][2].abs().max() > 0
