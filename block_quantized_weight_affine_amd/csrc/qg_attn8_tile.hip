@@ -110,39 +110,21 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && XT != XT_F32 && D <= 128 ? 2 : 
 #pragma unroll
     for (int i = 0; i <= KB; i++) first[i] = page_of((t0 >> 4) + 4 * i + (lane >> 4));
 
-    half8_t qf[CT][NP][NK];
-    float qs[CT];
+    // q sets out too, and is made operands of when everything else is on its way
+    constexpr int QW = XT == XT_F32 ? 2 : 1;
+    uint4 qraw[CT][NK][QW];
     KvSight see[CT];
 #pragma unroll
     for (int c = 0; c < CT; c++) {
         const int r = min(w0 + 32 * c + col, rows - 1), ri = r / a.group, head = h * a.group + r % a.group;
         see[c] = kv8_sight(sp, ri, a.causal, a.window);
         const int64_t at = (int64_t)(sp.r0 + ri) * a.q_row + head * a.q_head + 8 * g;
-        uint32_t top = 0;
 #pragma unroll
-        for (int k = 0; k < NK; k++) {
-            float x[8];
-            x_load8<XT>(a.Q, at + 16 * k, x);
+        for (int k = 0; k < NK; k++)
 #pragma unroll
-            for (int e = 0; e < 8; e++) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
-        }
-        top = max(top, (uint32_t)__shfl_xor((int)top, 32));
-        const int ex = q_exponent(top);
-        qs[c] = ldexpf(a.scale * kLog2e, -ex);
-#pragma unroll
-        for (int k = 0; k < NK; k++) {
-            float x[8];
-            x_load8<XT>(a.Q, at + 16 * k, x);
-#pragma unroll
-            for (int e = 0; e < 8; e++) {
-                const float v = a.scale < 0.f ? -ldexpf(x[e], ex) : ldexpf(x[e], ex);
-                const _Float16 hi = (_Float16)v;
-                qf[c][0][k][e] = hi;
-                if constexpr (NP == 2) qf[c][1][k][e] = (_Float16)(v - (float)hi);
-            }
-        }
-        qs[c] = fabsf(qs[c]);
+            for (int i = 0; i < QW; i++) qraw[c][k][i] = ((const uint4*)((const char*)a.Q + (at + 16 * k) * (2 * QW)))[i];
     }
+    __builtin_amdgcn_sched_barrier(0);
 
     int bi0 = -1, e0 = 0, eb = -1000;
     float ks0 = 0.f, vs0 = 0.f;
@@ -218,6 +200,9 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && XT != XT_F32 && D <= 128 ? 2 : 
             to[2 * j * D + (x & 1) * D + d] = __builtin_bit_cast(uint4, w);
         }
     };
+
+    half8_t qf[CT][NP][NK];
+    float qs[CT];
 
     // A weight is exp2(score + V scale's power - m + kBase), m the running maximum of what comes before
     // it: it has the V scale in it, and its sum for the denominator is taken times the reciprocal.
@@ -364,6 +349,33 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && XT != XT_F32 && D <= 128 ? 2 : 
             }
     };
 
+    // q's row as operands, scaled so that its largest value lies in [2^14, 2^15)
+    auto make_q = [&]() {
+#pragma unroll
+        for (int c = 0; c < CT; c++) {
+            float x[NK][8];
+            uint32_t top = 0;
+#pragma unroll
+            for (int k = 0; k < NK; k++) {
+                x_load8<XT>(qraw[c][k], 0, x[k]);
+#pragma unroll
+                for (int e = 0; e < 8; e++) top = max(top, __float_as_uint(x[k][e]) & 0x7fffffffu);
+            }
+            top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+            const int ex = q_exponent(top);
+            qs[c] = fabsf(ldexpf(a.scale * kLog2e, -ex));
+#pragma unroll
+            for (int k = 0; k < NK; k++)
+#pragma unroll
+                for (int e = 0; e < 8; e++) {
+                    const float v = a.scale < 0.f ? -ldexpf(x[k][e], ex) : ldexpf(x[k][e], ex);
+                    const _Float16 hi = (_Float16)v;
+                    qf[c][0][k][e] = hi;
+                    if constexpr (NP == 2) qf[c][1][k][e] = (_Float16)(v - (float)hi);
+                }
+        }
+    };
+
     uint4 rk[UN], rw[UN];
     half2_t sign[UN];
     f32x16_t s0[CT][2], s1[CT][2];
@@ -380,6 +392,8 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && XT != XT_F32 && D <= 128 ? 2 : 
                 fv[i] = *(const uint4*)(a.c.vc + (int64_t)max(__shfl(first[0], 16 * j), 0) * (16 * D) + d * 16);
                 rw[i] = *(const uint4*)(a.c.vc + (int64_t)max(__shfl(first[1], 16 * j), 0) * (16 * D) + d * 16);
             }
+        __builtin_amdgcn_sched_barrier(0);
+        make_q();
         if (bi0 >= 0) eb = v_exponent(vs0);
 #pragma unroll
         for (int x = 1; x < 64; x <<= 1) eb = max(eb, __shfl_xor(eb, x));
@@ -393,21 +407,29 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && XT != XT_F32 && D <= 128 ? 2 : 
         lds_barrier();
         sign_v(0, sign);
 #pragma unroll
-        for (int x = 0; x < 2 * UN; x++) {
+        for (int x = 0; x < 2 * UN; x++) store_k(x, fk[0], sk);
+        lds_barrier();
+        // the first S between the decoding of the next stages
 #pragma unroll
-            for (int i = 0; i < KB; i++) store_k(x, fk[i], sk + i * 8 * D);
-            store_v(x, fv, sign, sv[0]);
+        for (int x = 0; x < P1; x++) {
+            score(x, operand(x, sk, sv[0]), s0);
+#pragma unroll
+            for (int y = 2 * UN * KB * x / P1; y < 2 * UN * KB * (x + 1) / P1; y++) {
+                if (y < 2 * UN * (KB - 1))
+                    store_k(y % (2 * UN), fk[1 + y / (2 * UN)], sk + (1 + y / (2 * UN)) * 8 * D);
+                else
+                    store_v(y % (2 * UN), fv, sign, sv[0]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
         sign_v(1, sign);
-        lds_barrier();
     }
-#pragma unroll
-    for (int x = 0; x < P1; x++) score(x, operand(x, sk, sv[0]), s0);
     read_scales(0);
     scale_and_hide(0, s0);
 #pragma unroll
     for (int x = 0; x < 16; x++) top_pair(x, s0);
     settle();
+    lds_barrier();
     // Iteration t: S of stage t + 1 between the weights of stage t; then O of stage t between the maxima
     // of stage t + 1 and the decoding of stage t + KB's K and stage t + 1's V, whose successors' loads set
     // out as soon as their registers are free.  Stages past the last are hidden.
