@@ -132,7 +132,8 @@ int attn8_max_splits(AttnParams a);  // of any window and type
 size_t attn8_workspace(const AttnParams& a);
 hipError_t launch_attn8(AttnParams a, int xt, float* ws, hipStream_t s);
 
-// Y [T][N] = X [T][K] w^T in 8-bit integers; xq, xs: X's codes and row scales, set by the launcher.
+// Y [T][N] = X [T][K] w^T in 8-bit integers; set by the launcher: X's codes and row scales, and where K is
+// split over workgroups their sums [splits][T][N], `per` pieces of 128 k a split.
 struct W8A8Params {
     const int8_t* w;
     const float* ws;
@@ -141,6 +142,8 @@ struct W8A8Params {
     const float* xs;
     void* Y;
     int N, K, T, xt, yt;
+    int* part;
+    int splits, per;
 };
 size_t w8a8_workspace(int N, int K, int T);
 hipError_t launch_w8a8(W8A8Params p, void* ws, hipStream_t s);

@@ -6,6 +6,8 @@
 // The sums are exact in 32-bit integers (K <= 2^17), so no order of summation changes a result.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "qg_device.hpp"
 #include "qg_internal.hpp"
 
@@ -189,15 +191,17 @@ __global__ __launch_bounds__(64 * KS) void w8a8_rows_kernel(W8A8Params p) {
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n0 = blockIdx.x * 16 * RN, K = p.K;
-    const int units = (K + 127) / 128, pitch = fused_pitch(K);
+    // this split's pieces
+    const int lo = blockIdx.y * p.per, units = min(lo + p.per, (K + 127) / 128), end = min(K, 128 * units);
+    const int pitch = fused_pitch(K);
     const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc((void*)(p.w + (int64_t)n0 * K), 0,
                                                                         min(16 * RN, p.N - n0) * K, 0x00020000);
     const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc((void*)p.xq, 0, FUSED ? 0 : p.T * K, 0x00020000);
     // copy i has rows 8 i .. 8 i + 7
     const int even = 16 * ((lane & 7) ^ (lane >> 4)), odd = even ^ 64, from = (lane >> 3) * K;
     auto copy = [&](int8_t* s, int u) {
-        const int at[2] = {128 * u + even < K ? from + even + 128 * u : 0x40000000,
-                           128 * u + odd < K ? from + odd + 128 * u : 0x40000000};
+        const int at[2] = {128 * u + even < end ? from + even + 128 * u : 0x40000000,
+                           128 * u + odd < end ? from + odd + 128 * u : 0x40000000};
         int8_t* to = s + wave * kPiece;
 #pragma unroll
         for (int i = 0; i < 2 * RN; i++) buffer_copy16_lds(wr, to + i * 1024, at[i & 1] + 8 * i * K);
@@ -228,8 +232,8 @@ __global__ __launch_bounds__(64 * KS) void w8a8_rows_kernel(W8A8Params p) {
                 for (int i = 0; i < RN; i++) acc[i][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[i], x[t], acc[i][t], 0, 0, 0);
         }
     };
-    copy(s0, wave);
-    if constexpr (AHEAD > 1) copy(s1, wave + KS);
+    copy(s0, lo + wave);
+    if constexpr (AHEAD > 1) copy(s1, lo + wave + KS);
     if constexpr (FUSED) {
         if (p.xt == XT_F32)
             code_rows_lds<XT_F32, KS>(p.X, K, p.T, codes, dx, part);
@@ -250,7 +254,7 @@ __global__ __launch_bounds__(64 * KS) void w8a8_rows_kernel(W8A8Params p) {
         __builtin_amdgcn_sched_barrier(0);
         copy(s, u + KS * AHEAD);
     };
-    for (int u0 = wave; u0 < units; u0 += KS * AHEAD) {
+    for (int u0 = lo + wave; u0 < units; u0 += KS * AHEAD) {
         turn(s0, u0);
         if constexpr (AHEAD > 1) turn(s1, u0 + KS);
     }
@@ -269,6 +273,10 @@ __global__ __launch_bounds__(64 * KS) void w8a8_rows_kernel(W8A8Params p) {
         int sum = 0;
 #pragma unroll
         for (int v = 0; v < KS; v++) sum += red[(v * 16 * TT + t) * RP + n];
+        if (!FUSED && p.splits > 1) {
+            p.part[((int64_t)blockIdx.y * p.T + t) * p.N + n0 + n] = sum;
+            continue;
+        }
         const float d = FUSED ? dx[t] : p.xs[t];
         store_any(p.Y, p.yt, (int64_t)t * p.N + n0 + n, (float)sum * d * p.ws[n0 + n]);
     }
@@ -310,7 +318,8 @@ __global__ __launch_bounds__(64 * WT * WN) void w8a8_tile_kernel(W8A8Params p, i
     lin %= width;
     const int t0 = (first + lin % tall) * BT, n0 = lin / tall * BN;
 
-    const int K = p.K, stages = (K + 127) / 128;
+    const int K = p.K;
+    const int lo = blockIdx.y * p.per, stages = min(lo + p.per, (K + 127) / 128), end = min(K, 128 * stages);
     const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc((void*)(p.xq + (int64_t)t0 * K), 0,
                                                                         min(BT, p.T - t0) * K, 0x00020000);
     const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc((void*)(p.w + (int64_t)n0 * K), 0,
@@ -318,7 +327,7 @@ __global__ __launch_bounds__(64 * WT * WN) void w8a8_tile_kernel(W8A8Params p, i
     const int chunk = (lane & 7) ^ ((lane >> 4) + 4 * (wave & 1));  // of the row, for this lane's slot
     const int voff = (8 * wave + (lane >> 3)) * K + 16 * chunk;
     auto copy = [&](int st, int8_t* s) {
-        const int k = 128 * st + 16 * chunk < K ? voff + 128 * st : 0x40000000;  // past K: zeros
+        const int k = 128 * st + 16 * chunk < end ? voff + 128 * st : 0x40000000;  // past the end: zeros
 #pragma unroll
         for (int i = 0; i < XC; i++) buffer_copy16_lds(xr, s + (i * NW + wave) * 1024, k + i * NW * 8 * K);
 #pragma unroll
@@ -368,16 +377,16 @@ __global__ __launch_bounds__(64 * WT * WN) void w8a8_tile_kernel(W8A8Params p, i
     };
     // two arrays, so that a read of one never waits for the copies into the other; past the last stage the
     // copies are zeros
-    copy(0, s0);
-    copy(1, s1);
+    copy(lo, s0);
+    copy(lo + 1, s1);
     if constexpr (R > 2) {
-        copy(2, s2);
-        copy(3, s3);
+        copy(lo + 2, s2);
+        copy(lo + 3, s3);
     }
     __syncthreads();
     frags(s0, 0, x[0], w[0]);
     __builtin_amdgcn_sched_barrier(0);
-    for (int st = 0; st < stages; st += R) {
+    for (int st = lo; st < stages; st += R) {
         stage(st, s0, s1);
         stage(st + 1, s1, R > 2 ? s2 : s0);
         if constexpr (R > 2) {
@@ -388,6 +397,23 @@ __global__ __launch_bounds__(64 * WT * WN) void w8a8_tile_kernel(W8A8Params p, i
     }
     __builtin_amdgcn_s_waitcnt(0x0f70);  // the last copy has landed before its place is used again
     __syncthreads();
+
+    if (p.splits > 1) {
+#pragma unroll
+        for (int b = 0; b < MT; b++) {
+            const int t = t0 + 32 * (MT * wt + b) + r;
+            if (t >= p.T) continue;
+            int* to = p.part + ((int64_t)blockIdx.y * p.T + t) * p.N;
+#pragma unroll
+            for (int a = 0; a < NT; a++)
+#pragma unroll
+                for (int e = 0; e < 16; e++) {
+                    const int n = n0 + 32 * (NT * wn + a) + 8 * (e >> 2) + 4 * g + (e & 3);
+                    if (n < p.N) to[n] = acc[a][b][e];
+                }
+        }
+        return;
+    }
 
     // 32 tokens x 64 rows at a time through this wavefront's 8 KiB, so that stores are whole lines
     float* out = (float*)(s0 + wave * 8192);
@@ -442,6 +468,17 @@ __global__ __launch_bounds__(64 * WT * WN) void w8a8_tile_kernel(W8A8Params p, i
     }
 }
 
+// The sums of the splits of K; they are integers, so their order does not matter.
+__global__ __launch_bounds__(256) void w8a8_join_kernel(W8A8Params p) {
+    const int n = blockIdx.x * 256 + threadIdx.x, t = blockIdx.y;
+    if (n >= p.N) return;
+    const int64_t all = (int64_t)p.T * p.N, at = (int64_t)t * p.N + n;
+    int sum = 0;
+#pragma unroll 8
+    for (int i = 0; i < p.splits; i++) sum += p.part[i * all + at];
+    store_any(p.Y, p.yt, at, (float)sum * p.xs[t] * p.ws[n]);
+}
+
 constexpr int kRowsMax = 128;  // tokens of the streaming kernel
 bool fused(int K, int T) { return T <= 8 && T * fused_pitch(K) <= kFusedLds; }
 
@@ -449,7 +486,7 @@ template <int TT, int RN, int KS, int CODES>
 void launch_rows(const W8A8Params& p, hipStream_t s) {
     constexpr int kRing = KS * (RN + (CODES ? 0 : TT)) * 2048, kRed = KS * 16 * TT * (16 * RN + 4) * 4;
     constexpr int AHEAD = (kRed > kRing ? kRed : kRing) + kRing + CODES + 2048 <= 160 << 10 ? 2 : 1;
-    w8a8_rows_kernel<TT, RN, KS, AHEAD, CODES><<<(uint32_t)((p.N + 16 * RN - 1) / (16 * RN)), 64 * KS, 0, s>>>(p);
+    w8a8_rows_kernel<TT, RN, KS, AHEAD, CODES><<<dim3((p.N + 16 * RN - 1) / (16 * RN), p.splits), 64 * KS, 0, s>>>(p);
 }
 
 // Weight rows a workgroup: the fullest CU reads (16 RN + 16 TT) rows for each workgroup that it gets, and
@@ -486,22 +523,59 @@ void launch_fused(const W8A8Params& p, hipStream_t s) {
 template <int MT, int NT, int WT, int WN, int R>
 void launch_tile(const W8A8Params& p, hipStream_t s) {
     const int tt = (p.T + 32 * MT * WT - 1) / (32 * MT * WT), tn = (p.N + 32 * NT * WN - 1) / (32 * NT * WN);
-    w8a8_tile_kernel<MT, NT, WT, WN, R><<<(uint32_t)(tt * tn), 64 * WT * WN, 0, s>>>(p, tt, tn);
+    w8a8_tile_kernel<MT, NT, WT, WN, R><<<dim3(tt * tn, p.splits), 64 * WT * WN, 0, s>>>(p, tt, tn);
 }
 
 }  // namespace
 
+namespace {
+int64_t tiles_of(int N, int T, int side) { return (int64_t)((T + side - 1) / side) * ((N + side - 1) / side); }
+
+// Tokens of the streaming kernel's form that a call takes, by 16.
+int tokens_of(int T) {
+    const int tt = (T + 15) / 16;
+    return tt <= 4 ? tt : tt <= 6 ? 6 : 8;
+}
+
+// Splits of K over workgroups, where there are few of them for long rows: their sums take a third launch
+// (131 tokens, 315 x 8896: 30 us in one, 15 us in eight).
+void set_splits(W8A8Params& p) {
+    const int pieces = (p.K + 127) / 128;
+    int64_t groups, least;
+    if (p.T <= kRowsMax) {
+        const int rn = rows_of(p.N, tokens_of(p.T));
+        groups = (p.N + 16 * rn - 1) / (16 * rn), least = 16;
+    } else {
+        groups = tiles_of(p.N, p.T, 128) > 160 ? 256 : tiles_of(p.N, p.T, 64), least = 8;
+    }
+    p.splits = 1;
+    p.per = pieces;
+    if (fused(p.K, p.T) || groups >= 128 || pieces < 3 * least) return;
+    const int64_t splits = std::min(256 / groups, pieces / least);
+    p.per = (int)((pieces + splits - 1) / splits + 3) / 4 * 4;
+    p.splits = (pieces + p.per - 1) / p.per;
+}
+
+size_t codes_bytes(int K, int T) { return ((size_t)T * K + 255) / 256 * 256 + ((size_t)T * 4 + 255) / 256 * 256; }
+}  // namespace
+
 size_t w8a8_workspace(int N, int K, int T) {
-    return fused(K, T) ? 0 : ((size_t)T * K + 255) / 256 * 256 + (size_t)T * 4;
+    if (fused(K, T)) return 0;
+    W8A8Params p{};
+    p.N = N, p.K = K, p.T = T;
+    set_splits(p);
+    return codes_bytes(K, T) + (p.splits > 1 ? (size_t)p.splits * T * N * 4 : 0);
 }
 
 hipError_t launch_w8a8(W8A8Params p, void* ws, hipStream_t s) {
     const bool fuse = fused(p.K, p.T);
+    set_splits(p);
     if (!fuse) {
         float* xs = (float*)((char*)ws + ((size_t)p.T * p.K + 255) / 256 * 256);
         int8_t* xq = (int8_t*)ws;
         p.xq = xq;
         p.xs = xs;
+        p.part = (int*)((char*)ws + codes_bytes(p.K, p.T));
         if (p.xt == XT_F32)
             x_code_kernel<XT_F32><<<p.T, 512, 0, s>>>(p.X, p.K, xq, xs);
         else if (p.xt == XT_F16)
@@ -523,12 +597,13 @@ hipError_t launch_w8a8(W8A8Params p, void* ws, hipStream_t s) {
         launch_few<6, 4>(p, s);
     else if (p.T <= kRowsMax)
         launch_few<8, 4>(p, s);
-    else if ((int64_t)((p.T + 255) / 256) * ((p.N + 255) / 256) >= 192)
+    else if (tiles_of(p.N, p.T, 256) >= 192)
         launch_tile<2, 4, 4, 2, 2>(p, s);
-    else if ((int64_t)((p.T + 127) / 128) * ((p.N + 127) / 128) > 160)
+    else if (tiles_of(p.N, p.T, 128) > 160)
         launch_tile<2, 2, 2, 2, 4>(p, s);
     else
         launch_tile<1, 2, 2, 1, 4>(p, s);
+    if (p.splits > 1) w8a8_join_kernel<<<dim3((p.N + 255) / 256, p.T), 256, 0, s>>>(p);
     return hipGetLastError();
 }
 
