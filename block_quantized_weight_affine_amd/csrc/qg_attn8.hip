@@ -86,9 +86,7 @@ __global__ __launch_bounds__(64 * W, W == 4 && rows_registers(XT == XT_F32 ? 2 :
     auto index = [&](int tb, int page) {
         const int blk = (tb >> 4) + g;
         const uint32_t pi = kv8_div((uint32_t)blk, a.c.nb, a.c.magic);
-        const bool ok = (16 * blk < t1) & (16 * blk + 16 > lo_any) & (pi < (uint32_t)a.q.width) &
-                        ((uint32_t)page < (uint32_t)a.c.pages);
-        return ok ? (int)(((uint32_t)page * a.c.heads + h) * a.c.nb + ((uint32_t)blk - pi * (uint32_t)a.c.nb)) : -1;
+        return kv8_index(a.c, h, blk, pi, page, (16 * blk < t1) & (16 * blk + 16 > lo_any) & (pi < (uint32_t)a.q.width));
     };
     uint4 kw[4][NH], vw[NT];
     auto load_k = [&](int bi) {

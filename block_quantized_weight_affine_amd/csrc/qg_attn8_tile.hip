@@ -67,16 +67,17 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && XT != XT_F32 && D <= 128 ? 2 : 
 
     const int lane = threadIdx.x & 63, col = lane & 31, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    // sequences and heads first, so that the workgroups of one K/V head share a die's cache; the last
-    // tiles, which see the most, first
+    // sequences and heads first, so that the workgroups of one K/V head share a die's cache; of each sequence
+    // the last tile, which sees the most, first, so that the workgroups with nothing to do come last
     int b = blockIdx.x;
     const int pairs = a.q.seqs * a.c.heads;
     const int h = b % pairs % a.c.heads, s = b % pairs / a.c.heads;
     b /= pairs;
-    const int split = b % a.splits, tile = a.tiles - 1 - b / a.splits;
+    const int split = b % a.splits;
     const KvSpan sp = kv8_span(a.q, s);
     const int rows = sp.n * a.group;
-    if (tile * BR >= rows) return;
+    const int tile = (rows + BR - 1) / BR - 1 - b / a.splits;
+    if (tile < 0) return;
     const TileRange tr = tile_range(a, sp, tile * BR, BR);
     if (split > 0 && split >= tr.nact) return;
     const int t0 = tr.lo + split * a.chunk, t1 = min(t0 + a.chunk, tr.hi);
@@ -99,9 +100,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && XT != XT_F32 && D <= 128 ? 2 : 
     };
     auto index_of = [&](int blk, int page) {
         const uint32_t pi = kv8_div((uint32_t)blk, a.c.nb, a.c.magic);
-        const bool ok = (16 * blk < t1) & (16 * blk + 16 > lo_any) & (pi < (uint32_t)a.q.width) &
-                        ((uint32_t)page < (uint32_t)a.c.pages);
-        return ok ? (int)(((uint32_t)page * a.c.heads + h) * a.c.nb + ((uint32_t)blk - pi * (uint32_t)a.c.nb)) : -1;
+        return kv8_index(a.c, h, blk, pi, page, (16 * blk < t1) & (16 * blk + 16 > lo_any) & (pi < (uint32_t)a.q.width));
     };
     const int my_blk = (t0 >> 4) + tid;  // plus kInfo a segment
     // the first stages' codes set out before anything waits for their scales

@@ -1,7 +1,7 @@
 // qg_kv8.hpp -- the 8-bit key/value cache: where a token lies, and which tokens a sequence has.
 //
 // Plain C++, shared by the kernels and by host code.  Every index that comes from device memory (block
-// table, row offsets, lengths) passes through kv8_span and kv8_block, which turn what does not fit
+// table, row offsets, lengths) passes through kv8_span and kv8_index, which turn what does not fit
 // into "no rows" and "no block", so no kernel address depends on an unchecked value.
 #pragma once
 
@@ -59,15 +59,19 @@ QG_HD uint32_t kv8_div(uint32_t blk, int nb, uint32_t magic) {
     return nb == 1 ? blk : (uint32_t)(((uint64_t)blk * magic) >> 32);
 }
 
-// Index of token block blk (tokens 16 blk ..) of sequence s and head h, or -1 where the table has no
-// page for it.
+// Index of token block blk (tokens 16 blk ..) of head h in `page`, the table's entry pi = blk / nb, or -1 where
+// that is no page (or `there` is false).
+QG_HD int kv8_index(const KvCache& c, int h, int blk, uint32_t pi, int page, bool there) {
+    const bool ok = there & ((uint32_t)page < (uint32_t)c.pages);
+    return ok ? (int)(((uint32_t)page * c.heads + h) * c.nb + ((uint32_t)blk - pi * (uint32_t)c.nb)) : -1;
+}
+
+// Index of token block blk of sequence s and head h, or -1 where the table has no page for it.
 QG_HD int kv8_block(const KvCache& c, const KvSeqs& q, int s, int h, int blk) {
     if (blk < 0) return -1;
     const uint32_t pi = kv8_div((uint32_t)blk, c.nb, c.magic);
     if (pi >= (uint32_t)q.width) return -1;
-    const int page = q.table[(int64_t)s * q.width + pi];
-    if (page < 0 || page >= c.pages) return -1;
-    return (page * c.heads + h) * c.nb + (int)((uint32_t)blk - pi * (uint32_t)c.nb);
+    return kv8_index(c, h, blk, pi, q.table[(int64_t)s * q.width + pi], true);
 }
 
 QG_HD KvCache kv8_cache_of(int8_t* kc, float* ks, int8_t* vc, float* vs, int pages, int page, int heads, int dim) {
