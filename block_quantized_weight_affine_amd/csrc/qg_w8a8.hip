@@ -116,11 +116,11 @@ __device__ __forceinline__ void store_any(void* Y, int yt, int64_t i, float v) {
 // pieces of both operands straight into its own part of shared memory, AHEAD of them on their way, 8 rows
 // of whole 128-byte lines a copy: loads into registers in the operands' layout (16 rows of 64 bytes) are
 // bound by the lines that a load touches.  A row's 16-byte chunks lie at slot chunk ^ (row / 2 % 8), so
-// that reads meet all banks.  CODES > 0 (at most 8 tokens): every workgroup codes X itself into CODES bytes of
+// that reads meet all banks.  CODES > 0 (few codes): every workgroup codes X itself into CODES bytes of
 // shared memory while its first weights are on their way, which saves a launch.
 // Bound by memory: one token 4096 x 4096 5.5 us (3.0 TB/s of 16.8 MB), 45
 // tokens 11009 x 4112 13 us after the 2.4-4 us in which X is coded (3.5 TB/s).
-constexpr int kFusedLds = 64 << 10, kFusedSmall = 16 << 10;  // bytes of X codes a workgroup keeps
+constexpr int kFusedCodes = 32768, kFusedLds = 34 << 10;  // X codes a workgroup keeps (fewer than), bytes with pitches
 
 __host__ __device__ __forceinline__ int fused_pitch(int K) { return (K + 127) / 128 * 128 + 16; }
 
@@ -197,9 +197,18 @@ __global__ __launch_bounds__(64 * KS) void w8a8_rows_kernel(W8A8Params p) {
     const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc((void*)(p.w + (int64_t)n0 * K), 0,
                                                                         min(16 * RN, p.N - n0) * K, 0x00020000);
     const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc((void*)p.xq, 0, FUSED ? 0 : p.T * K, 0x00020000);
+    // The sums are integers, so each workgroup begins at a piece of its own: begun together at the rows'
+    // starts, workgroups meet on the same memory channels where K is a power of two (16 tokens 8192 x 8192:
+    // 21.9 us so, 16.3 us with pieces 5 apart).
+    const int count = units - lo, first = (int)(5 * blockIdx.x % (unsigned)max(count, 1));
+    auto piece = [&](int u) {
+        const int v = u + first;
+        return u >= units ? 0x400000 : v >= units ? v - count : v;
+    };
     // copy i has rows 8 i .. 8 i + 7
     const int even = 16 * ((lane & 7) ^ (lane >> 4)), odd = even ^ 64, from = (lane >> 3) * K;
-    auto copy = [&](int8_t* s, int u) {
+    auto copy = [&](int8_t* s, int nth) {
+        const int u = piece(nth);
         const int at[2] = {128 * u + even < end ? from + even + 128 * u : 0x40000000,
                            128 * u + odd < end ? from + odd + 128 * u : 0x40000000};
         int8_t* to = s + wave * kPiece;
@@ -211,7 +220,8 @@ __global__ __launch_bounds__(64 * KS) void w8a8_rows_kernel(W8A8Params p) {
         }
     };
     i32x4_t acc[RN][TT] = {};
-    auto multiply = [&](const int8_t* s, int u) {
+    auto multiply = [&](const int8_t* s, int nth) {
+        const int u = piece(nth);
         const int8_t* at = s + wave * kPiece + r * 128;
 #pragma unroll
         for (int h = 0; h < 2; h++) {
@@ -480,7 +490,16 @@ __global__ __launch_bounds__(256) void w8a8_join_kernel(W8A8Params p) {
 }
 
 constexpr int kRowsMax = 128;  // tokens of the streaming kernel
-bool fused(int K, int T) { return T <= 8 && T * fused_pitch(K) <= kFusedLds; }
+// Coding X in every workgroup saves a launch (2.5 us) but is paid again by every workgroup that a CU gets and
+// grows with X.  One launch and two, us: 4096 x 4096, 1, 4, 8 tokens 6.3, 7.3, 8.6 and 7.9, 8.1, 8.0; 2048 x 8192,
+// 1, 4 tokens 6.9, 9.0 and 8.0, 8.2; 4096 x 14336, 1, 2, 4 tokens 12.5, 14.2, 16.2 and 14.0, 15.3, 14.0; with two
+// row blocks a workgroup 8192 x 2048, 1, 4 tokens 6.1, 6.8 and 8.1, 8.2; 8192 x 4096, 1, 2, 4, 8 tokens 8.5, 9.1,
+// 10.1, 12.2 and 9.8; past that it loses: 20000 x 2048, 1, 8 tokens 14.2, 18.7 and 12.3, 12.8.
+constexpr int kFusedRows = 4096;
+bool fused(int N, int K, int T) {
+    return T <= 8 && N <= 2 * kFusedRows && (int64_t)T * K * (N <= kFusedRows ? 1 : 2) < kFusedCodes;
+}
+static_assert(kFusedCodes + 8 * (127 + 16) <= kFusedLds, "codes");
 
 template <int TT, int RN, int KS, int CODES>
 void launch_rows(const W8A8Params& p, hipStream_t s) {
@@ -509,15 +528,6 @@ void launch_few(const W8A8Params& p, hipStream_t s) {
         case 3: return launch_rows<TT, 3, KS, 0>(p, s);
         default: return launch_rows<TT, 4, KS, 0>(p, s);
     }
-}
-
-// One launch: X's codes in the least shared memory that holds them, so that CUs hold several workgroups.
-template <int KS>
-void launch_fused(const W8A8Params& p, hipStream_t s) {
-    if (p.T * fused_pitch(p.K) <= kFusedSmall)
-        launch_rows<1, 1, KS, kFusedSmall>(p, s);
-    else
-        launch_rows<1, 1, KS, kFusedLds>(p, s);
 }
 
 template <int MT, int NT, int WT, int WN, int R>
@@ -550,7 +560,7 @@ void set_splits(W8A8Params& p) {
     }
     p.splits = 1;
     p.per = pieces;
-    if (fused(p.K, p.T) || groups >= 128 || pieces < 3 * least) return;
+    if (fused(p.N, p.K, p.T) || groups >= 128 || pieces < 3 * least) return;
     const int64_t splits = std::min(256 / groups, pieces / least);
     p.per = (int)((pieces + splits - 1) / splits + 3) / 4 * 4;
     p.splits = (pieces + p.per - 1) / p.per;
@@ -560,7 +570,7 @@ size_t codes_bytes(int K, int T) { return ((size_t)T * K + 255) / 256 * 256 + ((
 }  // namespace
 
 size_t w8a8_workspace(int N, int K, int T) {
-    if (fused(K, T)) return 0;
+    if (fused(N, K, T)) return 0;
     W8A8Params p{};
     p.N = N, p.K = K, p.T = T;
     set_splits(p);
@@ -568,7 +578,7 @@ size_t w8a8_workspace(int N, int K, int T) {
 }
 
 hipError_t launch_w8a8(W8A8Params p, void* ws, hipStream_t s) {
-    const bool fuse = fused(p.K, p.T);
+    const bool fuse = fused(p.N, p.K, p.T);
     set_splits(p);
     if (!fuse) {
         float* xs = (float*)((char*)ws + ((size_t)p.T * p.K + 255) / 256 * 256);
@@ -584,7 +594,7 @@ hipError_t launch_w8a8(W8A8Params p, void* ws, hipStream_t s) {
             x_code_kernel<XT_BF16><<<p.T, 512, 0, s>>>(p.X, p.K, xq, xs);
     }
     if (fuse)
-        p.N <= 8192 ? launch_fused<16>(p, s) : launch_fused<4>(p, s);
+        p.N <= kFusedRows ? launch_rows<1, 1, 16, kFusedLds>(p, s) : launch_rows<1, 2, 8, kFusedLds>(p, s);
     else if (p.T <= 16)
         launch_few<1, 8>(p, s);
     else if (p.T <= 32)

@@ -101,6 +101,9 @@ def test_tiles_of_both_heights(dim, xt, seqs):
 SIZES = [(t, n, k) for t in (1, 2, 3, 5, 8, 9) for n, k in ((8200, 144), (33, 8208))]
 SIZES += [(t, n, k) for t in (16, 17, 32, 33, 48, 49, 64, 65, 96, 97, 128, 129) for n, k in ((100, 2064), (12305, 272))]
 SIZES += [(1, 48, 32784), (20, 70, 65536), (129, 65, 32784), (1500, 2001, 400), (3000, 4200, 272)]
+# X coded in the product's launch or before it: N at one and two row blocks a workgroup, T K at the limit
+SIZES += [(8, 4096, 4080), (8, 4096, 4096), (7, 4097, 2320), (7, 4097, 2352), (1, 8192, 16368), (1, 8193, 16384)]
+SIZES += [(1, 4081, 32752), (2, 6000, 8176), (3, 8192, 16)]
 
 
 @pytest.mark.parametrize("i", range(len(SIZES)))
