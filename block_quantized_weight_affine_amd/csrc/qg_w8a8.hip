@@ -489,7 +489,10 @@ __global__ __launch_bounds__(256) void w8a8_join_kernel(W8A8Params p) {
     store_any(p.Y, p.yt, at, (float)sum * p.xs[t] * p.ws[n]);
 }
 
-constexpr int kRowsMax = 128;  // tokens of the streaming kernel
+// The streaming kernel and the tiles, us: 72, 96 tokens 11000 x 4112 21.8, 23.5 and 24.5, 24.3, 14336 x 4096 25.6,
+// 27.2 and 21.3, 22.5, 28672 x 8192 77, 80 and 63, 65; 128 tokens 4096 x 14336 39 and 44-47, 6144 x 4096 20.8 and
+// 16.1, 20000 x 2048 35 and 21.
+bool streams(int N, int T) { return T <= 64 || (T <= 96 && N <= 12288) || (T <= 128 && N <= 5120); }
 // Coding X in every workgroup saves a launch (2.5 us) but is paid again by every workgroup that a CU gets and
 // grows with X.  One launch and two, us: 4096 x 4096, 1, 4, 8 tokens 6.3, 7.3, 8.6 and 7.9, 8.1, 8.0; 2048 x 8192,
 // 1, 4 tokens 6.9, 9.0 and 8.0, 8.2; 4096 x 14336, 1, 2, 4 tokens 12.5, 14.2, 16.2 and 14.0, 15.3, 14.0; with two
@@ -541,6 +544,14 @@ void launch_tile(const W8A8Params& p, hipStream_t s) {
 namespace {
 int64_t tiles_of(int N, int T, int side) { return (int64_t)((T + side - 1) / side) * ((N + side - 1) / side); }
 
+// Tiles of 256 a side: a CU takes one in the time of 4/3 of two tiles of 128 (768 tokens 14336 x 4096: 62 and 77
+// us; 1024 tokens 8192 x 8192: 106 and 84 us).  Tiles of 128: a CU holds two of them with two stages each, or one
+// with four, which is the faster where there are no more than CUs (384 tokens 14336 x 4096: 42 and 55 us; 256
+// tokens: 37 and 31 us).
+bool large_tiles(int N, int T) {
+    return 4 * ((tiles_of(N, T, 256) + 255) / 256) < 3 * ((tiles_of(N, T, 128) + 511) / 512);
+}
+
 // Tokens of the streaming kernel's form that a call takes, by 16.
 int tokens_of(int T) {
     const int tt = (T + 15) / 16;
@@ -552,7 +563,7 @@ int tokens_of(int T) {
 void set_splits(W8A8Params& p) {
     const int pieces = (p.K + 127) / 128;
     int64_t groups, least;
-    if (p.T <= kRowsMax) {
+    if (streams(p.N, p.T)) {
         const int rn = rows_of(p.N, tokens_of(p.T));
         groups = (p.N + 16 * rn - 1) / (16 * rn), least = 16;
     } else {
@@ -603,12 +614,12 @@ hipError_t launch_w8a8(W8A8Params p, void* ws, hipStream_t s) {
         launch_few<3, 4>(p, s);
     else if (p.T <= 64)
         launch_few<4, 4>(p, s);
-    else if (p.T <= 96)
-        launch_few<6, 4>(p, s);
-    else if (p.T <= kRowsMax)
-        launch_few<8, 4>(p, s);
-    else if (tiles_of(p.N, p.T, 256) >= 192)
+    else if (streams(p.N, p.T))
+        p.T <= 96 ? launch_few<6, 4>(p, s) : launch_few<8, 4>(p, s);
+    else if (large_tiles(p.N, p.T))
         launch_tile<2, 4, 4, 2, 2>(p, s);
+    else if (tiles_of(p.N, p.T, 128) > 256)
+        launch_tile<2, 2, 2, 2, 2>(p, s);
     else if (tiles_of(p.N, p.T, 128) > 160)
         launch_tile<2, 2, 2, 2, 4>(p, s);
     else

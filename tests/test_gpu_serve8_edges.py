@@ -104,6 +104,9 @@ SIZES += [(1, 48, 32784), (20, 70, 65536), (129, 65, 32784), (1500, 2001, 400), 
 # X coded in the product's launch or before it: N at one and two row blocks a workgroup, T K at the limit
 SIZES += [(8, 4096, 4080), (8, 4096, 4096), (7, 4097, 2320), (7, 4097, 2352), (1, 8192, 16368), (1, 8193, 16384)]
 SIZES += [(1, 4081, 32752), (2, 6000, 8176), (3, 8192, 16)]
+# the streaming kernel and the tiles, and the tiles' forms, at both sides of their limits
+SIZES += [(65, 12288, 144), (96, 12289, 144), (97, 5120, 272), (128, 5121, 272), (100, 700, 16400)]
+SIZES += [(256, 16384, 272), (257, 16400, 272), (640, 13200, 144), (700, 14100, 144)]
 
 
 @pytest.mark.parametrize("i", range(len(SIZES)))
