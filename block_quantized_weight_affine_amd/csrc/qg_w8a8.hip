@@ -559,19 +559,22 @@ int tokens_of(int T) {
 }
 
 // Splits of K over workgroups, where there are few of them for long rows: their sums take a third launch
-// (131 tokens, 315 x 8896: 30 us in one, 15 us in eight).
+// (131 tokens, 315 x 8896: 30 us in one, 15 us in eight), which few tokens do not repay (1024 x 8192, 16, 32, 64,
+// 96 tokens 8.5, 10.2, 12.8, 15.6 us in one, 10.4, 10.5, 11.5, 12.9 us in four; 2048 x 8192, 32, 64, 128 tokens
+// 10.4, 12.9, 19.7 us in one, 11.1, 12.5, 16.7 us in two).
 void set_splits(W8A8Params& p) {
     const int pieces = (p.K + 127) / 128;
     int64_t groups, least;
     if (streams(p.N, p.T)) {
-        const int rn = rows_of(p.N, tokens_of(p.T));
+        const int tt = tokens_of(p.T), rn = rows_of(p.N, tt);
         groups = (p.N + 16 * rn - 1) / (16 * rn), least = 16;
+        if (pieces * (rn + tt) < 256) groups = 256;
     } else {
         groups = tiles_of(p.N, p.T, 128) > 160 ? 256 : tiles_of(p.N, p.T, 64), least = 8;
     }
     p.splits = 1;
     p.per = pieces;
-    if (fused(p.N, p.K, p.T) || groups >= 128 || pieces < 3 * least) return;
+    if (fused(p.N, p.K, p.T) || groups > 128 || pieces < 3 * least) return;
     const int64_t splits = std::min(256 / groups, pieces / least);
     p.per = (int)((pieces + splits - 1) / splits + 3) / 4 * 4;
     p.splits = (pieces + p.per - 1) / p.per;

@@ -107,6 +107,7 @@ SIZES += [(1, 4081, 32752), (2, 6000, 8176), (3, 8192, 16)]
 # the streaming kernel and the tiles, and the tiles' forms, at both sides of their limits
 SIZES += [(65, 12288, 144), (96, 12289, 144), (97, 5120, 272), (128, 5121, 272), (100, 700, 16400)]
 SIZES += [(256, 16384, 272), (257, 16400, 272), (640, 13200, 144), (700, 14100, 144)]
+SIZES += [(9, 300, 8208), (64, 2048, 8208), (256, 2048, 6160)]       # K in one and in several splits
 
 
 @pytest.mark.parametrize("i", range(len(SIZES)))
