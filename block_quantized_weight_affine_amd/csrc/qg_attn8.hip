@@ -6,6 +6,9 @@
 // instructions with f32 sums: q enters as f16 after an exact power of two per row (f32 q as two such
 // f16 pieces), the weights as f16 after the block's V scale.  Nothing of the cache is decoded into
 // memory.
+#include <algorithm>
+#include <cmath>
+
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -429,7 +432,7 @@ namespace {
 // 124 rows 98 and 45; 2 sequences 48 rows 13.5 and 18.6, 96 rows 19.4 and 20.2.  Over 20000, f16, dim 64, 2
 // sequences 96 rows 46 and 32; over 8000, f32, dim 128, 4 sequences 48 rows 44 and 44, 96 rows 70 and 47.
 constexpr int64_t kTileFrom = 64;
-// Tokens a split at least, and tokens that are not split where the heads are few: 1024 of 8 heads of 128 take
+// Tokens a split at least, and tokens that are not split however few the heads are: 1024 of 8 heads of 128 take
 // 9.4 us in one launch; 5.8 and 3.8 us in two.
 constexpr int64_t kMinChunk = 256, kAlone = 1024;
 void set_tiles(AttnParams& a, int xt) {
@@ -437,10 +440,15 @@ void set_tiles(AttnParams& a, int xt) {
     a.tile_rows = rows >= kTileFrom ? attn8_tile_rows(a, xt) : 16;
     a.tiles = (int)((rows + a.tile_rows - 1) / a.tile_rows);
 }
-// Splits of `span` tokens.  Rows kernel: enough to fill the card (a CU holds 2 or 3 of its workgroups, or
-// one of the larger ones), and of the longest sequence always a few, so that sequences of different lengths
-// even out; one where 8 wavefronts are through sooner than a second kernel would join.  Tile kernel: a stage of 64 tokens takes about 24 times as long as a tile's part in writing
-// and joining the sums of one more split, so at most sqrt(24 stages / workgroups); none once the card is full.
+// Splits of `span` tokens.  Rows kernel: one where the workgroups that there are take no longer than a second
+// kernel would (bf16, dim 128, sequences x heads: 128 of 2048 tokens 15.8 us in one launch, 20.8 us in eight splits,
+// of 8192 62.4 and 61.1 us; 216 of 1024 13.5 and 19.3 us; 512 of 4096 98 and 109 us, of lengths up to that 62 and
+// 65 us), but of no more than 4096 tokens, as one long sequence among short ones has its heads' workgroups alone.
+// Otherwise, of few heads the splits that fill all CUs evenly, the fewest such (8 of 200000 tokens: 32 splits 82 us,
+// 64 86 us, 128 92 us), of more some 1024 workgroups and always a few splits, so that sequences of different
+// lengths even out (128 of up to 32768 tokens: 8 splits 108 us, 6 splits 123 us; all of 32768: 203 and 196 us).
+// Tile kernel: a stage of 64 tokens takes about 24 times as long as a tile's part in writing and joining the sums of
+// one more split, so at most sqrt(24 stages / workgroups); none once the card is full.
 int64_t wanted_splits(const AttnParams& a, int xt, int64_t span) {
     const int64_t base = (int64_t)a.q.seqs * a.c.heads * a.tiles;
     if (a.tile_rows > 16) {
@@ -449,8 +457,15 @@ int64_t wanted_splits(const AttnParams& a, int xt, int64_t span) {
         return k;
     }
     if (rows_late(xt == XT_F32 ? 2 : 1, a.c.dim)) return std::max((256 + base - 1) / base, (int64_t)3);
-    if (span <= kAlone && base <= 128) return 1;
-    return std::max((1024 + base - 1) / base, (int64_t)6);
+    if (span <= std::clamp(16 * base, kAlone, 4 * kAlone)) return 1;
+    if (base >= 32) return std::max((1024 + base - 1) / base, (int64_t)6);
+    int64_t best = 0;
+    double least = 0;
+    for (int64_t k = 256 / base; k <= 1024 / base; k++) {
+        const double turns = k * base / 256.0, cost = std::ceil(turns) / turns + 0.03 * turns;
+        if (!best || cost < least) best = k, least = cost;
+    }
+    return best;
 }
 }  // namespace
 
@@ -474,7 +489,11 @@ void attn8_plan(AttnParams& a, int xt) {
     if (a.causal && a.window > 0 && seen < span) span = seen;
     const int64_t want = wanted_splits(a, xt, span);
     int64_t chunk = (span + want - 1) / want;
-    a.row_waves = rows_late(xt == XT_F32 ? 2 : 1, a.c.dim) || (want == 1 && a.tile_rows == 16) ? 8 : 4;
+    // 8 wavefronts a workgroup where its registers let a CU hold one, or there are few (320 workgroups of one
+    // launch, dim 192, 2048 tokens: 62 us, with 4 59 us; 4096 of different lengths: 69 and 83 us)
+    const int64_t groups = want * a.q.seqs * a.c.heads * a.tiles;
+    const bool wide = a.tile_rows == 16 && (want == 1 ? groups < 512 : groups <= 256 && chunk >= 1024);
+    a.row_waves = rows_late(xt == XT_F32 ? 2 : 1, a.c.dim) || wide ? 8 : 4;
     const int64_t unit = a.tile_rows > 16 ? 64 : 64 * a.row_waves;
     if (chunk < kMinChunk) chunk = kMinChunk;
     a.chunk = (int)((chunk + unit - 1) / unit * unit);

@@ -97,6 +97,22 @@ def test_tiles_of_both_heights(dim, xt, seqs):
     _check_attend(b, q, xt, 16, dim ** -0.5, True, 0, got)
 
 
+# one launch and several splits of few and of many heads, 4 and 8 wavefronts: (sequences, longest)
+@pytest.mark.parametrize("seqs,longest", [(33, 2112), (33, 2113), (64, 4096), (64, 4097), (129, 300), (129, 4100),
+                                          (1, 40001), (7, 40001), (8, 17000)])
+@pytest.mark.parametrize("dim,xt", [(64, "f16"), (96, "f32")])
+def test_one_token_of_one_long_sequence(seqs, longest, dim, xt):
+    """The longest stands among short ones: what the host plans by it holds for all of them."""
+    print(f"steps seqs={seqs} longest={longest} dim={dim} {xt}", flush=True)
+    rng = np.random.default_rng(seqs + longest)
+    lens = [(1, int(n)) for n in rng.integers(1, 40, seqs)]
+    lens[seqs // 2] = (1, longest)
+    b = Batch(lens, 4, dim, 64, 31).upload()
+    q = _values(b.rng, (b.T, 8, dim), xt).cuda()
+    got = _attend(b, q, 8, dim ** -0.5, True, 0)
+    _check_attend(b, q, xt, 8, dim ** -0.5, True, 0, got)
+
+
 # T at both sides of every change of kernel; N over one, several and many workgroups; K past a ring's pieces
 SIZES = [(t, n, k) for t in (1, 2, 3, 5, 8, 9) for n, k in ((8200, 144), (33, 8208))]
 SIZES += [(t, n, k) for t in (16, 17, 32, 33, 48, 49, 64, 65, 96, 97, 128, 129) for n, k in ((100, 2064), (12305, 272))]
