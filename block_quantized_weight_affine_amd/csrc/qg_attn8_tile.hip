@@ -48,7 +48,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // 293 us, 0.94 PFLOP/s (a product of 8192^3 in f16: 1.46).  A stage of 256 rows takes 3550 cycles, 2048 of
 // them products and about 2300 vector instructions of two wavefronts a SIMD; the clock falls to 1.8 GHz from
 // the 2.4 GHz that the same kernel has on zeros.  A workgroup's start (lengths, table, scales, first codes)
-// takes 6.4 us, its end 2 us.  Measured against it: 64 rows a wavefront and one wavefront a SIMD 25 % slower
+// takes 5-6 us, its end 2 us.  Measured against it: 64 rows a wavefront and one wavefront a SIMD 25 % slower
 // a stage (one wavefront issues an instruction every 6.5 cycles), 32-token stages 10 %, half of the
 // wavefronts half a stage behind the others the same.
 template <int XT, int D, int NW, int CT>
