@@ -447,6 +447,9 @@ void set_tiles(AttnParams& a, int xt) {
 // Otherwise, of few heads the splits that fill all CUs evenly, the fewest such (8 of 200000 tokens: 32 splits 82 us,
 // 64 86 us, 128 92 us), of more some 1024 workgroups and always a few splits, so that sequences of different
 // lengths even out (128 of up to 32768 tokens: 8 splits 108 us, 6 splits 123 us; all of 32768: 203 and 196 us).
+// Where the registers leave room for one workgroup a CU, no more than the CUs in a turn (f32, dim 256: 24 of 32768
+// tokens 8 splits 72 us, 11 splits 97 us; 96 of 32768 5 splits 247 us, 3 splits 350 us, of lengths up to that 119 and
+// 167 us; 256 of 3000 one launch 77 us, 3 splits 92 us).
 // Tile kernel: a stage of 64 tokens takes about 24 times as long as a tile's part in writing and joining the sums of
 // one more split, so at most sqrt(24 stages / workgroups); none once the card is full.
 int64_t wanted_splits(const AttnParams& a, int xt, int64_t span) {
@@ -456,7 +459,10 @@ int64_t wanted_splits(const AttnParams& a, int xt, int64_t span) {
         while ((k + 1) * base <= 256 && (k + 1) * (k + 1) * base <= 24 * (span / 64)) k++;
         return k;
     }
-    if (rows_late(xt == XT_F32 ? 2 : 1, a.c.dim)) return std::max((256 + base - 1) / base, (int64_t)3);
+    if (rows_late(xt == XT_F32 ? 2 : 1, a.c.dim)) {
+        if (base >= 192 && span <= std::min(16 * base, 4 * kAlone)) return 1;
+        return base <= 85 ? 256 / base : base <= 102 ? 512 / base : 3;
+    }
     if (span <= std::clamp(16 * base, kAlone, 4 * kAlone)) return 1;
     if (base >= 32) return std::max((1024 + base - 1) / base, (int64_t)6);
     int64_t best = 0;

@@ -99,8 +99,9 @@ def test_tiles_of_both_heights(dim, xt, seqs):
 
 # one launch and several splits of few and of many heads, 4 and 8 wavefronts: (sequences, longest)
 @pytest.mark.parametrize("seqs,longest", [(33, 2112), (33, 2113), (64, 4096), (64, 4097), (129, 300), (129, 4100),
-                                          (1, 40001), (7, 40001), (8, 17000)])
-@pytest.mark.parametrize("dim,xt", [(64, "f16"), (96, "f32")])
+                                          (1, 40001), (7, 40001), (8, 17000), (12, 9000), (25, 9000), (47, 3000),
+                                          (48, 3071), (48, 3073)])
+@pytest.mark.parametrize("dim,xt", [(64, "f16"), (96, "f32"), (256, "f32")])
 def test_one_token_of_one_long_sequence(seqs, longest, dim, xt):
     """The longest stands among short ones: what the host plans by it holds for all of them."""
     print(f"steps seqs={seqs} longest={longest} dim={dim} {xt}", flush=True)
