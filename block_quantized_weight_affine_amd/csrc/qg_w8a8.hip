@@ -199,11 +199,13 @@ __global__ __launch_bounds__(64 * KS) void w8a8_rows_kernel(W8A8Params p) {
     const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc((void*)p.xq, 0, FUSED ? 0 : p.T * K, 0x00020000);
     // The sums are integers, so each workgroup begins at a piece of its own: begun together at the rows'
     // starts, workgroups meet on the same memory channels where K is a power of two (16 tokens 8192 x 8192:
-    // 21.9 us so, 16.3 us with pieces 5 apart).
-    const int count = units - lo, first = (int)(5 * blockIdx.x % (unsigned)max(count, 1));
+    // 21.9 us so, 16.3 us with pieces 5 apart; one token, coded here, 8192 x 4096 10.2 and 8.6 us).  The least form, one
+    // workgroup a CU, has more of beginning at once (one token 4096 x 1024 4.5 us so, 4.8 us with pieces apart).
+    constexpr bool kApart = !FUSED || RN > 1;
+    const int count = units - lo, first = kApart ? (int)(5 * blockIdx.x % (unsigned)max(count, 1)) : 0;
     auto piece = [&](int u) {
         const int v = u + first;
-        return u >= units ? 0x400000 : v >= units ? v - count : v;
+        return !kApart ? u : u >= units ? 0x400000 : v >= units ? v - count : v;
     };
     // copy i has rows 8 i .. 8 i + 7
     const int even = 16 * ((lane & 7) ^ (lane >> 4)), odd = even ^ 64, from = (lane >> 3) * K;
