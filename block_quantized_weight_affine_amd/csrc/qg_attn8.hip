@@ -176,7 +176,7 @@ __global__ __launch_bounds__(64 * W, W == 4 && rows_registers(XT == XT_F32 ? 2 :
             }
         }
         const int was = bi;
-        const float vnow = vs, kf = vs - vs == 0.f ? ks * qs : __builtin_nanf("");
+        const float vnow = vs, kf = finite_scales(ks, vs) ? ks * qs : __builtin_nanf("");
         const bool more = tb + 64 * W < t1;
         if (kLate) {
             __builtin_amdgcn_sched_barrier(0);

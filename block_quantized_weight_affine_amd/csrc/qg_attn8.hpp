@@ -60,6 +60,9 @@ __device__ __forceinline__ half8_t codes8_f16(uint32_t w0, uint32_t w1, half2_t 
     r[2] = a, r[3] = b;
     return __builtin_bit_cast(half8_t, r);
 }
+// Both scales of a block are finite.  Else its scores become NaN: an infinite K scale by itself would score tokens
+// of negative products -inf, as if they were hidden.
+__device__ __forceinline__ bool finite_scales(float ks, float vs) { return (ks - ks) + (vs - vs) == 0.f; }
 // The factor of a block's V codes: the V scale's sign.
 __device__ __forceinline__ uint32_t v_sign(float vs) { return vs == 0.f ? 0u : vs < 0.f ? 0xbc00bc00u : 0x3c003c00u; }
 // log2(|vs| 2^-e0), 0 where the scale is 0 (its codes count as 0) or not finite (its K scale becomes NaN).

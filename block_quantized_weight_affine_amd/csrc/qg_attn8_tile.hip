@@ -91,8 +91,8 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && XT != XT_F32 && D <= 128 ? 2 : 
 
     // What the kernel has to know of each block, looked up by a thread each for 64 stages at a time: its
     // index (-1: hidden from all), the K scale, and the V scale relative to 2^e0 as a power of two, its
-    // reciprocal and its sign.  A NaN or infinite V scale becomes a K scale of NaN: rows that see the
-    // block are NaN, others whole.
+    // reciprocal and its sign.  A NaN or infinite scale, K's or V's, becomes a K scale of NaN: rows that see
+    // the block are NaN, others whole.
     const int tid = threadIdx.x;
     auto page_of = [&](int blk) {
         const uint32_t pi = kv8_div((uint32_t)blk, a.c.nb, a.c.magic);
@@ -138,7 +138,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && XT != XT_F32 && D <= 128 ? 2 : 
         const int x = (kInfo * seg + tid) & (2 * kInfo - 1);
         const float lv = v_power(vs, e0);
         in_bi[x] = bi;
-        in_ks[x] = bi < 0 ? -1.f : vs - vs == 0.f ? ks : __builtin_nanf("");
+        in_ks[x] = bi < 0 ? -1.f : finite_scales(ks, vs) ? ks : __builtin_nanf("");
         in_lv[x] = lv;
         in_rv[x] = __builtin_amdgcn_exp2f(-lv);
         in_sg[x] = v_sign(vs);

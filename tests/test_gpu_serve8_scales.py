@@ -1,0 +1,89 @@
+"""Attention over the 8-bit cache where scales are extreme: each row keeps the precision of what it sees itself.
+
+Tolerance, per element, with u = 2^-24, n tokens and half-steps h as in test_gpu_serve8.py:
+  scores, weights' rounding, sums, output: 2 ds mean + (2^-11 or 2^-22) mean + 2 (n + 16) u mean + h |o| as there, all
+      of the row's own weighted mean of |v|;
+  weights under f16's range: an error of 2^-25 where the largest weight times its V scale stands at 2^9 or above, so
+      n 2^-34 127 peak with peak the row's largest (weight / sum of weights) * |V scale|;
+  results under the type's smallest normal value: half its smallest step."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import serve8
+from test_gpu_serve8 import HALF, TYPES, Batch, _attend, _values
+
+pytestmark = pytest.mark.gpu
+
+
+def _reference(b, q, scale, causal, window):
+    """o, mean, reach and peak of every row and head in f64 (NaN where a row sees a scale that is not finite)."""
+    T, QH, D = q.shape
+    G = QH // b.H
+    o, mean, reach, peak = (np.full(s, np.nan) for s in (q.shape, q.shape, (T, QH, 1), (T, QH, 1)))
+    for s, (r0, n, total) in enumerate(b.spans()):
+        if not n:
+            continue
+        j = np.arange(total)
+        page, off = b.table[s][j // b.page], j % b.page
+        for h in range(b.H):
+            kd, vd = (x[page, h, off // 16].astype(np.float64) for x in (b.ks, b.vs))
+            with np.errstate(invalid="ignore"):
+                k = b.kc[page, h, off].astype(np.float64) * kd[:, None]
+                v = b.vc[page, h, off].astype(np.float64) * vd[:, None]
+            for i in range(n):
+                pos = total - n + i
+                seen = (j <= pos if causal else j >= 0) & (j > pos - window if window else j >= 0)
+                if not (np.isfinite(kd[seen]).all() and np.isfinite(vd[seen]).all()):
+                    continue
+                x = q[r0 + i, h * G:(h + 1) * G].T
+                sc = (k[seen] @ x) * scale
+                w = np.exp(sc - sc.max(0))
+                w /= w.sum(0)
+                at = (r0 + i, slice(h * G, (h + 1) * G))
+                o[at] = w.T @ v[seen]
+                mean[at] = w.T @ np.abs(v[seen])
+                reach[at] = abs(scale) * (np.abs(k[seen]) @ np.abs(x)).max(0)[:, None]
+                peak[at] = (w * np.abs(vd[seen])[:, None]).max(0)[:, None]
+    return o, mean, reach, peak
+
+
+def _check(b, q, xt, scale, causal, window, got, rows=None):
+    """Compares rows (of T; all that the reference gives) and returns them."""
+    o, mean, reach, peak = _reference(b, q.double().cpu().numpy(), scale, causal, window)
+    u, n, D = 2.0 ** -24, b.max_kv, b.D
+    two = xt == "f32"
+    ds = ((D + 10) * u + (2.0 ** -22 if two else 0)) * reach + 2.0 ** -22
+    step = torch.finfo(TYPES[xt]).smallest_normal * torch.finfo(TYPES[xt]).eps / 2
+    tol = 2 * ds * mean + (2.0 ** -22 if two else 2.0 ** -11) * mean + n * 2.0 ** -34 * 127 * peak + \
+        2 * (n + 16) * u * mean + HALF[xt] * np.abs(o) + step
+    if rows is None:
+        rows = ~np.isnan(o).any((1, 2))
+    assert rows.any()
+    err = np.abs(got.double().cpu().numpy() - o)[rows]
+    print(f"worst error / tolerance {np.max(np.nan_to_num(err, nan=np.inf) / tol[rows]):.3f}", flush=True)
+    bad = ~(err <= tol[rows])
+    assert not bad.any(), (np.argwhere(bad)[:5], err[bad][:5], tol[rows][bad][:5], o[rows][bad][:5])
+    return rows
+
+
+@pytest.mark.parametrize("new", [5, 40, 150])
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("value", [np.inf, -np.inf])
+@pytest.mark.parametrize("xt", ["f16", "f32"])
+def test_an_infinite_scale_makes_rows_nan(new, which, value, xt):
+    """The block of the last tokens has an infinite scale; its codes and q give products of one sign, so that every
+    score is -inf for one sign of a K scale."""
+    print(f"infinite {which} {value} new={new} {xt}", flush=True)
+    for codes in (1, -1):
+        b = Batch([(new, 333)], 1, 128, 32, 41)
+        q = _values(b.rng, (b.T, 4, 128), xt).abs().cuda()
+        p, off = serve8.place(b.table, 32, b.P, 0, 320)
+        b.kc[p, :, off:off + 16] = codes * (np.abs(b.kc[p, :, off:off + 16]) | 1)
+        (b.ks if which == "k" else b.vs)[p, :, off // 16] = value
+        got = _attend(b.upload(), q, 4, 0.09, True, 0)
+        before = max(0, new - 13)
+        assert torch.all(torch.isnan(got[before:]))
+        if before:
+            rows = _check(b, q, xt, 0.09, True, 0, got)
+            assert np.array_equal(rows, np.arange(b.T) < before)
