@@ -57,6 +57,7 @@ __global__ __launch_bounds__(64 * W, W == 4 && rows_registers(XT == XT_F32 ? 2 :
     constexpr bool kLate = rows_late(NP, D);
     __shared__ float sh_o[W][16][DH + 4];
     __shared__ float sh_m[W][16], sh_l[W][16];
+    __shared__ float2 sh_all[16];
 
     const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -252,16 +253,22 @@ __global__ __launch_bounds__(64 * W, W == 4 && rows_registers(XT == XT_F32 ? 2 :
         sh_l[wave][col] = l;
     }
     __syncthreads();
-    float mt = kNegInf;
+    // each wavefront's sums as its share of the split's mean: no larger than the values, which may lie anywhere in
+    // f32's range
+    float mt = kNegInf, lt = 0.f;
 #pragma unroll
     for (int w = 0; w < W; w++) mt = fmaxf(mt, sh_m[w][col]);
-    const float f = m == kNegInf ? 0.f : ldexpf(__builtin_amdgcn_exp2f(m - mt), e0);
+#pragma unroll
+    for (int w = 0; w < W; w++)
+        lt += sh_l[w][col] * (sh_m[w][col] == kNegInf ? 1.f : __builtin_amdgcn_exp2f(sh_m[w][col] - mt));
+    const float share = m == kNegInf || lt == 0.f ? 0.f : __builtin_amdgcn_exp2f(m - mt) / lt;
+    if (threadIdx.x < 16) sh_all[col] = make_float2(mt, lt);
 #pragma unroll
     for (int d0 = 0; d0 < D; d0 += DH) {
         if (d0) __syncthreads();
 #pragma unroll
         for (int i = 0; i < DH / 16; i++) {
-            const f32x4_t v = o[d0 / 16 + i] * f;
+            const f32x4_t v = ldexp4(o[d0 / 16 + i] * share, e0);
             *(f32x4_t*)&sh_o[wave][col][16 * i + 4 * g] = v;
         }
         __syncthreads();
@@ -269,13 +276,6 @@ __global__ __launch_bounds__(64 * W, W == 4 && rows_registers(XT == XT_F32 ? 2 :
             const int row = x / (DH / 4), d = 4 * (x % (DH / 4));
             const int rr = tile * 16 + row;
             if (rr >= rows) continue;
-            float mr = kNegInf;
-#pragma unroll
-            for (int w = 0; w < W; w++) mr = fmaxf(mr, sh_m[w][row]);
-            float lr = 0.f;
-#pragma unroll
-            for (int w = 0; w < W; w++)
-                lr += sh_l[w][row] * (sh_m[w][row] == kNegInf ? 1.f : __builtin_amdgcn_exp2f(sh_m[w][row] - mr));
             f32x4_t v = *(const f32x4_t*)&sh_o[0][row][d];
 #pragma unroll
             for (int w = 1; w < W; w++) v += *(const f32x4_t*)&sh_o[w][row][d];
@@ -284,16 +284,15 @@ __global__ __launch_bounds__(64 * W, W == 4 && rows_registers(XT == XT_F32 ? 2 :
             if (tr.nact > 1) {
                 const int64_t pi = (trow * a.q_heads + hd) * a.splits + split;
                 *(f32x4_t*)(a.part_o + pi * D + d0 + d) = v;
-                if (d0 + d == 0) *(float2*)(a.part_ml + pi * 2) = make_float2(mr, lr);
+                if (d0 + d == 0) *(float2*)(a.part_ml + pi * 2) = sh_all[row];
             } else {
-                const float inv = lr == 0.f ? 0.f : 1.0f / lr;
                 const int64_t at = trow * a.o_row + hd * a.o_head + d0 + d;
                 if constexpr (XT == XT_F32)
-                    *(f32x4_t*)((float*)a.O + at) = v * inv;
+                    *(f32x4_t*)((float*)a.O + at) = v;
                 else {
                     u32x2_t y;
-                    y[0] = (uint32_t)f32_to_16<XT>(v[0] * inv) | (uint32_t)f32_to_16<XT>(v[1] * inv) << 16;
-                    y[1] = (uint32_t)f32_to_16<XT>(v[2] * inv) | (uint32_t)f32_to_16<XT>(v[3] * inv) << 16;
+                    y[0] = (uint32_t)f32_to_16<XT>(v[0]) | (uint32_t)f32_to_16<XT>(v[1]) << 16;
+                    y[1] = (uint32_t)f32_to_16<XT>(v[2]) | (uint32_t)f32_to_16<XT>(v[3]) << 16;
                     *(u32x2_t*)((uint16_t*)a.O + at) = y;
                 }
             }
@@ -309,8 +308,8 @@ __device__ __forceinline__ void store2(void* o, int64_t at, float a, float b) {
         *(uint32_t*)((uint16_t*)o + at) = (uint32_t)f32_to_16<XT>(keep_f32(a)) | (uint32_t)f32_to_16<XT>(keep_f32(b)) << 16;
 }
 
-// Joins the splits of a row and head: W wavefronts take the splits in turn, 4 / W rows a workgroup.  The
-// order of the sums is fixed, so results repeat bit for bit.
+// Joins the splits of a row and head, each a mean with its weight: W wavefronts take the splits in turn, 4 / W
+// rows a workgroup.  The order of the sums is fixed, so results repeat bit for bit.
 template <int XT, int D, int W>
 __global__ __launch_bounds__(256) void attn8_join_kernel(AttnParams a) {
     constexpr int NV = (D + 127) / 128;  // pairs of dims a lane
@@ -326,21 +325,34 @@ __global__ __launch_bounds__(256) void attn8_join_kernel(AttnParams a) {
     const TileRange tr = tile_range(a, sp, r / a.tile_rows * a.tile_rows, a.tile_rows);
     if (tr.nact <= 1) return;
     const int64_t p0 = ((int64_t)(sp.r0 + i) * a.q_heads + head) * a.splits;
-    float mt = kNegInf;
-    for (int x = lane; x < tr.nact; x += 64) mt = fmaxf(mt, a.part_ml[(p0 + x) * 2]);
+    float2 ml = make_float2(kNegInf, 0.f);
+    if (lane < tr.nact) ml = *(const float2*)(a.part_ml + (p0 + lane) * 2);
+    float mt = ml.x, l = ml.y;
+    for (int x = lane + 64; x < tr.nact; x += 64) {
+        const float2 next = *(const float2*)(a.part_ml + (p0 + x) * 2);
+        const float mn = fmaxf(mt, next.x);
+        l = fmaf(l, mt == kNegInf ? 1.f : __builtin_amdgcn_exp2f(mt - mn),
+                 next.y * (next.x == kNegInf ? 1.f : __builtin_amdgcn_exp2f(next.x - mn)));
+        mt = mn;
+    }
+    float mu = mt;
 #pragma unroll
-    for (int e = 1; e < 64; e <<= 1) mt = fmaxf(mt, __shfl_xor(mt, e));
-    const float mu = mt == kNegInf ? 0.f : mt;
-    float l = 0.f;
+    for (int e = 1; e < 64; e <<= 1) mu = fmaxf(mu, __shfl_xor(mu, e));
+    if (mt != kNegInf) l *= __builtin_amdgcn_exp2f(mt - mu);
+#pragma unroll
+    for (int e = 1; e < 64; e <<= 1) l += __shfl_xor(l, e);
+    if (mu == kNegInf) mu = 0.f;
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
     float2 o[NV];
 #pragma unroll
     for (int e = 0; e < NV; e++) o[e] = make_float2(0.f, 0.f);
     for (int x0 = 0; x0 < tr.nact; x0 += 64) {
-        // a lane has a split's factor; the sums take eight splits' loads at a time
-        float2 ml = make_float2(kNegInf, 0.f);
-        if (x0 + lane < tr.nact) ml = *(const float2*)(a.part_ml + (p0 + x0 + lane) * 2);
-        const float w = __builtin_amdgcn_exp2f(ml.x - mu);
-        l += ml.y == 0.f ? 0.f : ml.y * w;
+        // a lane has a split's share; the sums take eight splits' loads at a time
+        if (x0 > 0) {
+            ml = make_float2(kNegInf, 0.f);
+            if (x0 + lane < tr.nact) ml = *(const float2*)(a.part_ml + (p0 + x0 + lane) * 2);
+        }
+        const float w = ml.y == 0.f ? 0.f : __builtin_amdgcn_exp2f(ml.x - mu) * (ml.y * inv);
         const int n = min(tr.nact - x0, 64);
         for (int y = W > 1 ? wave : 0; y < n; y += 8 * W) {
             float2 v[8][NV];
@@ -360,14 +372,12 @@ __global__ __launch_bounds__(256) void attn8_join_kernel(AttnParams a) {
             }
         }
     }
-#pragma unroll
-    for (int e = 1; e < 64; e <<= 1) l += __shfl_xor(l, e);
     const int64_t at = (int64_t)(sp.r0 + i) * a.o_row + head * a.o_head;
     if constexpr (W == 1) {
 #pragma unroll
         for (int e = 0; e < NV; e++) {
             const int d = 2 * lane + 128 * e;
-            if (d < D) store2<XT>(a.O, at + d, l == 0.f ? 0.f : o[e].x / l, l == 0.f ? 0.f : o[e].y / l);
+            if (d < D) store2<XT>(a.O, at + d, o[e].x, o[e].y);
         }
         return;
     }
@@ -381,10 +391,8 @@ __global__ __launch_bounds__(256) void attn8_join_kernel(AttnParams a) {
     if (d >= D) return;
     float y[2];
 #pragma unroll
-    for (int e = 0; e < 2; e++) {
-        const float v = sh_o[0][d + e] + sh_o[W > 1 ? 1 : 0][d + e] + sh_o[W > 1 ? 2 : 0][d + e] + sh_o[W > 1 ? 3 : 0][d + e];
-        y[e] = l == 0.f ? 0.f : v / l;
-    }
+    for (int e = 0; e < 2; e++)
+        y[e] = sh_o[0][d + e] + sh_o[W > 1 ? 1 : 0][d + e] + sh_o[W > 1 ? 2 : 0][d + e] + sh_o[W > 1 ? 3 : 0][d + e];
     store2<XT>(a.O, at + d, y[0], y[1]);
 }
 

@@ -90,6 +90,10 @@ __device__ __forceinline__ TileRange tile_range(const AttnParams& a, const KvSpa
     return t;
 }
 
+__device__ __forceinline__ f32x4_t ldexp4(f32x4_t v, int e) {
+    return f32x4_t{ldexpf(v[0], e), ldexpf(v[1], e), ldexpf(v[2], e), ldexpf(v[3], e)};
+}
+
 // Power of two that brings the largest of a row's values (its bits without the sign) into [2^14, 2^15).
 __device__ __forceinline__ int q_exponent(uint32_t top) {
     const int eb = top >> 23;

@@ -514,29 +514,28 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && XT != XT_F32 && D <= 128 ? 2 : 
         if (r >= rows) continue;
         const int64_t trow = sp.r0 + r / a.group;
         const int hd = h * a.group + r % a.group;
+        // divided before the V scales' power: the values may lie anywhere in f32's range
+        const float inv = lt == 0.f ? 0.f : 1.0f / lt;
+        auto mean = [&](int i, int e) {
+            return ldexp4(f32x4_t{o[c][i][4 * e], o[c][i][4 * e + 1], o[c][i][4 * e + 2], o[c][i][4 * e + 3]} * inv, e0);
+        };
         if (tr.nact > 1) {
-            const float un = ldexpf(1.f, e0);
             const int64_t pi = (trow * a.q_heads + hd) * a.splits + split;
             float* to = a.part_o + pi * D + 4 * g;
 #pragma unroll
             for (int i = 0; i < NT; i++)
 #pragma unroll
-                for (int e = 0; e < 4; e++)
-                    *(f32x4_t*)(to + 32 * i + 8 * e) = f32x4_t{o[c][i][4 * e] * un, o[c][i][4 * e + 1] * un,
-                                                             o[c][i][4 * e + 2] * un, o[c][i][4 * e + 3] * un};
+                for (int e = 0; e < 4; e++) *(f32x4_t*)(to + 32 * i + 8 * e) = mean(i, e);
             if (g == 0) *(float2*)(a.part_ml + pi * 2) = make_float2(m[c], lt);
         } else {
-            const float inv = lt == 0.f ? 0.f : 1.0f / lt;
             const int64_t at = trow * a.o_row + hd * a.o_head + 4 * g;
 #pragma unroll
             for (int i = 0; i < NT; i++)
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
-                    float y[4];
-#pragma unroll
-                    for (int x = 0; x < 4; x++) y[x] = ldexpf(o[c][i][4 * e + x] * inv, e0);
+                    const f32x4_t y = mean(i, e);
                     if constexpr (XT == XT_F32)
-                        *(f32x4_t*)((float*)a.O + at + 32 * i + 8 * e) = f32x4_t{y[0], y[1], y[2], y[3]};
+                        *(f32x4_t*)((float*)a.O + at + 32 * i + 8 * e) = y;
                     else {
                         u32x2_t p;
                         p[0] = (uint32_t)f32_to_16<XT>(y[0]) | (uint32_t)f32_to_16<XT>(y[1]) << 16;

@@ -125,7 +125,7 @@ struct AttnParams {
     int causal, window;
     int tile_rows, tiles, splits, chunk;   // rows a tile, tiles a K/V head, splits of the tokens, tokens a split
     int row_waves;                         // wavefronts a workgroup of 16 rows
-    float *part_o, *part_ml;               // splits > 1: sums [row][head][split][dim], (maximum, weight sum)
+    float *part_o, *part_ml;               // splits > 1: means [row][head][split][dim], (maximum, weight sum)
 };
 void attn8_plan(AttnParams& a, int xt);
 int attn8_max_splits(AttnParams a);  // of any window and type

@@ -67,6 +67,11 @@ def _check(b, q, xt, scale, causal, window, got, rows=None):
     return rows
 
 
+# (rows, tokens): rows kernel in one launch and in splits, tile kernel in few and in many splits
+FORMS = [(1, 900), (5, 5000), (150, 900), (90, 5000)]
+ONE = (150, 250)                                       # a tile in one launch
+
+
 @pytest.mark.parametrize("new", [5, 40, 150])
 @pytest.mark.parametrize("which", ["k", "v"])
 @pytest.mark.parametrize("value", [np.inf, -np.inf])
@@ -87,3 +92,17 @@ def test_an_infinite_scale_makes_rows_nan(new, which, value, xt):
         if before:
             rows = _check(b, q, xt, 0.09, True, 0, got)
             assert np.array_equal(rows, np.arange(b.T) < before)
+
+
+@pytest.mark.parametrize("new,total", FORMS + [ONE])
+@pytest.mark.parametrize("xt", ["bf16", "f32"])
+def test_values_near_the_largest(new, total, xt):
+    """V up to 2^125, all of one sign, weights alike: the sums before the division would pass the largest f32."""
+    print(f"large values new={new} total={total} {xt}", flush=True)
+    b = Batch([(new, total)], 2, 64, 48, 42)
+    b.vc = np.abs(b.vc) | 1
+    b.vs *= np.float32(2.0 ** 123)
+    b.upload()
+    q = (_values(b.rng, (b.T, 4, 64), xt) / 16).cuda()
+    got = _attend(b, q, 4, 0.125, True, 0)
+    _check(b, q, xt, 0.125, True, 0, got)
