@@ -58,6 +58,7 @@ __global__ __launch_bounds__(64 * W, W == 4 && rows_registers(XT == XT_F32 ? 2 :
     __shared__ float sh_o[W][16][DH + 4];
     __shared__ float sh_m[W][16], sh_l[W][16];
     __shared__ float2 sh_all[16];
+    __shared__ FarSum sh_far[W][64];
 
     const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -155,7 +156,8 @@ __global__ __launch_bounds__(64 * W, W == 4 && rows_registers(XT == XT_F32 ? 2 :
     f32x4_t o[NT];
 #pragma unroll
     for (int i = 0; i < NT; i++) o[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    float m = kNegInf, limit = kNegInf, mu = (float)kBase, l = 0.f;
+    float m = kNegInf, l = 0.f;
+    bool any_far = false;  // sh_far holds sums
     int e0 = bi < 0 ? -1000 : v_exponent(vs);
     e0 = max(e0, __shfl_xor(e0, 16));
     e0 = __builtin_amdgcn_readfirstlane(max(e0, __shfl_xor(e0, 32)));
@@ -200,21 +202,26 @@ __global__ __launch_bounds__(64 * W, W == 4 && rows_registers(XT == XT_F32 ? 2 :
 #pragma unroll
             for (int j = 0; j < 16; j++) p[j] = ((j >= jl) & (j < jh)) ? p[j] : kNegInf;
         }
+        if (__any(is_far(lv))) {
+            FarSum f = {kNegInf, 0.f};
+            if (any_far) f = sh_far[wave][lane];
+            if (is_far(lv)) far_add(f, p);
+            sh_far[wave][lane] = f;
+            any_far = true;
+        }
         float top = p[0];
 #pragma unroll
         for (int j = 1; j < 16; j++) top = fmaxf(top, p[j]);
         top += lv;
-        if (__any(top > limit)) {
+        if (__any(top > m + kLag)) {
             const float mn = fmaxf(m, groups_max(top));
             const float f = m == kNegInf ? 0.f : __builtin_amdgcn_exp2f(m - mn);
             l *= f;
 #pragma unroll
             for (int i = 0; i < NT; i++) o[i] *= f;
             m = mn;
-            limit = mn + kLag;
-            mu = mn == kNegInf ? (float)kBase : (float)kBase - mn;
         }
-        const float c = lv + mu;
+        const float c = lv + above_m(m);
         half8_t pf[NP][2];
         float sum = 0.f;
 #pragma unroll
@@ -225,7 +232,7 @@ __global__ __launch_bounds__(64 * W, W == 4 && rows_registers(XT == XT_F32 ? 2 :
             pf[0][j >> 3][j & 7] = hi;
             if constexpr (NP == 2) pf[1][j >> 3][j & 7] = (_Float16)(w - (float)hi);
         }
-        l = fmaf(sum, __builtin_amdgcn_exp2f(-lv), l);
+        l = fmaf(sum, v_reciprocal(lv), l);
         const half2_t f = __builtin_bit_cast(half2_t, v_sign(vnow)), fc = f * (half2_t){(_Float16)-1152.f, (_Float16)-1152.f};
 #pragma unroll
         for (int i = 0; i < NT; i++) {
@@ -247,10 +254,16 @@ __global__ __launch_bounds__(64 * W, W == 4 && rows_registers(XT == XT_F32 ? 2 :
     }
 
     // join the wavefronts
-    l = groups_sum(l);
+    FarSum far = {kNegInf, 0.f};
+    if (any_far) {
+        far = sh_far[wave][lane];
+        far_add(far, __shfl_xor(far.m, 16), __shfl_xor(far.l, 16));
+        far_add(far, __shfl_xor(far.m, 32), __shfl_xor(far.l, 32));
+    }
+    const RowEnd end = row_end(groups_sum(l), m, far, e0);
     if (g == 0) {
-        sh_m[wave][col] = m;
-        sh_l[wave][col] = l;
+        sh_m[wave][col] = end.m;
+        sh_l[wave][col] = end.l;
     }
     __syncthreads();
     // each wavefront's sums as its share of the split's mean: no larger than the values, which may lie anywhere in
@@ -261,14 +274,14 @@ __global__ __launch_bounds__(64 * W, W == 4 && rows_registers(XT == XT_F32 ? 2 :
 #pragma unroll
     for (int w = 0; w < W; w++)
         lt += sh_l[w][col] * (sh_m[w][col] == kNegInf ? 1.f : __builtin_amdgcn_exp2f(sh_m[w][col] - mt));
-    const float share = m == kNegInf || lt == 0.f ? 0.f : __builtin_amdgcn_exp2f(m - mt) / lt;
+    const float share = end.m == kNegInf ? 0.f : __builtin_amdgcn_exp2f(end.m - mt) / lt;
     if (threadIdx.x < 16) sh_all[col] = make_float2(mt, lt);
 #pragma unroll
     for (int d0 = 0; d0 < D; d0 += DH) {
         if (d0) __syncthreads();
 #pragma unroll
         for (int i = 0; i < DH / 16; i++) {
-            const f32x4_t v = ldexp4(o[d0 / 16 + i] * share, e0);
+            const f32x4_t v = ldexp4(o[d0 / 16 + i] * share, end.e);
             *(f32x4_t*)&sh_o[wave][col][16 * i + 4 * g] = v;
         }
         __syncthreads();

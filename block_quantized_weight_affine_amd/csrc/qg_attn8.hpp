@@ -23,6 +23,8 @@ constexpr float kNegInf = -__builtin_inff();
 // f16's full precision down to 2^-23 of the row's largest.  e0 only keeps the powers in f32's range.
 constexpr float kLag = 6.f;
 constexpr int kBase = 9;
+// kBase - m; before a row has a maximum, kBase.
+__device__ __forceinline__ float above_m(float m) { return m == kNegInf ? (float)kBase : (float)kBase - m; }
 
 // Four codes as four f16 values, exactly: byte ^ 0x80 below 0x64 is 1024 + (code + 128).
 __device__ __forceinline__ void codes4_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
@@ -65,11 +67,55 @@ __device__ __forceinline__ half8_t codes8_f16(uint32_t w0, uint32_t w1, half2_t 
 __device__ __forceinline__ bool finite_scales(float ks, float vs) { return (ks - ks) + (vs - vs) == 0.f; }
 // The factor of a block's V codes: the V scale's sign.
 __device__ __forceinline__ uint32_t v_sign(float vs) { return vs == 0.f ? 0u : vs < 0.f ? 0xbc00bc00u : 0x3c003c00u; }
-// log2(|vs| 2^-e0), 0 where the scale is 0 (its codes count as 0) or not finite (its K scale becomes NaN).
+// log2(|vs| 2^-e0): -inf where the scale is 0, 0 where it is not finite (its K scale becomes NaN).
 __device__ __forceinline__ float v_power(float vs, int e0) {
     const float va = fabsf(vs);
-    if (va == 0.f || !(va < __builtin_inff())) return 0.f;
+    if (va == 0.f) return kNegInf;
+    if (!(va < __builtin_inff())) return 0.f;
     return fminf(fmaxf(__builtin_amdgcn_logf(ldexpf(va, -e0)), -100.f), 100.f);
+}
+// A block whose weights say nothing about its part of the denominator: it has an own sum for that, FarSum, and the
+// factor 0 in the other.  V scales of 0: their tokens weigh nothing in the numerator, and whatever they score, the
+// running maximum of what stands there must not rise for them.
+__device__ __forceinline__ bool is_far(float lv) { return fabsf(lv) > 1000.f; }
+__device__ __forceinline__ float v_reciprocal(float lv) { return is_far(lv) ? 0.f : __builtin_amdgcn_exp2f(-lv); }
+struct FarSum {
+    float m, l;  // sum of exp2(s - m), m the largest s
+};
+template <int N>
+__device__ __forceinline__ void far_add(FarSum& f, const float (&s)[N]) {
+    float m = f.m;
+#pragma unroll
+    for (int i = 0; i < N; i++) m = fmaxf(m, s[i]);
+    if (m == kNegInf) return;
+    f.l *= __builtin_amdgcn_exp2f(f.m - m);
+#pragma unroll
+    for (int i = 0; i < N; i++) f.l += __builtin_amdgcn_exp2f(s[i] - m);
+    f.m = m;
+}
+__device__ __forceinline__ void far_add(FarSum& f, float m, float l) {
+    const float mn = fmaxf(f.m, m);
+    if (mn == kNegInf) return;
+    f.l = f.l * __builtin_amdgcn_exp2f(f.m - mn) + l * __builtin_amdgcn_exp2f(m - mn);
+    f.m = mn;
+}
+// A row's weights at the end: their sum is l 2^m, and o / l has to be taken times 2^e.
+struct RowEnd {
+    float l, m;
+    int e;
+};
+// From the sum l of the other blocks' weights below the maximum m (-inf: there are none), and that of the far ones.
+__device__ __forceinline__ RowEnd row_end(float l, float m, const FarSum& f, int e0) {
+    const float mu = above_m(m);
+    float k = 0.f;  // a whole power, so that nothing is rounded by it
+    if (f.m > kNegInf) {
+        k = __builtin_rintf(f.m + mu);
+        if (m > kNegInf) k = fmaxf(k, 0.f);
+        float rest = (mu - k) + f.m;
+        if (k != 0.f) rest = fminf(fmaxf(rest, -1.f), 1.f);
+        l = (l == 0.f ? 0.f : l * __builtin_amdgcn_exp2f(-k)) + f.l * __builtin_amdgcn_exp2f(rest);
+    }
+    return RowEnd{l, l == 0.f ? kNegInf : k - mu, e0 - (int)fminf(fmaxf(k, -5000.f), 5000.f)};
 }
 // Exponent of |vs|, -1000 where it is 0 or not finite.
 __device__ __forceinline__ int v_exponent(float vs) {

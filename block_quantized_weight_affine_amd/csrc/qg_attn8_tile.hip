@@ -64,6 +64,8 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && XT != XT_F32 && D <= 128 ? 2 : 
     __shared__ __attribute__((aligned(16))) float in_ks[2 * kInfo], in_lv[2 * kInfo], in_rv[2 * kInfo];
     __shared__ uint32_t in_sg[2 * kInfo];
     __shared__ int in_top[NW];
+    __shared__ FarSum sh_far[NW][CT][64];
+    bool any_far = false;  // sh_far holds sums
 
     const int lane = threadIdx.x & 63, col = lane & 31, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -136,11 +138,14 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && XT != XT_F32 && D <= 128 ? 2 : 
     for (int i = 0; i <= KB; i++) first[i] = index_of((t0 >> 4) + 4 * i + (lane >> 4), first[i]);
     auto note = [&](int seg, int bi, float ks, float vs) {
         const int x = (kInfo * seg + tid) & (2 * kInfo - 1);
-        const float lv = v_power(vs, e0);
+        const float lv = bi < 0 ? 0.f : v_power(vs, e0);
         in_bi[x] = bi;
-        in_ks[x] = bi < 0 ? -1.f : finite_scales(ks, vs) ? ks : __builtin_nanf("");
+        // a far block's K scale is below 0 here, and its sign that of the zero beside it: scale_and_hide tells far
+        // blocks by what it looks at for negative scales
+        const float k = is_far(lv) ? -fabsf(ks) : ks;
+        in_ks[x] = bi < 0 ? -1.f : finite_scales(ks, vs) ? k : __builtin_nanf("");
         in_lv[x] = lv;
-        in_rv[x] = __builtin_amdgcn_exp2f(-lv);
+        in_rv[x] = is_far(lv) ? copysignf(0.f, ks) : v_reciprocal(lv);
         in_sg[x] = v_sign(vs);
     };
 
@@ -211,7 +216,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && XT != XT_F32 && D <= 128 ? 2 : 
     for (int c = 0; c < CT; c++) m[c] = limit[c] = kNegInf, l[c] = 0.f, mu[c] = (float)kBase;
     float kf[CT][4], cf[CT][4];  // factor and addend of a score
 
-    // Stage st's scales; where a row does not see all of it, or a scale is negative, NaN or infinite, the
+    // Stage st's scales; where a row does not see all of it, or a scale is negative, NaN, infinite or far, the
     // scores are scaled and hidden one by one.
     f32x4_t kb, lv, rv, rn;
     auto read_scales = [&](int st) {
@@ -236,6 +241,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && XT != XT_F32 && D <= 128 ? 2 : 
                 const int jl = see[c].lo - tb - 4 * g, jh = see[c].hi - tb - 4 * g;
 #pragma unroll
                 for (int q = 0; q < 4; q++) {
+                    if (is_far(lv[q])) kf[c][q] = copysignf(kb[q], rn[q]) * qs[c];
 #pragma unroll
                     for (int e = 0; e < 8; e++) {
                         const int j = 16 * q + 8 * (e >> 2) + (e & 3);
@@ -244,6 +250,26 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && XT != XT_F32 && D <= 128 ? 2 : 
                     }
                     kf[c][q] = 1.f;
                 }
+            }
+            float far = 0.f;
+#pragma unroll
+            for (int q = 0; q < 4; q++) far = fmaxf(far, fabsf(lv[q]));
+            if (is_far(__uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(far))))) {
+#pragma unroll
+                for (int c = 0; c < CT; c++) {
+                    FarSum f = {kNegInf, 0.f};
+                    if (any_far) f = sh_far[wave][c][lane];
+#pragma unroll
+                    for (int q = 0; q < 4; q++) {
+                        if (!is_far(lv[q])) continue;
+                        float s[8];
+#pragma unroll
+                        for (int e = 0; e < 8; e++) s[e] = sc[c][q >> 1][8 * (q & 1) + e];
+                        far_add(f, s);
+                    }
+                    sh_far[wave][c][lane] = f;
+                }
+                any_far = true;
             }
         }
     };
@@ -277,7 +303,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && XT != XT_F32 && D <= 128 ? 2 : 
                     for (int e = 0; e < 16; e++) o[c][i][e] *= f;
                 m[c] = mn;
                 limit[c] = mn + kLag;
-                mu[c] = mn == kNegInf ? (float)kBase : (float)kBase - mn;
+                mu[c] = above_m(mn);
             }
         }
         rv = rn;
@@ -510,14 +536,19 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && XT != XT_F32 && D <= 128 ? 2 : 
 #pragma unroll
     for (int c = 0; c < CT; c++) {
         const int r = w0 + 32 * c + col;
-        const float lt = l[c] + __shfl_xor(l[c], 32);
+        FarSum far = {kNegInf, 0.f};
+        if (any_far) {
+            far = sh_far[wave][c][lane];
+            far_add(far, __shfl_xor(far.m, 32), __shfl_xor(far.l, 32));
+        }
+        const RowEnd end = row_end(l[c] + __shfl_xor(l[c], 32), m[c], far, e0);
         if (r >= rows) continue;
         const int64_t trow = sp.r0 + r / a.group;
         const int hd = h * a.group + r % a.group;
         // divided before the V scales' power: the values may lie anywhere in f32's range
-        const float inv = lt == 0.f ? 0.f : 1.0f / lt;
+        const float inv = end.l == 0.f ? 0.f : 1.0f / end.l;
         auto mean = [&](int i, int e) {
-            return ldexp4(f32x4_t{o[c][i][4 * e], o[c][i][4 * e + 1], o[c][i][4 * e + 2], o[c][i][4 * e + 3]} * inv, e0);
+            return ldexp4(f32x4_t{o[c][i][4 * e], o[c][i][4 * e + 1], o[c][i][4 * e + 2], o[c][i][4 * e + 3]} * inv, end.e);
         };
         if (tr.nact > 1) {
             const int64_t pi = (trow * a.q_heads + hd) * a.splits + split;
@@ -526,7 +557,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && XT != XT_F32 && D <= 128 ? 2 : 
             for (int i = 0; i < NT; i++)
 #pragma unroll
                 for (int e = 0; e < 4; e++) *(f32x4_t*)(to + 32 * i + 8 * e) = mean(i, e);
-            if (g == 0) *(float2*)(a.part_ml + pi * 2) = make_float2(m[c], lt);
+            if (g == 0) *(float2*)(a.part_ml + pi * 2) = make_float2(end.m, end.l);
         } else {
             const int64_t at = trow * a.o_row + hd * a.o_head + 4 * g;
 #pragma unroll

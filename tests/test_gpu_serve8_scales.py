@@ -67,6 +67,13 @@ def _check(b, q, xt, scale, causal, window, got, rows=None):
     return rows
 
 
+def _set_v(b, s, lo, hi, f):
+    """Applies f to the V scales of the blocks of tokens lo..hi-1 of sequence s (lo a multiple of 16)."""
+    for j in range(lo, hi, 16):
+        p, o = serve8.place(b.table, b.page, b.P, s, j)
+        b.vs[p, :, o // 16] = f(b.vs[p, :, o // 16])
+
+
 # (rows, tokens): rows kernel in one launch and in splits, tile kernel in few and in many splits
 FORMS = [(1, 900), (5, 5000), (150, 900), (90, 5000)]
 ONE = (150, 250)                                       # a tile in one launch
@@ -106,3 +113,53 @@ def test_values_near_the_largest(new, total, xt):
     q = (_values(b.rng, (b.T, 4, 64), xt) / 16).cuda()
     got = _attend(b, q, 4, 0.125, True, 0)
     _check(b, q, xt, 0.125, True, 0, got)
+
+
+@pytest.mark.parametrize("new,total", FORMS)
+@pytest.mark.parametrize("size", [1.0, 1e-5, 1e-7])
+@pytest.mark.parametrize("xt", ["f16", "bf16", "f32"])
+def test_blocks_of_zeros_before_small_values(new, total, size, xt):
+    """All V before the last 250 tokens are zero, those of the last small: the weights of the zeros belong to the
+    denominator and to nothing else."""
+    if xt == "f16":
+        size *= 64                                     # results stay in f16's normal range
+    print(f"zeros new={new} total={total} {size} {xt}", flush=True)
+    b = Batch([(new, total)], 2, 128, 32, 43)
+    b.vs *= np.float32(size)
+    _set_v(b, 0, 0, total - 250, lambda x: 0)
+    b.upload()
+    q = _values(b.rng, (b.T, 8, 128), xt).cuda()
+    got = _attend(b, q, 8, 0.09, True, 0)
+    _check(b, q, xt, 0.09, True, 0, got)
+
+
+@pytest.mark.parametrize("new,total,at", [(n, t, at) for n, t in FORMS for at in (0, 416, 640)] + [ONE + (0,), ONE + (64,)])
+@pytest.mark.parametrize("xt", ["bf16", "f32"])
+def test_a_block_of_zeros_that_has_the_weight(new, total, at, xt):
+    """A block of V zeros scores some 20 above the rest: the result is small, and as precise as any."""
+    print(f"zero block with the weight at={at} new={new} total={total} {xt}", flush=True)
+    b = Batch([(new, total)], 1, 64, 16, 44)
+    p, _ = serve8.place(b.table, 16, b.P, 0, at)
+    b.kc[p] = 100
+    b.ks[p] = 0.06
+    b.vs[p] = 0
+    b.upload()
+    q = (_values(b.rng, (b.T, 2, 64), "f32") / 16 + 0.4).to(TYPES[xt]).cuda()
+    got = _attend(b, q, 2, 0.125, True, 0)
+    _check(b, q, xt, 0.125, True, 0, got)
+
+
+def test_only_zeros():
+    """Rows that see nothing but V zeros are zero, beside rows that see more."""
+    for new, total in FORMS:
+        print(f"only zeros new={new} total={total}", flush=True)
+        b = Batch([(new, total)], 1, 64, 16, 45)
+        b.vs[:] = 0
+        b.ks[::2] = 0
+        _set_v(b, 0, (total - 1) // 16 * 16, total, lambda x: 0.01)
+        q = _values(b.rng, (b.T, 2, 64), "f32").cuda()
+        got = _attend(b.upload(), q, 2, 0.125, True, 0)
+        _check(b, q, "f32", 0.125, True, 0, got)
+        first = new - ((total - 1) % 16 + 1)           # rows before the last block
+        if first > 0:
+            assert torch.all(got[:first] == 0)
