@@ -205,7 +205,12 @@ __global__ __launch_bounds__(64 * W, W == 4 && rows_registers(XT == XT_F32 ? 2 :
         if (__any(is_far(lv))) {
             FarSum f = {kNegInf, 0.f};
             if (any_far) f = sh_far[wave][lane];
-            if (is_far(lv)) far_add(f, p);
+            if (is_far(lv)) {
+                far_add(f, p);
+                const float rest = v_power_rest(vnow, e0, lv);
+#pragma unroll
+                for (int j = 0; j < 16; j++) p[j] += rest;
+            }
             sh_far[wave][lane] = f;
             any_far = true;
         }

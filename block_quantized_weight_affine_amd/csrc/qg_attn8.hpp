@@ -20,7 +20,8 @@ constexpr float kNegInf = -__builtin_inff();
 //   w = exp2(s + log2(vs 2^-e0) - m + kBase),  m a running maximum of what stands before it in the row,
 // and the denominator takes w times the reciprocal, so a row's precision is set by the blocks that it sees
 // and by no others.  m may lag by kLag before the sums are rescaled: weights stay at or below 2^15 and keep
-// f16's full precision down to 2^-23 of the row's largest.  e0 only keeps the powers in f32's range.
+// f16's full precision down to 2^-23 of the row's largest.  e0, an exponent of V scales near by, keeps the powers
+// small.
 constexpr float kLag = 6.f;
 constexpr int kBase = 9;
 // kBase - m; before a row has a maximum, kBase.
@@ -72,12 +73,21 @@ __device__ __forceinline__ float v_power(float vs, int e0) {
     const float va = fabsf(vs);
     if (va == 0.f) return kNegInf;
     if (!(va < __builtin_inff())) return 0.f;
-    return fminf(fmaxf(__builtin_amdgcn_logf(ldexpf(va, -e0)), -100.f), 100.f);
+    return __builtin_amdgcn_logf(__builtin_amdgcn_frexp_mantf(va)) + (float)(__builtin_amdgcn_frexp_expf(va) - e0);
 }
-// A block whose weights say nothing about its part of the denominator: it has an own sum for that, FarSum, and the
-// factor 0 in the other.  V scales of 0: their tokens weigh nothing in the numerator, and whatever they score, the
-// running maximum of what stands there must not rise for them.
-__device__ __forceinline__ bool is_far(float lv) { return fabsf(lv) > 1000.f; }
+// What a far block's power lost to rounding: its scores take it once they are in FarSum.
+__device__ __forceinline__ float v_power_rest(float vs, int e0, float lv) {
+    if (lv == kNegInf) return 0.f;
+    const float va = fabsf(vs);
+    return ((float)(__builtin_amdgcn_frexp_expf(va) - e0) - lv) + __builtin_amdgcn_logf(__builtin_amdgcn_frexp_mantf(va));
+}
+// A far block's weights say nothing about its part of the denominator: it has an own sum for that, FarSum, and the
+// factor 0 in the other.  Far are V scales of 0, whose tokens weigh nothing in the numerator (whatever they score, the
+// running maximum of what stands there must not rise for them), and those so far from 2^e0 that the reciprocal or the
+// sum could leave f32's range: e0 comes from blocks that a row need not see.  With 2^32 a row's other blocks keep
+// theirs while its V scales lie within 2^100 of each other.
+constexpr float kFar = 32.f;
+__device__ __forceinline__ bool is_far(float lv) { return fabsf(lv) > kFar; }
 __device__ __forceinline__ float v_reciprocal(float lv) { return is_far(lv) ? 0.f : __builtin_amdgcn_exp2f(-lv); }
 struct FarSum {
     float m, l;  // sum of exp2(s - m), m the largest s

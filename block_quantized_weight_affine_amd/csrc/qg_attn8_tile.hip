@@ -266,6 +266,9 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && XT != XT_F32 && D <= 128 ? 2 : 
 #pragma unroll
                         for (int e = 0; e < 8; e++) s[e] = sc[c][q >> 1][8 * (q & 1) + e];
                         far_add(f, s);
+                        const float rest = v_power_rest(a.c.vs[max(bi[q], 0)], e0, lv[q]);
+#pragma unroll
+                        for (int e = 0; e < 8; e++) sc[c][q >> 1][8 * (q & 1) + e] += rest;
                     }
                     sh_far[wave][c][lane] = f;
                 }

@@ -163,3 +163,67 @@ def test_only_zeros():
         first = new - ((total - 1) % 16 + 1)           # rows before the last block
         if first > 0:
             assert torch.all(got[:first] == 0)
+
+
+@pytest.mark.parametrize("new,total", [(5, 370), (30, 370), (5, 5042), (150, 370), (90, 5042), (150, 178)])
+@pytest.mark.parametrize("far", [20, 60, 120, 126])
+@pytest.mark.parametrize("xt", ["f16", "bf16", "f32"])
+def test_a_hidden_block_of_another_size(new, total, far, xt):
+    """The last two tokens have V scales of 2^far times the others', which causality hides from the rows before them."""
+    print(f"hidden far={far} new={new} total={total} {xt}", flush=True)
+    b = Batch([(new, total)], 2, 64, 16, 46)
+    last = total // 16 * 16
+    assert total - last == 2
+    _set_v(b, 0, last, total, lambda x: np.float32(2.0 ** (far - 7)))
+    b.upload()
+    q = _values(b.rng, (b.T, 4, 64), xt).cuda()
+    got = _attend(b, q, 4, 0.125, True, 0)
+    _check(b, q, xt, 0.125, True, 0, got, np.arange(b.T) < new - 2)
+    if far <= 60 and xt != "f16":                      # f16 has no such values
+        _check(b, q, xt, 0.125, True, 0, got)
+
+
+@pytest.mark.parametrize("new,total", FORMS)
+@pytest.mark.parametrize("power", [-90, -40, 40, 90])
+def test_later_blocks_of_another_size(new, total, power):
+    """V scales 2^power apart between the first tokens and the last, all of them seen."""
+    print(f"later blocks 2^{power} new={new} total={total}", flush=True)
+    for xt in ("bf16", "f32"):
+        b = Batch([(new, total)], 2, 64, 48, 47)
+        _set_v(b, 0, (total - 280) // 16 * 16, total, lambda x: x * np.float32(2.0 ** power))
+        b.upload()
+        q = _values(b.rng, (b.T, 4, 64), xt).cuda()
+        got = _attend(b, q, 4, 0.125, True, 0)
+        _check(b, q, xt, 0.125, True, 0, got)
+
+
+@pytest.mark.parametrize("new", [1, 6, 100])
+@pytest.mark.parametrize("xt", ["f16", "bf16", "f32"])
+def test_heads_and_sequences_of_different_sizes(new, xt):
+    """Heads and sequences whose V scales lie far below the cache's largest are as precise as the others."""
+    print(f"heads of different sizes new={new} {xt}", flush=True)
+    b = Batch([(new, 400), (new, 1100), (new, 130)], 3, 64, 32, 48)
+    b.vs[:, 1] *= np.float32(2.0 ** -10)
+    b.vs[:, 2] *= np.float32(2.0 ** (-12 if xt == "f16" else -70))
+    if xt != "f16":
+        _set_v(b, 1, 0, 1100, lambda x: x * np.float32(2.0 ** -30))
+    unused = sorted(set(range(b.P)) - set(b.table.reshape(-1).tolist()))
+    b.vs[unused] = np.float32(2.0 ** 90)
+    b.upload()
+    q = _values(b.rng, (b.T, 6, 64), xt).cuda()
+    got = _attend(b, q, 6, 0.125, True, 0)
+    _check(b, q, xt, 0.125, True, 0, got)
+
+
+@pytest.mark.parametrize("xt", ["f16", "bf16"])
+def test_tall_tiles(xt):
+    """Tiles of 256 rows: V zeros under the first tokens, the last two of 2^120 times the others' size and hidden from the
+    rows before them."""
+    print(f"tall tiles {xt}", flush=True)
+    b = Batch([(64, 194)] + [(i % 4, 20 + i % 4) for i in range(63)], 4, 64, 32, 49)
+    _set_v(b, 0, 0, 64, lambda x: 0)
+    _set_v(b, 0, 192, 194, lambda x: np.float32(2.0 ** 113))
+    b.upload()
+    q = _values(b.rng, (b.T, 16, 64), xt).cuda()
+    got = _attend(b, q, 16, 0.125, True, 0)
+    _check(b, q, xt, 0.125, True, 0, got, (np.arange(b.T) < 62) | (np.arange(b.T) >= 64))
