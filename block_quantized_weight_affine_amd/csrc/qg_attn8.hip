@@ -11,8 +11,6 @@
 
 #include <hip/hip_runtime.h>
 
-#include <algorithm>
-
 #include "qg_attn8.hpp"
 
 namespace qg {
@@ -62,7 +60,7 @@ __global__ __launch_bounds__(64 * W, W == 4 && rows_registers(XT == XT_F32 ? 2 :
 
     const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    int b = blockIdx.x;
+    int b = a.first + blockIdx.x;
     const int tile = b % a.tiles;
     b /= a.tiles;
     const int h = b % a.c.heads;
@@ -417,16 +415,20 @@ __global__ __launch_bounds__(256) void attn8_join_kernel(AttnParams a) {
 constexpr int64_t kJoinWide = 2048;  // rows that are joined by a workgroup each, where a wavefront has more than 8 splits to read
 
 template <int XT, int D>
-hipError_t launch_one(const AttnParams& a, hipStream_t s) {
+hipError_t launch_one(AttnParams a, hipStream_t s) {
     const int64_t grid = (int64_t)a.q.seqs * a.splits * a.c.heads * a.tiles;
     if (a.tile_rows > 16) {
         const hipError_t e = launch_attn8_tile(a, XT, s);
         if (e != hipSuccess) return e;
     } else {
-        if (a.row_waves == 8)
-            attn8_rows_kernel<XT, D, 8><<<dim3((uint32_t)grid), 512, 0, s>>>(a);
-        else if constexpr (!rows_late(XT == XT_F32 ? 2 : 1, D))
-            attn8_rows_kernel<XT, D, 4><<<dim3((uint32_t)grid), 256, 0, s>>>(a);
+        for (int64_t first = 0; first < grid; first += kLaunchGroups) {
+            a.first = (int)first;
+            const dim3 part((uint32_t)std::min(grid - first, kLaunchGroups));
+            if (a.row_waves == 8)
+                attn8_rows_kernel<XT, D, 8><<<part, 512, 0, s>>>(a);
+            else if constexpr (!rows_late(XT == XT_F32 ? 2 : 1, D))
+                attn8_rows_kernel<XT, D, 4><<<part, 256, 0, s>>>(a);
+        }
     }
     if (a.splits > 1) {
         const uint32_t rows = (uint32_t)a.q.max_new * (uint32_t)a.q_heads;

@@ -1,4 +1,6 @@
 // qg_attn8_tile.hip -- attention over the 8-bit cache for many rows a K/V head: prompts and chunks.
+#include <algorithm>
+
 #include <hip/hip_runtime.h>
 
 #include "qg_attn8.hpp"
@@ -71,7 +73,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && XT != XT_F32 && D <= 128 ? 2 : 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // sequences and heads first, so that the workgroups of one K/V head share a die's cache; of each sequence
     // the last tile, which sees the most, first, so that the workgroups with nothing to do come last
-    int b = blockIdx.x;
+    int b = a.first + blockIdx.x;
     const int pairs = a.q.seqs * a.c.heads;
     const int h = b % pairs % a.c.heads, s = b % pairs / a.c.heads;
     b /= pairs;
@@ -582,15 +584,16 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && XT != XT_F32 && D <= 128 ? 2 : 
 }
 
 template <int XT, int D>
-hipError_t launch_one(const AttnParams& a, hipStream_t s) {
-    const uint32_t grid = (uint32_t)((int64_t)a.q.seqs * a.splits * a.c.heads * a.tiles);
-    if constexpr (XT != XT_F32 && D <= 128) {
-        if (a.tile_rows == 256) {
-            attn8_tile_kernel<XT, D, 8, 1><<<grid, 512, 0, s>>>(a);
-            return hipGetLastError();
-        }
+hipError_t launch_one(AttnParams a, hipStream_t s) {
+    const int64_t grid = (int64_t)a.q.seqs * a.splits * a.c.heads * a.tiles;
+    for (int64_t first = 0; first < grid; first += kLaunchGroups) {
+        a.first = (int)first;
+        const uint32_t part = (uint32_t)std::min(grid - first, kLaunchGroups);
+        if (a.tile_rows == 128)
+            attn8_tile_kernel<XT, D, 4, 1><<<part, 256, 0, s>>>(a);
+        else if constexpr (XT != XT_F32 && D <= 128)
+            attn8_tile_kernel<XT, D, 8, 1><<<part, 512, 0, s>>>(a);
     }
-    attn8_tile_kernel<XT, D, 4, 1><<<grid, 256, 0, s>>>(a);
     return hipGetLastError();
 }
 

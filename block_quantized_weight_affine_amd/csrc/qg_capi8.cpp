@@ -88,8 +88,9 @@ qg_status attn_params(const qg_kv8_cache* cache, const qg_kv8_seqs* seqs, int q_
     a.window = window > 0 ? window : 0;
     if (empty(a.q)) return QG_OK;
     if ((int64_t)a.q.max_new * q_heads >= ((int64_t)1 << 31)) return QG_ESHAPE;
+    // workgroups stay below 2^31: tiles of 128 rows at least, or at most 4 tiles of 16 rows in 6 splits a head
+    if ((int64_t)a.q.seqs * a.q.max_new * q_heads >= ((int64_t)1 << 37)) return QG_ESHAPE;
     qg::attn8_plan(a, xt);
-    if ((int64_t)a.q.seqs * a.splits * a.c.heads * a.tiles >= ((int64_t)1 << 31)) return QG_ESHAPE;
     return QG_OK;
 }
 

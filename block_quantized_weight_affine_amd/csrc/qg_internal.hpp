@@ -105,6 +105,10 @@ hipError_t launch_moe_combine(const float* O, int R, const int32_t* slot_row, co
                               int T, int k, int accumulate, hipStream_t s);
 
 
+// Workgroups of a launch at most, of up to 512 work items, which a launch counts in 32 bits: larger grids take
+// several launches.
+constexpr int64_t kLaunchGroups = 1 << 22;
+
 // ---- 8-bit serving operators ------------------------------------------------------------------------
 // Elements between tokens and between heads of K and V rows.
 struct KvStrides {
@@ -125,6 +129,7 @@ struct AttnParams {
     int causal, window;
     int tile_rows, tiles, splits, chunk;   // rows a tile, tiles a K/V head, splits of the tokens, tokens a split
     int row_waves;                         // wavefronts a workgroup of 16 rows
+    int first;                             // a launch's first workgroup
     float *part_o, *part_ml;               // splits > 1: means [row][head][split][dim], (maximum, weight sum)
 };
 void attn8_plan(AttnParams& a, int xt);

@@ -527,9 +527,9 @@ size_t qg_attn_kv8_workspace(const qg_kv8_cache* cache, const qg_kv8_seqs* seqs,
  * a block whose K or V scale is NaN or infinite is NaN; what a row does not see never reaches it.  Single
  * tokens, drafts and whole prompts take the same call.  The order of the sums is fixed: results repeat bit
  * for bit.
- * q_heads a multiple of heads, <= 65536, max_new * q_heads < 2^31, else QG_ESHAPE; strides as in
- * qg_kv8_write (o as an output); workspace 16-byte aligned, QG_EWORKSPACE if NULL or too small.  It needs
- * no initialisation; calls that overlap in time need one each. */
+ * q_heads a multiple of heads, <= 65536, max_new * q_heads < 2^31, seqs * max_new * q_heads < 2^37, else
+ * QG_ESHAPE; strides as in qg_kv8_write (o as an output); workspace 16-byte aligned, QG_EWORKSPACE if NULL or
+ * too small.  It needs no initialisation; calls that overlap in time need one each. */
 qg_status qg_attn_kv8(const qg_kv8_cache* cache, const qg_kv8_seqs* seqs, const void* q, int64_t q_row,
                       int64_t q_head, void* o, int64_t o_row, int64_t o_head, qg_xtype xt, int q_heads,
                       float scale, int causal, int window, void* workspace, size_t ws_bytes,
