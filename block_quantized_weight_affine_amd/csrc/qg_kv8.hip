@@ -4,6 +4,8 @@
 //   d = amax / 127 over the block, code = rint(x / d), value = code * d.
 // A block that held tokens before keeps the larger of its scale and the new tokens'; where it grows,
 // the earlier codes are coded again as rint(code * d_old / d).
+#include <algorithm>
+
 #include <hip/hip_runtime.h>
 
 #include "qg_device.hpp"
@@ -108,6 +110,11 @@ __device__ __forceinline__ Item kv8_item(const KvCache& c, const KvSpan& sp, int
     return t;
 }
 
+// This wavefront's item; group0: the launch's first workgroup.
+__device__ __forceinline__ int wave_item(uint32_t group0) {
+    return (int)((group0 + blockIdx.x) * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
+}
+
 // One wavefront codes one block of one head, K or V.  It holds the block in registers (16 dim values),
 // so the new tokens are read once and nothing goes through shared memory:
 //   K  a lane takes 16 dims of a token (16 codes = the 16 bytes that lie together in the cache);
@@ -118,9 +125,9 @@ __device__ __forceinline__ Item kv8_item(const KvCache& c, const KvSpan& sp, int
 // its loads: 13 x 701 f32 tokens of 5 heads of 96 9.2 -> 8.7 us.
 template <int XT, int D>
 __global__ __launch_bounds__(64 * kWaves) void kv8_write_kernel(KvCache c, KvSeqs q, const void* k, const void* v,
-                                                                KvStrides st) {
+                                                                KvStrides st, uint32_t group0) {
     const int lane = threadIdx.x & 63, s = blockIdx.y;
-    const Item t = kv8_item(c, kv8_span(q, s), blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
+    const Item t = kv8_item(c, kv8_span(q, s), wave_item(group0));
     if (t.none) return;
     const bool begun = t.j0 > 0;
     if (!t.is_v) {
@@ -238,9 +245,10 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 // layout of the write kernel, so the stores of a token are one contiguous run.  Bound as the write kernel:
 // 24576 tokens back as bf16 in 25 us (6 TB/s, the codes are still in the cache), 48 tokens in 4.2 us.
 template <int YT, int D>
-__global__ __launch_bounds__(64 * kWaves) void kv8_read_kernel(KvCache c, KvSeqs q, void* k, void* v, KvStrides st) {
+__global__ __launch_bounds__(64 * kWaves) void kv8_read_kernel(KvCache c, KvSeqs q, void* k, void* v, KvStrides st,
+                                                               uint32_t group0) {
     const int lane = threadIdx.x & 63, s = blockIdx.y;
-    const Item t = kv8_item(c, kv8_span(q, s), blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
+    const Item t = kv8_item(c, kv8_span(q, s), wave_item(group0));
     if (t.none) return;
     const int bi = kv8_block(c, q, s, t.h, t.blk);
     const float d = bi < 0 ? 0.f : (t.is_v ? c.vs : c.ks)[bi];  // no page: zeros
@@ -300,11 +308,14 @@ template <int XT, int D>
 void launch_one(bool write, const KvCache& c, const KvSeqs& q, void* k, void* v, const KvStrides& st, hipStream_t s) {
     // blocks that n consecutive tokens touch at most
     const int nblk = (q.max_new + 30) / 16;
-    const dim3 grid((uint32_t)(((int64_t)nblk * 2 * c.heads + kWaves - 1) / kWaves), q.seqs);
-    if (write)
-        kv8_write_kernel<XT, D><<<grid, 64 * kWaves, 0, s>>>(c, q, k, v, st);
-    else
-        kv8_read_kernel<XT, D><<<grid, 64 * kWaves, 0, s>>>(c, q, k, v, st);
+    const int64_t groups = ((int64_t)nblk * 2 * c.heads + kWaves - 1) / kWaves;
+    for (int64_t first = 0; first < groups; first += kLaunchGroups) {
+        const dim3 grid((uint32_t)std::min(groups - first, kLaunchGroups), q.seqs);
+        if (write)
+            kv8_write_kernel<XT, D><<<grid, 64 * kWaves, 0, s>>>(c, q, k, v, st, (uint32_t)first);
+        else
+            kv8_read_kernel<XT, D><<<grid, 64 * kWaves, 0, s>>>(c, q, k, v, st, (uint32_t)first);
+    }
 }
 
 template <int XT>

@@ -1,11 +1,11 @@
 """The 8-bit serving operators where a call's bounds ask for more workgroups than one launch may have (a launch counts
 its work items in 32 bits): the same results as under tight bounds."""
-import numpy as np
 import pytest
 import torch
 
 import block_quantized_weight_affine_amd as qg
-from test_gpu_serve8 import TYPES, Batch, _attend, _dev, _values
+from oracle import serve8
+from test_gpu_serve8 import TYPES, Batch, _attend, _check_cache, _dev, _values
 from test_gpu_serve8_scales import _check
 
 pytestmark = pytest.mark.gpu
@@ -54,3 +54,17 @@ def test_attend_refuses_more_rows_than_it_counts():
         assert e.value.status == qg.QG_ESHAPE
         assert torch.all(o == 3)
     assert qg.qg_attn_kv8_workspace(b.cache, seqs, 64) == 0
+
+def test_write_past_one_launch():
+    """A bound of 2^19 new tokens of 1024 heads: 2^24 workgroups.  The rows are one row, repeated by a stride of 0."""
+    print("kv8 write: 2^24 workgroups", flush=True)
+    b = Batch([(40, 57), (1, 1)], 1024, 64, 16, 64).upload()
+    T = 1 << 19
+    one = _values(b.rng, (2, 1024, 64), "f16")
+    k, v = (x.cuda()[None].expand(T, 1024, 64) for x in one)
+    seqs = qg.kv8_seqs(_dev(b.table), _dev(b.rows), _dev(b.kv_len), T, T, T)
+    qg.qg_kv8_write(b.cache, seqs, k, v)
+    for x, codes, scales in zip(one, (b.kc, b.vc), (b.ks, b.vs)):
+        serve8.kv8_write(codes, scales, b.table, b.spans(), x.float().numpy()[None].repeat(b.T, 0))
+    torch.cuda.synchronize()
+    _check_cache(b, None, None)
