@@ -460,11 +460,14 @@ def kv8_seqs(table, rows, kv_len, T, max_new, max_kv):
 
 
 _entries = {}
+_int8 = None
 
 
 def _entry(name):
     """An entry point, looked up once: these calls are made a few at a time for microseconds of work."""
     import torch
+    global _int8
+    _int8 = torch.int8
     _XT.update({torch.float32: QG_X_F32, torch.float16: QG_X_F16, torch.bfloat16: QG_X_BF16})
     _entries[name] = call = getattr(lib(), name)
     return call
@@ -531,7 +534,7 @@ def qgemm_w8a8(w_codes, w_scales, X, Y, N, K, T, workspace=None, stream=None):
     qgemm_w8a8_workspace bytes."""
     call = _entries.get("qgemm_w8a8") or _entry("qgemm_w8a8")
     xt, yt = _XT.get(X.dtype), _XT.get(Y.dtype)
-    if xt is None or yt is None or w_codes.itemsize != 1 or w_scales.itemsize != 4:
+    if xt is None or yt is None or w_codes.dtype is not _int8 or _XT.get(w_scales.dtype) != QG_X_F32:
         raise QGError(QG_EINVAL, "qgemm_w8a8")
     if X.numel() < T * K or Y.numel() < T * N or w_codes.numel() < N * K or w_scales.numel() < N:
         raise QGError(QG_ESHAPE, "qgemm_w8a8")
