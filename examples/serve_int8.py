@@ -58,10 +58,11 @@ class Model:
         self.head = Linear(vocab, hidden, gen)
 
     def workspace(self, seqs):
-        """Bytes that one call needs at most; they follow each other on one stream and share the buffer."""
+        """A buffer of the bytes that one call needs at most; they follow each other on one stream and share it.  Each
+        call's own number of rows counts: fewer of them can need more."""
         sizes = [qg.qg_attn_kv8_workspace(self.layers[0][0], seqs, self.q_heads)]
-        for m in list(self.layers[0][1:]) + [self.head]:
-            sizes.append(qg.qgemm_w8a8_workspace(m.N, m.K, seqs.T))
+        for m, rows in [(m, seqs.T) for m in self.layers[0][1:]] + [(self.head, self.users)]:
+            sizes.append(qg.qgemm_w8a8_workspace(m.N, m.K, rows))
         return torch.empty(max(sizes + [16]), dtype=torch.uint8, device="cuda")
 
     def __call__(self, tokens, seqs, last, work):

@@ -514,7 +514,8 @@ qg_status qg_kv8_read(const qg_kv8_cache* cache, const qg_kv8_seqs* seqs, void* 
                       hipStream_t stream);
 
 /* Bytes of workspace that qg_attn_kv8 needs for these descriptors and q_heads, whatever its mask (0: none,
- * or arguments that it would refuse). */
+ * or arguments that it would refuse).  Smaller bounds can need more (more splits of the tokens): a buffer
+ * for several calls has the largest of their sizes. */
 size_t qg_attn_kv8_workspace(const qg_kv8_cache* cache, const qg_kv8_seqs* seqs, int q_heads);
 
 /* Attention of the rows q [T][q_heads][dim] over the cache, o of the same shape and type.  Head h reads K/V
@@ -542,7 +543,8 @@ qg_status qg_attn_kv8(const qg_kv8_cache* cache, const qg_kv8_seqs* seqs, const 
  * row-major.  The integer sum is exact.  A NaN or infinity in a row of X makes that row of Y NaN.
  * 1 <= N <= 2^24, 16 <= K <= 2^17, K % 16 == 0, 0 <= T <= 2^21, else QG_ESHAPE; T = 0: QG_OK; w_codes, X
  * and workspace 16-byte aligned, w_scales 4, Y its element's size, else QG_EALIGN; null pointers or
- * unknown types QG_EINVAL; QG_EWORKSPACE if ws_bytes < qgemm_w8a8_workspace(N, K, T).  Asynchronous. */
+ * unknown types QG_EINVAL; QG_EWORKSPACE if ws_bytes < qgemm_w8a8_workspace(N, K, T), which can fall as T grows: a
+ * buffer for several calls has the largest of their sizes.  Asynchronous. */
 size_t qgemm_w8a8_workspace(int N, int K, int T);
 qg_status qgemm_w8a8(const int8_t* w_codes, const float* w_scales, const void* X, qg_xtype xt, void* Y,
                      qg_xtype yt, int N, int K, int T, void* workspace, size_t ws_bytes,
