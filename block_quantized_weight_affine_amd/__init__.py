@@ -147,13 +147,16 @@ _raw_stream = None
 def _stream(stream):
     if stream is None:
         # the current device's current stream as an address; torch.cuda.current_stream() builds an object
-        # around it first, 1 us that a launch of a few does not have
+        # around it first, 1 us that a launch of a few does not have, but a torch without the two calls has that
         global _raw_stream
         if _raw_stream is None:
             import torch
             torch.cuda.current_stream()  # initialises the device
-            get, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-            _raw_stream = lambda: get(device())  # noqa: E731
+            get, device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+            if get and device:
+                _raw_stream = lambda: get(device())  # noqa: E731
+            else:
+                _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
         return _raw_stream()
     if isinstance(stream, int):
         return stream

@@ -52,3 +52,19 @@ def test_the_example_sizes_every_call(monkeypatch, vocab, hidden, users, lengths
     assert size >= qg.qg_attn_kv8_workspace(cache, seqs, model.q_heads)
     assert size >= max(qg.qgemm_w8a8_workspace(m.N, m.K, seqs.T) for m in products)
     assert size >= qg.qgemm_w8a8_workspace(vocab, hidden, users)
+
+
+@pytest.mark.parametrize("missing", [(), ("_cuda_getCurrentRawStream",), ("_cuda_getDevice",)])
+def test_the_current_stream_without_torch_internals(monkeypatch, missing):
+    """A torch that lacks the calls behind the current stream's address still gives it, by its public ones."""
+    class Stream:
+        cuda_stream = 4096
+    monkeypatch.setattr(torch.cuda, "current_stream", Stream)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 4096 if device == 3 else 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 3, raising=False)
+    for name in missing:
+        monkeypatch.delattr(torch._C, name)
+    monkeypatch.setattr(qg, "_raw_stream", None)
+    assert qg._stream(None) == 4096
+    assert qg._stream(None) == 4096
+    assert qg._stream(17) == 17 and qg._stream(Stream()) == 4096
