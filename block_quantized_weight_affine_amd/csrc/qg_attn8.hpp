@@ -20,8 +20,10 @@ constexpr float kNegInf = -__builtin_inff();
 //   w = exp2(s + log2(vs 2^-e0) - m + kBase),  m a running maximum of what stands before it in the row,
 // and the denominator takes w times the reciprocal, so a row's precision is set by the blocks that it sees
 // and by no others.  m may lag by kLag before the sums are rescaled: weights stay at or below 2^15 and keep
-// f16's full precision down to 2^-23 of the row's largest.  e0, an exponent of V scales near by, keeps the powers
-// small.
+// f16's full precision down to 2^-23 of the row's largest.  16-bit rows take one f16 piece of a weight, f32 rows
+// two: an error of at most 2^-11 (2^-22) of the weighted mean of |v|, where values do not cancel no more than the
+// rounding of an f16 result, and one piece halves the second product.  e0, an exponent of V scales near by, keeps the
+// powers small.
 constexpr float kLag = 6.f;
 constexpr int kBase = 9;
 // kBase - m; before a row has a maximum, kBase.
@@ -79,7 +81,8 @@ __device__ __forceinline__ float v_power(float vs, int e0) {
 __device__ __forceinline__ float v_power_rest(float vs, int e0, float lv) {
     if (lv == kNegInf) return 0.f;
     const float va = fabsf(vs);
-    return ((float)(__builtin_amdgcn_frexp_expf(va) - e0) - lv) + __builtin_amdgcn_logf(__builtin_amdgcn_frexp_mantf(va));
+    const float whole = (float)(__builtin_amdgcn_frexp_expf(va) - e0);
+    return (whole - lv) + __builtin_amdgcn_logf(__builtin_amdgcn_frexp_mantf(va));
 }
 // A far block's weights say nothing about its part of the denominator: it has an own sum for that, FarSum, and the
 // factor 0 in the other.  Far are V scales of 0, whose tokens weigh nothing in the numerator (whatever they score, the

@@ -522,12 +522,13 @@ size_t qg_attn_kv8_workspace(const qg_kv8_cache* cache, const qg_kv8_seqs* seqs,
  * head h / (q_heads / heads).  A row at position p of its sequence (the rows are its last tokens) sees the
  * tokens j with j <= p if causal, and p - window < j if window > 0:
  *     o = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale * q . k_j);  a row that sees nothing gets 0.
- * Products of the exact codes with q, sums, maxima and weights are in f32; q (f16 / bf16 exactly, f32 in
- * two pieces of 11 bits) and the weights times their V scale (rounded to f16; for f32 rows in two pieces)
- * feed f16 matrix instructions.  The V scales that one row sees may lie up to 2^100 apart.  A row that sees
- * a block whose K or V scale is NaN or infinite is NaN; what a row does not see never reaches it.  Single
- * tokens, drafts and whole prompts take the same call.  The order of the sums is fixed: results repeat bit
- * for bit.
+ * Products of the exact codes with q, sums, maxima and weights are in f32; q (f32 in two pieces of 11 bits;
+ * f16 and bf16 exactly, but elements below 2^-28 of their row's largest to 2^-39 of it) and the weights times
+ * their V scale (rounded to f16; for f32 rows in two pieces) feed f16 matrix instructions.  The V scales that
+ * one row sees may lie up to 2^100 apart, with scales of 0 among them.  A row that sees a block whose K or V
+ * scale is NaN or infinite is NaN; what a row does not see never reaches it.  Single tokens, drafts and whole
+ * prompts take the same call.  Kernel and splits follow the bounds: results repeat bit for bit under the same
+ * ones, and speed is best under tight ones.
  * q_heads a multiple of heads, <= 65536, max_new * q_heads < 2^31, seqs * max_new * q_heads < 2^37, else
  * QG_ESHAPE; strides as in qg_kv8_write (o as an output); workspace 16-byte aligned, QG_EWORKSPACE if NULL or
  * too small.  It needs no initialisation; calls that overlap in time need one each. */
