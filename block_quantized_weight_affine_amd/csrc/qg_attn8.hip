@@ -45,7 +45,7 @@ constexpr bool rows_late(int pieces, int dim) { return rows_registers(pieces, di
 // instructions' rate for G <= 16: bound by memory.  3 x 200002 tokens, 64 heads of 128 on 8: 219 us, 5.6 TB/s
 // of the 1.23 GB that it cannot do without (a copy of this card: 4.8 TB/s read and written); 64 users of up
 // to 8192 tokens: 105 us, 4.7 TB/s.  Short calls are bound by the chain of loads (lengths, table, codes) and
-// the decoding of one wavefront: 1024 tokens of one user 8.9 us.  Splits that end their own kernel cost 4 us.
+// the decoding of one wavefront: 1024 tokens of one user 9.0 us.  Splits that end their own kernel cost 4 us.
 template <int XT, int D, int W>
 __global__ __launch_bounds__(64 * W, W == 4 && rows_registers(XT == XT_F32 ? 2 : 1, D) <= 128 ? 3 : 2) void attn8_rows_kernel(AttnParams a) {
     constexpr int NP = XT == XT_F32 ? 2 : 1;  // f16 pieces of a q value and of a weight
