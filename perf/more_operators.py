@@ -76,7 +76,7 @@ def draw(rng):
     xt = rng.choice(["f32", "f16", "bf16"])
     if op == "plan":
         return dict(op=op, seqs=_log(rng, 1, 64), nodes=_log(rng, 2, 256), ragged=rng.random() < 0.5,
-                    hist=_log(rng, 1, 100000), wide=rng.randint(1, 8), window=0 if rng.random() < 0.6 else _log(rng, 1, 64),
+                    hist=_log(rng, 1000, 100000), wide=rng.randint(1, 8), window=0 if rng.random() < 0.6 else _log(rng, 1, 64),
                     lens=lens)
     if op == "verify":
         tree = rng.random() < 0.5
@@ -231,6 +231,9 @@ def prepare(case, seed):
         st["y"] = torch.empty(st["x"].shape, dtype=st["x"].dtype, device="cuda")
         return st
     new, hist = _lengths(dict(c, hist=c.get("hist", 3000)))
+    if c["op"] == "plan":
+        lens = random.Random(seed)
+        st["hist"] = hist = [lens.randint(0, c["hist"]) for _ in hist]
     total = [a + b for a, b in zip(new, hist)]
     T = sum(new)
     st.update(rows=_ints(_offsets(new)), kv_len=_ints(total), T=T, max_new=max(new), max_kv=max(total))
@@ -733,10 +736,10 @@ def _exact_tree(st):
 
 def _exact_plan(st):
     c = st["case"]
-    new, hist = _lengths(c)
+    new, _ = _lengths(c)
     words = -(-max(new) // 32)
     masks, pos = [], []
-    for n, h, par in zip(new, hist, st["trees"]):
+    for n, h, par in zip(new, st["hist"], st["trees"]):
         lines = []
         for r, p in enumerate(par):
             lines.append(([] if p < 0 else lines[p]) + [r])
