@@ -38,6 +38,8 @@ SYMBOLS = [
     "qg_moe_plan_host", "qg_moe_plan", "qg_x_half", "qg_x_half_guard", "qgemm_moe_grouped", "qg_swiglu", "qg_moe_combine",
     "qg_moe_ffn_workspace", "qg_moe_ffn", "qg_moe_ffn_noalloc",
     "qg_kv8_write", "qg_kv8_read", "qg_attn_kv8_workspace", "qg_attn_kv8", "qgemm_w8a8_workspace", "qgemm_w8a8",
+    "qg_rope_freqs", "qg_rope", "qg_kv8_write_rope", "qg_tree_plan", "qg_attn_kv8_tree", "qg_draft_verify_workspace",
+    "qg_draft_verify",
 ]
 
 
@@ -102,7 +104,16 @@ def lib() -> C.CDLL:
         L.qg_attn_kv8.argtypes = [_p, _p, _p, _i64, _i64, _p, _i64, _i64, _i, _i, C.c_float, _i, _i, _p, _sz, _p]
         L.qgemm_w8a8_workspace.argtypes = [_i, _i, _i]
         L.qgemm_w8a8.argtypes = [_p, _p, _p, _i, _p, _i, _i, _i, _i, _p, _sz, _p]
-        for name in ("qg_attn_kv8_workspace", "qgemm_w8a8_workspace"):
+        _d = C.c_double
+        L.qg_rope_freqs.argtypes = [_i, _i, _d, _d, _d, _d, _d, _p, _p]
+        L.qg_rope.argtypes = [_p, _p, _p, _i64, _i64, _p, _i64, _i64, _i, _i, _i, _i, _p]
+        L.qg_kv8_write_rope.argtypes = [_p, _p, _p, _p, _p, _i64, _i64, _p, _i64, _i64, _p, _i, _p, _i64, _i64, _p, _i64,
+                                        _i64, _i, _i, _p]
+        L.qg_tree_plan.argtypes = [_p, _p, _p, _i, _p, _i, _p]
+        L.qg_attn_kv8_tree.argtypes = [_p, _p, _p, _i, _p, _p, _i64, _i64, _p, _i64, _i64, _i, _i, C.c_float, _i, _p, _sz, _p]
+        L.qg_draft_verify_workspace.argtypes = [_p, _i]
+        L.qg_draft_verify.argtypes = [_p, _p, _p, _p, _i64, _p, _i64, _i, _i, _p, _p, _p, _p, _p, _p, _p, _p, _p, _sz, _p]
+        for name in ("qg_attn_kv8_workspace", "qgemm_w8a8_workspace", "qg_draft_verify_workspace"):
             getattr(L, name).restype = _sz
         for name in SYMBOLS:
             if name not in ("qg_strerror", "qg_abi_version") and not name.endswith("_workspace"):
@@ -463,14 +474,14 @@ def kv8_seqs(table, rows, kv_len, T, max_new, max_kv):
 
 
 _entries = {}
-_int8 = None
+_int8 = _int32 = None
 
 
 def _entry(name):
     """An entry point, looked up once: these calls are made a few at a time for microseconds of work."""
     import torch
-    global _int8
-    _int8 = torch.int8
+    global _int8, _int32
+    _int8, _int32 = torch.int8, torch.int32
     _XT.update({torch.float32: QG_X_F32, torch.float16: QG_X_F16, torch.bfloat16: QG_X_BF16})
     _entries[name] = call = getattr(lib(), name)
     return call
@@ -548,6 +559,193 @@ def qgemm_w8a8(w_codes, w_scales, X, Y, N, K, T, workspace=None, stream=None):
                   _stream(stream))
     if status:
         raise QGError(status, "qgemm_w8a8")
+
+
+# ---- drafted tokens over the 8-bit cache ------------------------------------------------------------
+ROPE = {None: 0, "plain": 0, "linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
+
+
+class QgRotary(C.Structure):
+    """qg_rotary of qgemm.h."""
+    _fields_ = [("freqs", C.c_void_p), ("rot", C.c_int), ("interleaved", C.c_int), ("mscale", C.c_float)]
+
+
+def rope_freqs(rot, base=10000.0, scaling=None, factor=1.0, context=0.0, low=1.0, high=32.0):
+    """Frequencies of rotary positions (numpy f64 [rot / 2], radians a position) and the factor mscale; scaling: None,
+    "linear", "ntk", "bands" or "yarn" (qg_rope_freqs in qgemm.h)."""
+    freqs, mscale = np.empty(max(0, rot // 2), np.float64), C.c_float()
+    kind = ROPE.get(scaling, scaling if isinstance(scaling, int) else -1)
+    _check(lib().qg_rope_freqs(kind, rot, base, factor, context, low, high, freqs.ctypes.data, C.addressof(mscale)),
+           "qg_rope_freqs")
+    return freqs, mscale.value
+
+
+def rotary(freqs, interleaved=False, mscale=1.0):
+    """Descriptor of rotary positions over a contiguous f64 device tensor of rot / 2 frequencies (None: nothing is turned).
+    Keep it as long as it is used."""
+    import torch
+    if freqs is None:
+        return _Desc(QgRotary(None, 0, 0, 1.0), ())
+    _expect(freqs.dtype == torch.float64 and freqs.dim() == 1 and freqs.is_contiguous(), "rotary")
+    return _Desc(QgRotary(freqs.data_ptr(), 2 * freqs.numel(), int(bool(interleaved)), mscale), (freqs,))
+
+
+def _ints(where, n, *tensors):
+    """Contiguous int32 tensors of at least n values."""
+    for x in tensors:
+        if x is not None:
+            if x.dtype is not _int32:
+                raise QGError(QG_EINVAL, where)
+            if x.numel() < n:
+                raise QGError(QG_ESHAPE, where)
+            if not x.is_contiguous():
+                raise QGError(QG_EALIGN, where)
+
+
+def _floats(where, n, *tensors):
+    """Contiguous f32 tensors of at least n values."""
+    for x in tensors:
+        if x is not None:
+            if _XT.get(x.dtype) != QG_X_F32:
+                raise QGError(QG_EINVAL, where)
+            if x.numel() < n:
+                raise QGError(QG_ESHAPE, where)
+            if not x.is_contiguous():
+                raise QGError(QG_EALIGN, where)
+
+
+def qg_rope(rot, pos, x, y, stream=None):
+    """x [T][heads][dim] (any row and head strides) at positions pos [T] turned into y, which may be x."""
+    call = _entries.get("qg_rope") or _entry("qg_rope")
+    xt = x.dtype
+    if xt is not y.dtype or xt not in _XT:
+        raise QGError(QG_EINVAL, "qg_rope")
+    if x.dim() != 3 or x.shape != y.shape:
+        raise QGError(QG_ESHAPE, "qg_rope")
+    T, heads, dim = x.shape
+    _ints("qg_rope", T, pos)
+    x_row, x_head, x_one = x.stride()
+    y_row, y_head, y_one = y.stride()
+    if x_one != 1 or y_one != 1:
+        raise QGError(QG_EALIGN, "qg_rope")
+    status = call(rot.ptr, pos.data_ptr(), x.data_ptr(), x_row, x_head, y.data_ptr(), y_row, y_head, _XT[xt], T, heads, dim,
+                  _stream(stream))
+    if status:
+        raise QGError(status, "qg_rope")
+
+
+def qg_kv8_write_rope(cache, seqs, rot, k, v, q=None, q_out=None, pos=None, src=None, stream=None):
+    """qg_kv8_write with K turned on the way; q [T][q_heads][dim] is turned into q_out beside it.  pos [T]: positions other
+    than the rows' places; src [T]: row r is row src[r] of k and v, which then have any number of rows."""
+    where = "qg_kv8_write_rope"
+    call = _entries.get(where) or _entry(where)
+    xt, rows, inner = k.dtype, k.shape[0], (cache.heads, cache.dim)
+    if xt is not v.dtype or xt not in _XT:
+        raise QGError(QG_EINVAL, where)
+    if k.shape[1:] != inner or v.shape != k.shape or (src is None and rows != seqs.T):
+        raise QGError(QG_ESHAPE, where)
+    if pos is not None or src is not None:
+        _ints(where, seqs.T, pos, src)
+    k_row, k_head, k_one = k.stride()
+    v_row, v_head, v_one = v.stride()
+    if k_one != 1 or v_one != 1:
+        raise QGError(QG_EALIGN, where)
+    qs = (None, 0, 0, None, 0, 0, 0)
+    if q is not None:
+        if q_out is None or q.dtype is not xt or q_out.dtype is not xt:
+            raise QGError(QG_EINVAL, where)
+        if q.dim() != 3 or q.shape != q_out.shape or q.shape[0] != seqs.T or q.shape[2] != cache.dim or q.shape[1] == 0:
+            raise QGError(QG_ESHAPE, where)
+        q_row, q_head, q_one = q.stride()
+        o_row, o_head, o_one = q_out.stride()
+        if q_one != 1 or o_one != 1:
+            raise QGError(QG_EALIGN, where)
+        qs = (q.data_ptr(), q_row, q_head, q_out.data_ptr(), o_row, o_head, q.shape[1])
+    status = call(cache.ptr, seqs.ptr, rot.ptr, None if pos is None else pos.data_ptr(), k.data_ptr(), k_row, k_head,
+                  v.data_ptr(), v_row, v_head, None if src is None else src.data_ptr(), rows, *qs, _XT[xt], _stream(stream))
+    if status:
+        raise QGError(status, where)
+
+
+def _masks(where, seqs, mask):
+    """Words of a mask [T][words]."""
+    if mask.dtype is not _int32:
+        raise QGError(QG_EINVAL, where)
+    if mask.dim() != 2 or mask.shape[0] < seqs.T:
+        raise QGError(QG_ESHAPE, where)
+    if not mask.is_contiguous():
+        raise QGError(QG_EALIGN, where)
+    return mask.shape[1]
+
+
+def qg_tree_plan(seqs, parents, mask, pos, window=0, stream=None):
+    """Masks (int32 [T][words]) and positions (int32 [T]) of a batch of trees from their parents [T]."""
+    call = _entries.get("qg_tree_plan") or _entry("qg_tree_plan")
+    words = _masks("qg_tree_plan", seqs, mask)
+    _ints("qg_tree_plan", seqs.T, parents, pos)
+    status = call(seqs.ptr, parents.data_ptr(), mask.data_ptr(), words, pos.data_ptr(), window, _stream(stream))
+    if status:
+        raise QGError(status, "qg_tree_plan")
+
+
+def qg_attn_kv8_tree(cache, seqs, mask, q, o, q_heads, scale, window=0, pos=None, workspace=None, stream=None):
+    """Attention of q [T][q_heads][dim] over the cache into o, the batch's rows seeing each other by mask (int32
+    [T][words]); pos [T] is read with a window alone.  Workspace as for qg_attn_kv8."""
+    where = "qg_attn_kv8_tree"
+    call = _entries.get(where) or _entry(where)
+    xt, shape = q.dtype, (seqs.T, q_heads, cache.dim)
+    if xt is not o.dtype or xt not in _XT:
+        raise QGError(QG_EINVAL, where)
+    if q.shape != shape or o.shape != shape:
+        raise QGError(QG_ESHAPE, where)
+    words = _masks(where, seqs, mask)
+    if pos is not None:
+        _ints(where, seqs.T, pos)
+    q_row, q_head, q_one = q.stride()
+    o_row, o_head, o_one = o.stride()
+    if q_one != 1 or o_one != 1:
+        raise QGError(QG_EALIGN, where)
+    wp, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    status = call(cache.ptr, seqs.ptr, mask.data_ptr(), words, None if pos is None else pos.data_ptr(), q.data_ptr(), q_row,
+                  q_head, o.data_ptr(), o_row, o_head, _XT[xt], q_heads, scale, window, wp, size, _stream(stream))
+    if status:
+        raise QGError(status, where)
+
+
+def qg_draft_verify_workspace(seqs, vocab) -> int:
+    return int(lib().qg_draft_verify_workspace(seqs.ptr, vocab))
+
+
+def qg_draft_verify(seqs, tokens, target, accepted, next, rows_out, path, kv_out, sample=None, temps=None, parents=None,
+                    draft=None, accept=None, workspace=None, stream=None):
+    """Which drafted tokens [T] stay by the logits target [T][vocab], and what follows them: accepted, next and kv_out
+    [seqs], rows_out [seqs + 1], path [T] (int32).  draft: the logits that the tokens were drawn from, with accept [T]; None:
+    they were chosen.  sample [T] (f32; None: the largest logit throughout), temps [seqs] (f32; None: 1), parents [T] (None:
+    chains); workspace: a device tensor of at least qg_draft_verify_workspace bytes."""
+    where = "qg_draft_verify"
+    call = _entries.get(where) or _entry(where)
+    xt, T, n = target.dtype, seqs.T, seqs.struct.seqs
+    if xt not in _XT or (draft is not None and draft.dtype is not xt):
+        raise QGError(QG_EINVAL, where)
+    if target.dim() != 2 or target.shape[0] < T or (draft is not None and draft.shape != target.shape):
+        raise QGError(QG_ESHAPE, where)
+    t_row, one = target.stride()
+    d_row, d_one = (0, 1) if draft is None else draft.stride()
+    if one != 1 or d_one != 1:
+        raise QGError(QG_EALIGN, where)
+    _ints(where, T, tokens, path, parents)
+    _ints(where, n, accepted, next, kv_out)
+    _ints(where, n + 1, rows_out)
+    _floats(where, T, sample, accept)
+    _floats(where, n, temps)
+    wp, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    status = call(seqs.ptr, None if parents is None else parents.data_ptr(), tokens.data_ptr(), target.data_ptr(), t_row,
+                  None if draft is None else draft.data_ptr(), d_row, _XT[xt], target.shape[1],
+                  None if temps is None else temps.data_ptr(), None if accept is None else accept.data_ptr(),
+                  None if sample is None else sample.data_ptr(), accepted.data_ptr(), next.data_ptr(), rows_out.data_ptr(),
+                  path.data_ptr(), kv_out.data_ptr(), wp, size, _stream(stream))
+    if status:
+        raise QGError(status, where)
 
 
 # ---- host layout helpers (byte movement only) ----------------------------------------------------

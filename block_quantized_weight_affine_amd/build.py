@@ -13,8 +13,9 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libqgemm.so")
 OBJ = os.path.join(HERE, "_build")
-SOURCES = ["qg_gemm.hip", "qg_gemv.hip", "qg_moe.hip", "qg_misc.hip", "qg_kv8.hip", "qg_attn8.hip", "qg_attn8_tile.hip",
-           "qg_w8a8.hip", "qg_capi.cpp", "qg_capi8.cpp"]
+SOURCES = ["qg_gemm.hip", "qg_gemv.hip", "qg_moe.hip", "qg_misc.hip", "qg_kv8.hip", "qg_kv8_rope.hip", "qg_attn8.hip",
+           "qg_attn8_tile.hip", "qg_attn8_tree.hip", "qg_attn8_tree_tile.hip", "qg_draft.hip", "qg_w8a8.hip", "qg_capi.cpp",
+           "qg_capi8.cpp"]
 ARCH = os.environ.get("QG_OFFLOAD_ARCH", "gfx950")
 
 FLAGS = [
@@ -28,7 +29,7 @@ FLAGS = [
 # the attention kernels' sums stay in vector registers, where the softmax works on them, as far as those go: 16-bit
 # tiles with heads of 192 and 256 and f32 tiles from 96 on keep 10 to 220 of theirs in accumulation registers
 _SUMS = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
-EXTRA = {"qg_attn8.hip": _SUMS, "qg_attn8_tile.hip": _SUMS}
+EXTRA = {src: _SUMS for src in ("qg_attn8.hip", "qg_attn8_tile.hip", "qg_attn8_tree.hip", "qg_attn8_tree_tile.hip")}
 
 
 def _compile(src: str) -> str:

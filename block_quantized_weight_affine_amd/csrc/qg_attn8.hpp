@@ -136,15 +136,51 @@ __device__ __forceinline__ int v_exponent(float vs) {
     return va > 0.f && va < __builtin_inff() ? (int)(__float_as_uint(va) >> 23) - 126 : -1000;
 }
 
+// Tokens [lo, hi) that row i of a sequence sees.  TREE: those before the batch's rows; of these it sees the ones that
+// its mask has.
+template <bool TREE>
+__device__ __forceinline__ KvSight row_sight(const AttnParams& a, const KvSpan& sp, int i) {
+    if constexpr (!TREE) return kv8_sight(sp, i, a.causal, a.window);
+    const int hist = sp.len - sp.n;
+    int p = sp.len - 1;
+    if (a.window > 0) p = min(max(a.pos[sp.r0 + i], hist), sp.len - 1);
+    return KvSight{a.window > 0 ? max(p - a.window + 1, 0) : 0, hist};
+}
+// The same for the first or last row of some, so that every one of them sees lo and what follows it from `last` on, and
+// none sees what lies before `first`'s lo.  A tree's rows have positions in no order.
+template <bool TREE>
+__device__ __forceinline__ KvSight edge_sight(const AttnParams& a, const KvSpan& sp, int i, bool last) {
+    if constexpr (!TREE) return kv8_sight(sp, i, a.causal, a.window);
+    const int hist = sp.len - sp.n, p = last ? sp.len - 1 : hist;
+    return KvSight{a.window > 0 ? max(p - a.window + 1, 0) : 0, hist};
+}
+// Ones at lo .. hi - 1, limited to 16 and to 64 bits.
+__device__ __forceinline__ uint32_t bits_between(int lo, int hi) {
+    const uint32_t below = (1u << min(max(lo, 0), 16)) - 1, upto = (1u << min(max(hi, 0), 16)) - 1;
+    return upto & ~below;
+}
+__device__ __forceinline__ uint64_t ones64(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; }
+__device__ __forceinline__ uint64_t bits_between64(int lo, int hi) { return ones64(hi) & ~ones64(lo); }
+// Which of the tokens t .. t + 63 row i sees by its mask: bit j for token t + j.
+__device__ __forceinline__ uint64_t drafted_bits(const AttnParams& a, const KvSpan& sp, int i, int t) {
+    const int off = t - (sp.len - sp.n), w = off >> 5, sh = off & 31;  // row of token t, in words and bits
+    const uint32_t* m = a.mask + (int64_t)(sp.r0 + i) * a.words;
+    auto word = [&](int x) { return (uint32_t)x < (uint32_t)a.words ? m[x] : 0u; };
+    const uint64_t lo = word(w) | (uint64_t)word(w + 1) << 32, hi = word(w + 2);
+    const uint64_t bits = sh ? lo >> sh | hi << (64 - sh) : lo;
+    return bits & ones64(sp.len - t);
+}
+
 // What the rows r0 .. r0 + rows - 1 of a tile see together, and how the splits divide it.
 struct TileRange {
     int lo, hi, nact;  // tokens [lo, hi), lo a multiple of 64; splits that have any of them
 };
+template <bool TREE>
 __device__ __forceinline__ TileRange tile_range(const AttnParams& a, const KvSpan& sp, int r0, int rows) {
     const int i0 = r0 / a.group, i1 = (min(r0 + rows, sp.n * a.group) - 1) / a.group;
     TileRange t;
-    t.lo = kv8_sight(sp, i0, a.causal, a.window).lo & ~63;
-    t.hi = kv8_sight(sp, i1, a.causal, a.window).hi;
+    t.lo = edge_sight<TREE>(a, sp, i0, false).lo & ~63;
+    t.hi = TREE ? sp.len : edge_sight<TREE>(a, sp, i1, true).hi;
     t.nact = (t.hi - t.lo + a.chunk - 1) / a.chunk;
     return t;
 }
@@ -162,5 +198,8 @@ __device__ __forceinline__ int q_exponent(uint32_t top) {
 // The kernel of tiles of 128 or 256 rows (qg_attn8_tile.hip), and which of them a call takes.
 int attn8_tile_rows(const AttnParams& a, int xt);
 hipError_t launch_attn8_tile(const AttnParams& a, int xt, hipStream_t s);
+// The same kernels with masks among the batch's rows.
+hipError_t launch_attn8_tree(const AttnParams& a, int xt, hipStream_t s);
+hipError_t launch_attn8_tree_tile(const AttnParams& a, int xt, hipStream_t s);
 
 }  // namespace qg

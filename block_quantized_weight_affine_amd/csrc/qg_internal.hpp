@@ -118,6 +118,62 @@ struct KvStrides {
 hipError_t launch_kv8(bool write, const KvCache& c, const KvSeqs& q, void* k, void* v, int xt, const KvStrides& st,
                       hipStream_t s);
 
+// Rotary positions: radians a position of each pair, of the first `rot` values of a head.
+struct Rotary {
+    const double* freqs;  // [rot / 2]
+    int rot, inter;
+    float mscale;
+};
+// Rows x [T][heads][dim] turned into y; the rest is set by the launcher: how a head's values are shared out, tokens a
+// workgroup.
+struct RopeRows {
+    const void* x;
+    void* y;
+    int64_t x_row, x_head, y_row, y_head;
+    int heads, units, mode, per;
+};
+hipError_t launch_rope(const RopeRows& a, const Rotary& r, const int32_t* pos, int T, int dim, int xt, hipStream_t s);
+// New tokens turned into the cache, row r from row src[r] (src NULL: r) of k and v, at positions pos (NULL: those in the
+// sequence); q's rows (q.x NULL: none) turned beside them.  kv_groups is set by the launcher.
+struct KvRope {
+    Rotary rot;
+    const void *k, *v;
+    KvStrides st;
+    const int32_t *pos, *src;
+    int src_rows;
+    RopeRows q;
+    int kv_groups;
+};
+hipError_t launch_kv8_rope(const KvCache& c, const KvSeqs& q, const KvRope& a, int xt, hipStream_t s);
+
+// Masks [T][words] and positions [T] of trees; window > 0: masks end that many rows up.
+hipError_t launch_tree_plan(const KvSeqs& q, const int32_t* parents, uint32_t* mask, int words, int32_t* pos, int window,
+                            hipStream_t s);
+
+// Drafted tokens against the target's probabilities.  Set by the launcher: elements a chunk of a row, chunks a row, and
+// the workspace's parts.
+struct VerifyPart {
+    double sum;  // of exp((l - top) / temperature) over a chunk; NaN where the chunk has a NaN
+    float top;
+    int at;      // the first index that holds it
+};
+struct VerifyParams {
+    KvSeqs q;
+    const int32_t *parents, *tokens;
+    const void *target, *draft;
+    int64_t t_row, d_row;
+    int xt, vocab;
+    const float *temps, *accept, *sample;
+    int32_t *accepted, *next, *rows_out, *path, *kv_out;
+    int chunk, chunks;
+    VerifyPart* part;     // [target, draft][T][chunks]
+    double* mass;         // [seqs][chunks]
+    int32_t *drawn, *line; // [T]
+    uint32_t* tickets;    // [seqs + 1]
+};
+size_t verify_workspace(const KvSeqs& q, int vocab);
+hipError_t launch_draft_verify(VerifyParams p, void* ws, hipStream_t s);
+
 struct AttnParams {
     KvCache c;
     KvSeqs q;
@@ -127,6 +183,9 @@ struct AttnParams {
     int q_heads, group;
     float scale;
     int causal, window;
+    const uint32_t* mask;                  // a tree's rows: [T][words], which of its sequence's rows each sees (or NULL)
+    const int32_t* pos;                    // and their positions, for the window
+    int words;
     int tile_rows, tiles, splits, chunk;   // rows a tile, tiles a K/V head, splits of the tokens, tokens a split
     int row_waves;                         // wavefronts a workgroup of 16 rows
     int first;                             // a launch's first workgroup

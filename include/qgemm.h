@@ -551,6 +551,105 @@ qg_status qgemm_w8a8(const int8_t* w_codes, const float* w_scales, const void* X
                      qg_xtype yt, int N, int K, int T, void* workspace, size_t ws_bytes,
                      hipStream_t stream);
 
+/* ==== Drafted tokens over the 8-bit cache ===========================================================
+ *
+ * A step that checks several drafted tokens of every sequence at once: rotary positions on the way into the cache
+ * (qg_kv8_write_rope), attention for chains (qg_attn_kv8) or trees (qg_tree_plan, qg_attn_kv8_tree), and the verification
+ * (qg_draft_verify), whose outputs are the batch that qg_kv8_write_rope takes to move a tree's accepted rows together.
+ *
+ * Rotary positions: of every head's values the first `rot` are turned in pairs i < rot / 2,
+ *     y_a = mscale (x_a cos t - x_b sin t),  y_b = mscale (x_b cos t + x_a sin t),  t = position * freqs[i],
+ * (a, b) = (2i, 2i + 1) if interleaved, else (i, i + rot / 2); values from rot on stay.  Angles are reduced in 64 bits, sines
+ * and cosines rounded to f32 (off by no more than 2^-22 and 2^-52 |t|), products in f32.  freqs: f64 [rot / 2] radians
+ * a position, device memory, 8-byte aligned (QG_EALIGN).  rot even, 0 .. dim (QG_ESHAPE); 0 turns nothing, freqs unused. */
+typedef struct {
+    const double* freqs;
+    int rot, interleaved;
+    float mscale;
+} qg_rotary;
+
+/* Frequencies on the HOST (freqs [rot / 2], host memory): f_i = base^(-2i / rot), scaled for contexts longer than the
+ * `context` that a model was trained on:
+ *   QG_ROPE_PLAIN   f_i
+ *   QG_ROPE_LINEAR  f_i / factor
+ *   QG_ROPE_NTK     of base * factor^(rot / (rot - 2))
+ *   QG_ROPE_BANDS   f_i s + f_i / factor (1 - s): s = (turns - low) / (high - low) limited to 0 .. 1, of the turns
+ *                   context f_i / 2 pi that the pair makes
+ *   QG_ROPE_YARN    the same with s = 1 - (i - a) / (b - a): a the pair that makes `high` turns, rounded down, b the one
+ *                   that makes `low`, rounded up, both limited to 0 .. rot - 1; mscale = 0.1 ln factor + 1
+ * mscale is 1 but for QG_ROPE_YARN.  rot even, 2 .. 1024 (NTK: from 4 on) else QG_ESHAPE; base > 1, factor >= 1, context > 0
+ * and 0 < low < high where they are used, else QG_EINVAL.  What a scaling does not use is not looked at. */
+typedef enum { QG_ROPE_PLAIN = 0, QG_ROPE_LINEAR = 1, QG_ROPE_NTK = 2, QG_ROPE_BANDS = 3, QG_ROPE_YARN = 4 } qg_rope_scaling;
+qg_status qg_rope_freqs(qg_rope_scaling scaling, int rot, double base, double factor, double context, double low,
+                        double high, double* freqs, float* mscale);
+
+/* Rows x [T][heads][dim] at positions pos [T] (int32, negative ones turn back) turned into y, rounded once to the type.
+ * y may be x with the same strides (else QG_ESHAPE) and must not overlap it otherwise.  dim a multiple of 8, 8 .. 1024;
+ * 1 <= heads <= 65536; 0 <= T <= 2^21; strides as in qg_kv8_write (y as an output); T = 0: QG_OK.  Asynchronous. */
+qg_status qg_rope(const qg_rotary* rot, const int32_t* pos, const void* x, int64_t x_row, int64_t x_head, void* y,
+                  int64_t y_row, int64_t y_head, qg_xtype xt, int T, int heads, int dim, hipStream_t stream);
+
+/* qg_kv8_write with the rows of K turned before they are coded (in f32, not rounded to xt on the way).
+ * pos [T]: each row's position for its angles, NULL: its place in its sequence; where a row is written goes by its place
+ * either way.  src [T]: row r is read from row src[r] of k and v, 0 .. src_rows - 1 (others are read as zeros), NULL: from
+ * row r.  q_heads > 0: the rows q [T][q_heads][dim] of the batch's sequences are turned into q_out too, as by qg_rope
+ * (q_out may be q); with src QG_EUNSUPPORTED; rows of no sequence are left as they were.  The rest as qg_kv8_write;
+ * src_rows 0 .. 2^21, q_heads 0 .. 65536 else QG_ESHAPE. */
+qg_status qg_kv8_write_rope(const qg_kv8_cache* cache, const qg_kv8_seqs* seqs, const qg_rotary* rot, const int32_t* pos,
+                            const void* k, int64_t k_row, int64_t k_head, const void* v, int64_t v_row, int64_t v_head,
+                            const int32_t* src, int src_rows, const void* q, int64_t q_row, int64_t q_head, void* q_out,
+                            int64_t qo_row, int64_t qo_head, int q_heads, qg_xtype xt, hipStream_t stream);
+
+/* The plan of a batch of trees, once a step: parents [T] has the row that each row follows, counted from its sequence's
+ * first (a row before it; anything else: it follows the sequence's earlier tokens).  Bit j % 32 of word j / 32 of mask row r
+ * [T][words] is set if row r descends from its sequence's row j or is it, and pos[r] (int32 [T]) is the position that
+ * follows: tokens before the batch's rows plus rows above r.  window > 0: rows `window` and more steps up are left out of
+ * the mask.  Rows of no sequence are not written.
+ * max_new <= 1024, 32 words >= max_new, words <= 32, else QG_ESHAPE; 4-byte aligned.  kv_len as for the attention that
+ * follows (the rows are counted).  Asynchronous; empty batches as in qg_kv8_seqs. */
+qg_status qg_tree_plan(const qg_kv8_seqs* seqs, const int32_t* parents, uint32_t* mask, int words, int32_t* pos, int window,
+                       hipStream_t stream);
+
+/* qg_attn_kv8 for rows that see each other by a mask: row r of a sequence sees all of its tokens before the batch's rows
+ * (window > 0: those after pos[r] - window; pos [T] is limited to the positions of the sequence's rows and may be NULL
+ * without a window) and the batch's rows j whose bit j % 32 of word j / 32 of mask row r [T][words] is set, itself only if
+ * its own is.  Bits past the sequence's rows mean nothing.  Workspace: qg_attn_kv8_workspace.  max_new <= 1024, words as in
+ * qg_tree_plan, else QG_ESHAPE; the rest as qg_attn_kv8. */
+qg_status qg_attn_kv8_tree(const qg_kv8_cache* cache, const qg_kv8_seqs* seqs, const uint32_t* mask, int words,
+                           const int32_t* pos, const void* q, int64_t q_row, int64_t q_head, void* o, int64_t o_row,
+                           int64_t o_head, qg_xtype xt, int q_heads, float scale, int window, void* workspace,
+                           size_t ws_bytes, hipStream_t stream);
+
+/* Verification of drafted tokens.  A sequence's first row is a token that stands (the last one made); tokens [T] are the
+ * rows' tokens, target [T][t_row >= vocab] logits of what follows each row, and parents (as for qg_tree_plan; NULL: row r
+ * follows row r - 1) the rows' order.  With p = softmax(target / temperature) of a row, from temps [seqs] (NULL: 1):
+ *   draft NULL: tokens that were chosen.  Every row draws what follows it: the first index at which the running sum of p
+ *     exceeds sample[row].  The sequence goes on at the first row that follows this one and holds that token; where there is
+ *     none the drawn token is the next.
+ *   draft [T][d_row >= vocab]: logits (of the same type and temperature) that row r + 1's token x was drawn from, a chain
+ *     (with parents QG_EUNSUPPORTED).  With q their softmax at row r, x stays where accept[r + 1] q(x) < p(x); at the
+ *     first that does not the next token is drawn by sample[r] as above from max(p - q, 0) over its sum (p, where that
+ *     sum is 0), and behind the last row from p.
+ *   temperature 0, or sample NULL for all: the largest logit (the first of equal ones) in place of a draw, and of the
+ *     comparison.
+ * Outputs: accepted [seqs], rows that stay after the first; next [seqs], the token that follows; path [T], the rows that
+ * stay, first ones included, of all sequences one after the other and -1 behind them; rows_out [seqs + 1], where each
+ * sequence's begin there; kv_out [seqs] = kv_len - rows + rows that stay (may be kv_len itself; rows_out must not be rows:
+ * QG_EINVAL).  So (table, rows_out, kv_out) with src = path is the batch of the rows that stay, moved together.
+ * accept and sample: f32 [T] in [0, 1).  Logits may be -inf; a row with a NaN, with nothing but -inf, or (drawn from) with
+ * +inf, and a temperature below 0, NaN or infinite have no next token: -1, and nothing after that row stays.  A draft row
+ * without probabilities gives its token up, and the next one is drawn from p.  Drafted tokens outside of 0 .. vocab - 1
+ * never stay.  A sequence without rows: accepted 0, next -1.
+ * All probabilities and sums are in 64 bits; the result is the same every time.
+ * 1 <= vocab <= 2^24, max_new <= 1024, strides <= 2^40 else QG_ESHAPE; logits aligned to their elements, workspace 16-byte
+ * (QG_EALIGN); QG_EWORKSPACE if NULL or smaller than qg_draft_verify_workspace.  It needs no initialisation; calls that
+ * overlap in time need one each.  Asynchronous; empty batches as in qg_kv8_seqs (no output is written). */
+size_t qg_draft_verify_workspace(const qg_kv8_seqs* seqs, int vocab);
+qg_status qg_draft_verify(const qg_kv8_seqs* seqs, const int32_t* parents, const int32_t* tokens, const void* target,
+                          int64_t t_row, const void* draft, int64_t d_row, qg_xtype xt, int vocab, const float* temps,
+                          const float* accept, const float* sample, int32_t* accepted, int32_t* next, int32_t* rows_out,
+                          int32_t* path, int32_t* kv_out, void* workspace, size_t ws_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
