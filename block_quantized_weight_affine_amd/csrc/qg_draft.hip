@@ -40,11 +40,12 @@ __global__ __launch_bounds__(256) void tree_plan_kernel(KvSeqs q, const int32_t*
 // ---- verification -------------------------------------------------------------------------------------------------
 // Probabilities in 64 bits throughout: this card's 64-bit rate is that of 32, and a draw falls on a border between two
 // tokens of a vocabulary of 10^5 in one call of a hundred if sums are off by 2^-24.
-constexpr int kThreads = 256, kRun = 16;  // values a thread takes at a time
+//
+// A row is cut into pieces of kPiece values, 16 a lane of a wavefront.
+constexpr int kStep = 512, kPiece = 2 * kStep;
 
-// 2^t for t <= 0, off by less than 2^-52 of it.  Series of e^x to x^12.
+// 2^t, -1100 <= t <= 1, off by less than 2^-51 of it.  Series of e^x to x^12.
 __device__ __forceinline__ double exp2_64(double t) {
-    t = fmax(t, -1100.0);
     const double n = __builtin_rint(t), x = (t - n) * 0.69314718055994531;
     double y = 2.08767569878681e-9;
     y = fma(y, x, 2.50521083854417188e-8);
@@ -61,12 +62,45 @@ __device__ __forceinline__ double exp2_64(double t) {
     y = fma(y, x, 1.0);
     return __builtin_amdgcn_ldexp(y, (int)n);
 }
-// A logit's weight below the row's largest; c = log2(e) / temperature.
-__device__ __forceinline__ double weight(float l, float top, double c) {
-    if (l == -__builtin_inff()) return 0.0;
-    const double t = ((double)l - (double)top) * c;
-    return t == t ? exp2_64(t) : t;
+// The same for t = -a / 256, 0 <= a <= 281600, with 2^(j / 256) from a table, as two factors.  A series of 2^(-f / 256)
+// about f = 1/2 to the fourth power: off by less than 2^-53 for 0 <= f < 1.  9 64-bit instructions with the sum of products
+// that follows, and 3 of 32 bits; 64 entries take one more of each.
+constexpr int kTable = 256;
+__device__ __forceinline__ void exp2_64(double a, const double* table, double& u, double& v) {
+    const double f = __builtin_amdgcn_fract(a);
+    const int k = (int)-a;
+    double y = 2.2363655419893987e-12;
+    y = fma(y, f, -3.3082996515760766e-09);
+    y = fma(y, f, 3.6655655953957943e-06);
+    y = fma(y, f, -0.0027076061740619077);
+    u = fma(y, f, 1.0);
+    v = __builtin_amdgcn_ldexp(table[k & (kTable - 1)], k >> 8);
 }
+// The table, by all threads of a workgroup.
+__device__ __forceinline__ void make_table(double* table) {
+    for (int i = threadIdx.x; i < kTable; i += blockDim.x) table[i] = exp2_64(i / (double)kTable);
+    __syncthreads();
+}
+
+// A logit's weight below the row's largest; c = log2(e) / temperature.  0 where nothing is left to compare (both
+// infinite), or the logit is a NaN: pieces note those apart.
+__device__ __forceinline__ double weight(float l, float top, double c) {
+    return exp2_64(fmax(((double)l - (double)top) * c, -1100.0));
+}
+// The same for many values up to one top: 2^(-(m - 256 l c) / 256), m = 256 top c rounded up so that no difference falls
+// below 0, and what m gained by that as a factor of all of them.  0 for a NaN: pieces note those apart.
+struct Weigh {
+    double c, m, rest;
+    const double* table;
+    __device__ __forceinline__ Weigh(float top, double c_, const double* t) : c(256.0 * c_), table(t) {
+        m = (double)top * c;
+        m = fma(fabs(m), 2.220446049250313e-16, m);
+        rest = fma(fma(-(double)top, c, m), 0.69314718055994531 / 256, 1.0);
+    }
+    __device__ __forceinline__ void operator()(float l, double& u, double& v) const {
+        exp2_64(fmin(fma(-(double)l, c, m), 281600.0), table, u, v);
+    }
+};
 
 template <int XT>
 __device__ __forceinline__ float logit(const void* x, int64_t i) {
@@ -74,11 +108,103 @@ __device__ __forceinline__ float logit(const void* x, int64_t i) {
     const uint16_t u = ((const uint16_t*)x)[i];
     return XT == XT_F16 ? f16_to_f32(u) : bf16_to_f32(u);
 }
-
-__device__ __forceinline__ double wave_sum(double v) {
+// Eight values of a row, as they lie: rows may begin at any element.
+struct __attribute__((packed, aligned(2))) Loose16 {
+    uint32_t w[4];
+};
+template <int XT>
+struct Raw8 {
+    Loose16 a[XT == XT_F32 ? 2 : 1];
+};
+// Values first .. first + 7 of a row of n; where those would end past it they begin earlier, and open_raw hides the ones
+// before `first`.  Rows of fewer than 8 values are padded.
+template <int XT>
+__device__ __forceinline__ int row_start(int first, int n) { return n < 8 ? first : min(first, n - 8); }
+template <int XT>
+__device__ __forceinline__ Raw8<XT> load_raw(const void* x, int64_t at, int first, int n) {
+    if (n >= 8) return *(const Raw8<XT>*)((const char*)x + (at + row_start<XT>(first, n)) * (XT == XT_F32 ? 4 : 2));
+    Raw8<XT> r;
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+    for (int e = 0; e < 8; e++) {
+        const bool on = first + e < n;
+        if constexpr (XT == XT_F32) {
+            r.a[e >> 2].w[e & 3] = on ? ((const uint32_t*)x)[at + first + e] : 0xff800000u;
+        } else {
+            const uint32_t u = on ? ((const uint16_t*)x)[at + first + e] : XT == XT_F16 ? 0xfc00u : 0xff80u;
+            r.a[0].w[e >> 1] = e & 1 ? r.a[0].w[e >> 1] | u << 16 : u;
+        }
+    }
+    return r;
+}
+// last: whether some of the wavefront's values may have to be hidden.
+template <int XT>
+__device__ __forceinline__ void open_raw(const Raw8<XT>& r, int first, int n, bool last, float* v) {
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+        if constexpr (XT == XT_F32) {
+            v[e] = __uint_as_float(r.a[e >> 2].w[e & 3]);
+        } else {
+            const uint16_t u = (uint16_t)(r.a[0].w[e >> 1] >> (16 * (e & 1)));
+            v[e] = XT == XT_F16 ? f16_to_f32(u) : bf16_to_f32(u);
+        }
+    }
+    if (last) {
+        const int hide = first - row_start<XT>(first, n);
+#pragma unroll
+        for (int e = 0; e < 8; e++) v[e] = e < hide ? -__builtin_inff() : v[e];
+    }
+}
+
+// Over a wavefront by lane shifts: within rows of 16 lanes, then from row to row.  CTRL: shift right by 1, 2, 4, 8
+// (0x111 ..), row 0's and 2's last lane to the next row (0x142), lane 31 to the upper half (0x143).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double shifted(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xf, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xf, false);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double wave_scan(double v) {  // inclusive
+    v += shifted<0x111, 0xf>(v);
+    v += shifted<0x112, 0xf>(v);
+    v += shifted<0x114, 0xf>(v);
+    v += shifted<0x118, 0xf>(v);
+    v += shifted<0x142, 0xa>(v);
+    v += shifted<0x143, 0xc>(v);
     return v;
+}
+__device__ __forceinline__ double lane_of(double v, int lane) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double wave_sum(double v) { return lane_of(wave_scan(v), 63); }
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float max_shifted(float v) {
+    return fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(v), __float_as_int(v), CTRL, ROWS, 0xf, false)));
+}
+__device__ __forceinline__ float wave_max(float v) {
+    v = max_shifted<0x111, 0xf>(v);
+    v = max_shifted<0x112, 0xf>(v);
+    v = max_shifted<0x114, 0xf>(v);
+    v = max_shifted<0x118, 0xf>(v);
+    v = max_shifted<0x142, 0xa>(v);
+    v = max_shifted<0x143, 0xc>(v);
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int min_shifted(int v) {
+    return min(v, __builtin_amdgcn_update_dpp(v, v, CTRL, ROWS, 0xf, false));
+}
+__device__ __forceinline__ int wave_min(int v) {
+    v = min_shifted<0x111, 0xf>(v);
+    v = min_shifted<0x112, 0xf>(v);
+    v = min_shifted<0x114, 0xf>(v);
+    v = min_shifted<0x118, 0xf>(v);
+    v = min_shifted<0x142, 0xa>(v);
+    v = min_shifted<0x143, 0xc>(v);
+    return __builtin_amdgcn_readlane(v, 63);
 }
 
 // How a sequence draws: c > 0: from the probabilities of temperature log2(e) / c; 0: the largest logit; NaN: not at all.
@@ -88,29 +214,43 @@ __device__ __forceinline__ double draw_factor(const VerifyParams& p, int s) {
     return t == 0.f ? 0.0 : t > 0.f && t < __builtin_inff() ? 1.4426950408889634 / (double)t : __builtin_nan("");
 }
 
-__device__ __forceinline__ bool better(float a, int i, float b, int j) { return a > b || (a == b && i < j); }
-
-// Joins two chunks' parts.
-__device__ __forceinline__ void join(VerifyPart& a, const VerifyPart& b, double c) {
-    const bool first = better(a.top, a.at, b.top, b.at);
-    const float top = first ? a.top : b.top;
-    const int at = first ? a.at : b.at;
-    double sum = a.sum + b.sum;  // a NaN of either
-    if (c > 0.0) sum = (a.sum == 0.0 ? 0.0 : a.sum * weight(a.top, top, c)) + (b.sum == 0.0 ? 0.0 : b.sum * weight(b.top, top, c));
-    a = VerifyPart{sum, top, at};
-}
-
-// A row's parts, joined by a wavefront.
-__device__ __forceinline__ VerifyPart row_part(const VerifyPart* part, int chunks, double c) {
+// A row's parts, joined by a wavefront: lane l holds those of pieces l, l + 64, .., kHeld of them at most.
+constexpr int kHeld = 4;
+struct Row {
+    VerifyPart all;
+    double mass[kHeld];  // of the pieces held, below all.top (temperature above 0)
+};
+__device__ __forceinline__ Row row_of(const VerifyPart* part, int pieces, double c) {
     const int lane = threadIdx.x & 63;
-    VerifyPart a = {0.0, -__builtin_inff(), 0x7fffffff};
-    for (int i = lane; i < chunks; i += 64) join(a, part[i], c);
+    VerifyPart a[kHeld];
+    float top = -__builtin_inff();
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const VerifyPart b = {__shfl_xor(a.sum, o), __shfl_xor(a.top, o), __shfl_xor(a.at, o)};
-        join(a, b, c);
+    for (int i = 0; i < kHeld; i++) {
+        a[i] = VerifyPart{0.0, -__builtin_inff(), 0x7fffffff};
+        if (64 * i + lane < pieces) a[i] = part[64 * i + lane];
     }
-    return a;
+#pragma unroll
+    for (int i = 0; i < kHeld; i++) top = fmaxf(top, a[i].top);
+    for (int i = 64 * kHeld + lane; i < pieces; i += 64) top = fmaxf(top, part[i].top);
+    Row r;
+    r.all.top = top = wave_max(top);
+    double sum = 0.0;
+    int at = 0x7fffffff;
+#pragma unroll
+    for (int i = 0; i < kHeld; i++) {
+        r.mass[i] = a[i].sum;
+        if (64 * i < pieces && c > 0.0) r.mass[i] *= weight(a[i].top, top, c);
+        sum += r.mass[i];
+        if (a[i].top == top) at = min(at, a[i].at);
+    }
+    for (int i = 64 * kHeld + lane; i < pieces; i += 64) {
+        const VerifyPart b = part[i];
+        sum += c > 0.0 ? b.sum * weight(b.top, top, c) : b.sum;
+        if (b.top == top) at = min(at, b.at);
+    }
+    r.all.sum = wave_sum(sum);
+    r.all.at = c > 0.0 ? 0 : wave_min(at);
+    return r;
 }
 // Whether a row has a distribution, or a largest logit.
 __device__ __forceinline__ bool row_ok(const VerifyPart& a, double c) {
@@ -118,373 +258,456 @@ __device__ __forceinline__ bool row_ok(const VerifyPart& a, double c) {
     return c > 0.0 && a.sum > 0.0 && a.sum < __builtin_inf();
 }
 
-// Chunk blockIdx.x % chunks of a row: its largest logit, where that stands first, and the sum of weights below it.
+// Pieces of a row by a wavefront, p.per of them one after the other, the next one's values on their way: each piece's
+// largest logit, where that stands first (temperature 0), and the sum of weights below it.
 template <int XT>
-__global__ __launch_bounds__(kThreads) void verify_part_kernel(VerifyParams p, uint32_t group0) {
-    __shared__ VerifyPart sh[kThreads / 64];
-    const int s = blockIdx.y;
+__global__ __launch_bounds__(256) void verify_part_kernel(VerifyParams p, uint32_t group0) {
+    __shared__ double table[kTable];
+    const int s = blockIdx.y, lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const KvSpan sp = kv8_span(p.q, s);
-    uint32_t b = group0 + blockIdx.x;
-    if (b == 0 && threadIdx.x == 0) {
+    if (p.sample) make_table(table);
+    uint32_t b = (group0 + blockIdx.x) * 4 + wave;
+    if (b == 0 && lane == 0) {
         p.tickets[s] = 0;
         if (s == 0) p.tickets[p.q.seqs] = 0;
     }
-    const int k = b % p.chunks;
-    b /= p.chunks;
+    const uint32_t waves = (p.pieces + p.per - 1) / p.per;
+    const int k0 = b % waves * p.per, k1 = min(k0 + p.per, p.pieces);
+    b /= waves;
     const int r = b % p.q.max_new;
-    const bool of_draft = b / p.q.max_new;
-    if (r >= sp.n || (of_draft && r == sp.n - 1)) return;
+    b /= p.q.max_new;
+    const bool of_draft = b == 1;
+    if (b > (p.draft ? 1 : 0) || r >= sp.n || (of_draft && r == sp.n - 1)) return;
     const double c = draw_factor(p, s);
     if (of_draft && c == 0.0) return;
     const int64_t row = sp.r0 + r;
     const void* x = of_draft ? p.draft : p.target;
     const int64_t at = row * (of_draft ? p.d_row : p.t_row);
-    const int lo = k * p.chunk, hi = min(lo + p.chunk, p.vocab);
-    VerifyPart a = {0.0, -__builtin_inff(), 0x7fffffff};
-    for (int i0 = lo + threadIdx.x; i0 < hi; i0 += kThreads * kRun) {
-        float v[kRun];
+    VerifyPart* part = p.part + ((of_draft ? (int64_t)p.q.T : 0) + row) * p.pieces;
+    const int i0 = 8 * lane;
+    Raw8<XT> raw[2] = {load_raw<XT>(x, at, k0 * kPiece + i0, p.vocab), load_raw<XT>(x, at, k0 * kPiece + kStep + i0, p.vocab)};
+    for (int k = k0; k < k1; k++) {
+        float v[16];
+        const bool last = (k + 1) * kPiece > p.vocab;
 #pragma unroll
-        for (int e = 0; e < kRun; e++) {
-            const int i = i0 + e * kThreads;
-            v[e] = i < hi ? logit<XT>(x, at + i) : -__builtin_inff();
+        for (int h = 0; h < 2; h++) open_raw<XT>(raw[h], k * kPiece + h * kStep + i0, p.vocab, last, v + 8 * h);
+        if (k + 1 < k1)
+#pragma unroll
+            for (int h = 0; h < 2; h++) raw[h] = load_raw<XT>(x, at, (k + 1) * kPiece + h * kStep + i0, p.vocab);
+        float top = v[0];
+        bool nan = false;
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+            top = fmaxf(top, fmaxf(v[e], v[e + 1]));
+            nan |= __builtin_isunordered(v[e], v[e + 1]);
         }
-        VerifyPart n = {0.0, -__builtin_inff(), 0x7fffffff};
+        top = wave_max(top);
+        VerifyPart a = {0.0, top, 0x7fffffff};
+        if (c > 0.0) {
+            if (top > -__builtin_inff()) {
+                const Weigh w(top, c, table);
 #pragma unroll
-        for (int e = 0; e < kRun; e++) {
-            if (better(v[e], i0 + e * kThreads, n.top, n.at)) n.top = v[e], n.at = i0 + e * kThreads;
-            if (v[e] != v[e]) n.sum = __builtin_nan("");
+                for (int e = 0; e < 16; e++) {
+                    double f, g;
+                    w(v[e], f, g);
+                    a.sum = fma(f, g, a.sum);
+                }
+                a.sum *= w.rest;
+            }
+            a.sum = wave_sum(a.sum);
+        } else {
+#pragma unroll
+            for (int e = 15; e >= 0; e--)
+                if (v[e] == top) a.at = row_start<XT>(k * kPiece + (e >> 3) * kStep + i0, p.vocab) + (e & 7);
+            a.at = wave_min(a.at);
         }
-        if (c > 0.0)
-#pragma unroll
-            for (int e = 0; e < kRun; e++) n.sum += weight(v[e], n.top, c);
-        join(a, n, c);
-    }
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const VerifyPart n = {__shfl_xor(a.sum, o), __shfl_xor(a.top, o), __shfl_xor(a.at, o)};
-        join(a, n, c);
-    }
-    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = a;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < kThreads / 64; w++) join(a, sh[w], c);
-        p.part[((of_draft ? (int64_t)p.q.T : 0) + row) * p.chunks + k] = a;
+        if (__any(nan)) a.sum = __builtin_nan("");
+        if (lane == 0) part[k] = a;
     }
 }
 
-// The weight that token i has in a draw.
+// The probabilities in a draw of the tokens that load_raw gives for i: the target's, less the draft's.
 template <int XT>
 struct Mass {
     const void *target, *draft;
     int64_t t_at, d_at;
-    float t_top, d_top;
-    double c, t_inv, d_inv;  // 1 / sum; d_inv 0: the target's probabilities alone
-    __device__ __forceinline__ double operator()(int i) const {
+    Weigh t, d;
+    double t_inv, d_inv;  // 1 / sum times the weights' common factor; d_inv 0: the target's alone
+    int vocab;
+    __device__ __forceinline__ int start(int i) const { return row_start<XT>(i, vocab); }
+    __device__ __forceinline__ void operator()(int i, bool last, double (&m)[8]) const {
+        float v[8], w[8];
+        const Raw8<XT> rt = load_raw<XT>(target, t_at, i, vocab);
+        Raw8<XT> rd;
+        if (d_inv != 0.0) rd = load_raw<XT>(draft, d_at, i, vocab);
+        open_raw<XT>(rt, i, vocab, last, v);
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            double f, g;
+            t(v[e], f, g);
+            m[e] = f * g * t_inv;
+        }
+        if (d_inv == 0.0) return;
+        open_raw<XT>(rd, i, vocab, last, w);
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
 #pragma clang fp contract(off)  // equal probabilities leave nothing
-        const double t = weight(logit<XT>(target, t_at + i), t_top, c) * t_inv;
-        if (d_inv == 0.0) return t;
-        return fmax(t - weight(logit<XT>(draft, d_at + i), d_top, c) * d_inv, 0.0);
+            double f, g;
+            d(w[e], f, g);
+            const double q = f * g * d_inv;
+            m[e] = fmax(m[e] - q, 0.0);
+        }
     }
 };
 
-// Sum over a workgroup, to all threads; sh: 4 values.
-__device__ __forceinline__ double group_sum(double v, double* sh) {
-    v = wave_sum(v);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
-    __syncthreads();
-    return sh[0] + sh[1] + sh[2] + sh[3];
-}
-
-// The first i of lo .. hi - 1 at which the running sum of the masses exceeds goal; where rounding leaves none, the last
-// that has a mass; -1 if none has.  All threads of a workgroup call it.
+// The first token of piece k at which the running sum of the masses exceeds goal; where rounding leaves none, the last
+// that has a mass; -1 if none has.  By a wavefront.
 template <class M>
-__device__ __forceinline__ int find_in_chunk(const M& mass, int lo, int hi, double goal, double* sh, int* sh_at) {
-    const int per = (hi - lo + kThreads - 1) / kThreads, t = threadIdx.x, lane = t & 63;
-    const int i0 = min(lo + t * per, hi), i1 = min(i0 + per, hi);
-    double own = 0.0;
+__device__ __forceinline__ int find_in_piece(const M& mass, int k, double goal) {
+    const int lane = threadIdx.x & 63, i0 = k * kPiece + 8 * lane;
+    double m[2][8], before = 0.0;
     int last = -1;
-    for (int i = i0; i < i1; i++) {
-        const double m = mass(i);
-        own += m;
-        if (m > 0.0) last = i;
-    }
-    double run = own;  // inclusive, over the wavefront
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const double u = __shfl_up(run, o);
-        if (lane >= o) run += u;
-    }
-    __syncthreads();
-    if (lane == 63) sh[t >> 6] = run;
-    if (t == 0) sh_at[0] = 0x7fffffff, sh_at[1] = -1;
-    __syncthreads();
-    double before = run - own;
-    for (int w = 0; w < t >> 6; w++) before += sh[w];
-    if (last >= 0) {
-        atomicMax(&sh_at[1], last);
-        // a thread whose run may hold it looks; of several the first index counts
-        double sum = before;
-        if (before + own > goal)
-            for (int i = i0; i < i1; i++) {
-                const double m = mass(i);
-                sum += m;
-                if (m > 0.0 && sum > goal) {
-                    atomicMin(&sh_at[0], i);
-                    break;
-                }
+    for (int h = 0; h < 2; h++) mass(i0 + h * kStep, (k + 1) * kPiece > mass.vocab, m[h]);
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        double own = 0.0;
+#pragma unroll
+        for (int e = 0; e < 8; e++) own += m[h][e];
+        const double run = wave_scan(own);
+        const uint64_t some = __ballot(own > 0.0), hit = __ballot(own > 0.0 && before + run > goal);
+        if (some) {
+            // the lane of the first hit, else the last that has a mass
+            const int at = hit ? __builtin_ctzll(hit) : 63 - __builtin_clzll(some);
+            int found = -1;
+            double sum = before + (run - own);
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                const bool over = sum > goal;  // an earlier one already was
+                sum += m[h][e];
+                if (m[h][e] > 0.0 && !(over && found >= 0)) found = mass.start(i0 + h * kStep) + e;
             }
+            last = __builtin_amdgcn_readlane(found, at);
+            if (hit) return last;
+        }
+        before += lane_of(run, 63);
     }
-    __syncthreads();
-    return sh_at[0] == 0x7fffffff ? sh_at[1] : sh_at[0];
+    return last;
 }
 
-// The chunk in which the running sum of `mass` (each chunk's, in order) exceeds goal, and the sum before it.
-struct ChunkAt {
+// The piece in which the running sum of `mass` (each piece's, in order) exceeds goal, and the sum before it; where rounding
+// leaves none, the last that has a mass.  By a wavefront.
+struct PieceAt {
     int k;
     double before;
 };
 template <class F>
-__device__ __forceinline__ ChunkAt find_chunk(const F& mass, int chunks, double goal) {
+__device__ __forceinline__ PieceAt find_piece(const F& mass, int pieces, double goal) {
     const int lane = threadIdx.x & 63;
-    ChunkAt found = {-1, 0.0};
+    PieceAt found = {-1, 0.0};
     double sum = 0.0;
-    for (int k0 = 0; k0 < chunks; k0 += 64) {
-        const double own = k0 + lane < chunks ? mass(k0 + lane) : 0.0;
-        double run = own;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const double u = __shfl_up(run, o);
-            if (lane >= o) run += u;
-        }
-        const uint64_t hit = __ballot(own > 0.0 && sum + run > goal), any = __ballot(own > 0.0);
-        const int at = hit ? __builtin_ctzll(hit) : any ? 63 - __builtin_clzll(any) : -1;
-        if (at >= 0) found = ChunkAt{k0 + at, sum + __shfl(run - own, at)};
+    for (int k0 = 0; k0 < pieces; k0 += 64) {
+        const double own = k0 + lane < pieces ? mass(k0 + lane) : 0.0;
+        const double run = wave_scan(own);
+        const uint64_t hit = __ballot(own > 0.0 && sum + run > goal), some = __ballot(own > 0.0);
+        const int at = hit ? __builtin_ctzll(hit) : some ? 63 - __builtin_clzll(some) : -1;
+        if (at >= 0) found = PieceAt{k0 + at, sum + lane_of(run - own, at)};
         if (hit) break;
-        sum += __shfl(run, 63);
+        sum += lane_of(run, 63);
     }
     return found;
 }
 
-// Whether this is the last of n workgroups to come here; it then sees what the first wavefronts of all of them wrote.
-__device__ __forceinline__ bool last_of(uint32_t* ticket, uint32_t n, int* sh) {
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
-        *sh = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == n - 1;
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+// The same over pieces that are held, and over a row's own.
+__device__ __forceinline__ PieceAt find_held(const Row& row, int pieces, double goal) {
+    PieceAt found = {-1, 0.0};
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < kHeld; i++) {
+        if (64 * i >= pieces) break;
+        const double run = wave_scan(row.mass[i]);
+        const uint64_t hit = __ballot(row.mass[i] > 0.0 && sum + run > goal), some = __ballot(row.mass[i] > 0.0);
+        const int at = hit ? __builtin_ctzll(hit) : some ? 63 - __builtin_clzll(some) : -1;
+        if (at >= 0) found = PieceAt{64 * i + at, sum + lane_of(run - row.mass[i], at)};
+        if (hit) break;
+        sum += lane_of(run, 63);
     }
-    __syncthreads();
-    return *sh;
+    return found;
+}
+__device__ __forceinline__ PieceAt find_piece(const Row& row, const VerifyPart* part, int pieces, double c, double goal) {
+    if (pieces <= 64 * kHeld) return find_held(row, pieces, goal);
+    return find_piece([&](int k) { return part[k].sum * weight(part[k].top, row.all.top, c); }, pieces, goal);
 }
 
-// The last sequence to end packs the rows of all: p.accepted and p.line are theirs.
-__device__ __forceinline__ void finish(const VerifyParams& p, int* sh) {
-    if (!last_of(&p.tickets[p.q.seqs], p.q.seqs, sh)) return;
-    __shared__ int run[kThreads];
-    int total = 0;
-    for (int s0 = 0; s0 < p.q.seqs; s0 += kThreads) {
-        const int s = s0 + threadIdx.x;
-        KvSpan sp = {0, 0, 0};
-        int count = 0;
-        if (s < p.q.seqs) {
-            sp = kv8_span(p.q, s);
-            count = sp.n ? p.accepted[s] + 1 : 0;
+// What workgroups hand to each other within a launch: stores and loads that go past the dies' caches, so that no cache has
+// to be written back or emptied for them.
+template <class T>
+__device__ __forceinline__ void hand_over(T* p, T v) {
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <class T>
+__device__ __forceinline__ T handed(const T* p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// Whether this is the last of n wavefronts to come here; it then sees what all of them handed over.  A wavefront's stores
+// have arrived before it counts itself.
+__device__ __forceinline__ bool last_of(uint32_t* ticket, uint32_t n) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    uint32_t got = 0;
+    if ((threadIdx.x & 63) == 0) got = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const bool last = __builtin_amdgcn_readfirstlane(got) == n - 1;
+    asm volatile("" ::: "memory");
+    return last;
+}
+// The same for workgroups, of which the first wavefront goes on: counting at one address goes one after the other.
+__device__ __forceinline__ bool last_group_of(uint32_t* ticket, uint32_t n) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    return threadIdx.x < 64 && last_of(ticket, n);
+}
+
+// Ends a sequence of span sp whose rows line[0 .. count - 1] stay (counted from its first; NULL: 0 .. count - 1): the last
+// sequence to end packs the rows of all.  By a wavefront.
+__device__ __forceinline__ void finish(const VerifyParams& p, int s, const KvSpan& sp, int count, int next, const int* line) {
+    const int lane = threadIdx.x & 63;
+    if (lane == 0) p.next[s] = next;
+    if (p.q.seqs == 1) {
+        if (lane == 0) {
+            p.accepted[0] = max(count - 1, 0);
+            p.rows_out[0] = 0;
+            p.rows_out[1] = count;
+            p.kv_out[0] = p.q.kv_len[0] - sp.n + count;
         }
-        __syncthreads();
-        run[threadIdx.x] = count;
-        __syncthreads();
-        for (int o = 1; o < kThreads; o <<= 1) {
-            const int u = threadIdx.x >= o ? run[threadIdx.x - o] : 0;
-            __syncthreads();
-            run[threadIdx.x] += u;
-            __syncthreads();
-        }
-        if (s < p.q.seqs) {
-            const int to = total + run[threadIdx.x] - count;
-            p.rows_out[s] = to;
-            for (int i = 0; i < count; i++) p.path[to + i] = p.line[sp.r0 + i];
-            p.kv_out[s] = p.q.kv_len[s] - sp.n + count;
-        }
-        total += run[kThreads - 1];
+        for (int i = lane; i < p.q.T; i += 64) p.path[i] = i < count ? sp.r0 + (line ? line[i] : i) : -1;
+        return;
     }
-    if (threadIdx.x == 0) p.rows_out[p.q.seqs] = total;
-    for (int i = total + threadIdx.x; i < p.q.T; i += kThreads) p.path[i] = -1;
+    if (lane == 0) hand_over(&p.accepted[s], max(count - 1, 0));
+    if (line)
+        for (int i = lane; i < count; i += 64) hand_over(&p.line[sp.r0 + i], line[i]);
+    KvSpan first = {0, 0, 0};  // the first sequences', while the others are waited for
+    int first_kv = 0;
+    if (lane < p.q.seqs) first = kv8_span(p.q, lane), first_kv = p.q.kv_len[lane];
+    if (!last_of(&p.tickets[p.q.seqs], p.q.seqs)) return;
+    int total = 0;
+    for (int s0 = 0; s0 < p.q.seqs; s0 += 64) {
+        const int s = s0 + lane;
+        KvSpan sp = first;
+        int count = 0, kv = first_kv;
+        if (s < p.q.seqs) {
+            if (s0 > 0) sp = kv8_span(p.q, s), kv = p.q.kv_len[s];
+            count = sp.n ? handed(&p.accepted[s]) + 1 : 0;
+        }
+        int run = count;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int u = __shfl_up(run, o);
+            if (lane >= o) run += u;
+        }
+        if (s < p.q.seqs) {
+            const int to = total + run - count;
+            p.rows_out[s] = to;
+            p.kv_out[s] = kv - sp.n + count;
+            for (int i = 0; i < count; i += 8) {
+                int r[8];  // eight loads on their way
+#pragma unroll
+                for (int j = 0; j < 8; j++) r[j] = line ? handed(&p.line[sp.r0 + min(i + j, count - 1)]) : i + j;
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+                    if (i + j < count) p.path[to + i + j] = sp.r0 + r[j];
+            }
+        }
+        total += __shfl(run, 63);
+    }
+    if (lane == 0) p.rows_out[p.q.seqs] = total;
+    for (int i = total + lane; i < p.q.T; i += 64) p.path[i] = -1;
 }
 
 // Tokens that were chosen: every row draws its own next token, and the sequence follows the rows that hold what was
-// drawn.  A workgroup a row; the last one of a sequence follows it.
+// drawn.  A wavefront a row, four of them a workgroup; the last workgroup of a sequence follows it.
 template <int XT>
-__global__ __launch_bounds__(kThreads) void verify_tree_kernel(VerifyParams p) {
-    __shared__ double sh[4];
-    __shared__ int sh_at[2], sh_last, up[kMaxRows], tok[kMaxRows], drew[kMaxRows];
-    const int s = blockIdx.y, r = blockIdx.x;
+__global__ __launch_bounds__(256) void verify_tree_kernel(VerifyParams p) {
+    __shared__ double table[kTable];
+    __shared__ int up[kMaxRows], tok[kMaxRows], drew[kMaxRows], line[kMaxRows];
+    const int s = blockIdx.y, lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = blockIdx.x * 4 + wave;
     const KvSpan sp = kv8_span(p.q, s);
-    if (r >= max(sp.n, 1)) return;
+    if (blockIdx.x * 4 >= max(sp.n, 1)) return;
     const double c = draw_factor(p, s);
-    if (sp.n > 0) {
+    if (c > 0.0) make_table(table);
+    if (r < sp.n) {
         const int64_t row = sp.r0 + r;
-        const VerifyPart* part = p.part + row * p.chunks;
-        const VerifyPart all = row_part(part, p.chunks, c);
+        const VerifyPart* part = p.part + row * p.pieces;
+        const float u = p.sample ? p.sample[row] : 0.f;
+        const Row all = row_of(part, p.pieces, c);
         int token = -1;
-        if (row_ok(all, c)) {
-            token = all.at;
+        if (row_ok(all.all, c)) {
+            token = all.all.at;
             if (c > 0.0) {
-                const double goal = (double)p.sample[row] * all.sum;
-                const ChunkAt ch = find_chunk([&](int k) { return part[k].sum == 0.0 ? 0.0 : part[k].sum * weight(part[k].top, all.top, c); }, p.chunks, goal);
-                const Mass<XT> mass = {p.target, nullptr, row * p.t_row, 0, all.top, 0.f, c, 1.0, 0.0};
-                const int lo = ch.k * p.chunk;
-                token = find_in_chunk(mass, lo, min(lo + p.chunk, p.vocab), goal - ch.before, sh, sh_at);
+                const double goal = (double)u * all.all.sum;
+                const PieceAt at = find_piece(all, part, p.pieces, c, goal);
+                Mass<XT> mass = {p.target, nullptr, row * p.t_row, 0, Weigh(all.all.top, c, table), Weigh(0.f, c, table), 0.0, 0.0, p.vocab};
+                mass.t_inv = mass.t.rest;
+                token = find_in_piece(mass, at.k, goal - at.before);
             }
         }
-        if (threadIdx.x == 0) __hip_atomic_store(&p.drawn[row], token, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (lane == 0) hand_over(&p.drawn[row], token);
     }
-    if (!last_of(&p.tickets[s], max(sp.n, 1), &sh_last)) return;
-    for (int i = threadIdx.x; i < sp.n; i += kThreads) {
+    if (!last_group_of(&p.tickets[s], (max(sp.n, 1) + 3) / 4)) return;
+    for (int i = lane; i < sp.n; i += 64) {
         const int u = p.parents ? p.parents[sp.r0 + i] : i - 1;
         up[i] = u >= 0 && u < i ? u : -1;
         tok[i] = p.tokens[sp.r0 + i];
-        drew[i] = p.drawn[sp.r0 + i];
+        drew[i] = handed(&p.drawn[sp.r0 + i]);
     }
-    __syncthreads();
-    if (threadIdx.x < 64) {
-        const int lane = threadIdx.x;
-        int cur = 0, count = 0, next = -1;
-        while (cur < sp.n) {  // cur grows
-            if (lane == 0) p.line[sp.r0 + count] = sp.r0 + cur;
-            count++;
-            next = drew[cur];
-            int to = sp.n;
-            for (int i0 = cur + 1; i0 < sp.n && next >= 0; i0 += 64) {
-                const int i = i0 + lane;
-                const uint64_t hit = __ballot(i < sp.n && up[min(i, sp.n - 1)] == cur && tok[min(i, sp.n - 1)] == next);
-                if (hit) {
-                    to = i0 + __builtin_ctzll(hit);
-                    break;
-                }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");  // one wavefront is left
+    int cur = 0, count = 0, next = -1;
+    while (cur < sp.n) {  // cur grows
+        next = drew[cur];
+        if (lane == 0) line[count] = cur;
+        count++;
+        int to = sp.n;
+        for (int i0 = cur + 1; i0 < sp.n && next >= 0; i0 += 64) {
+            const int i = min(i0 + lane, sp.n - 1);
+            const uint64_t hit = __ballot(i == i0 + lane && up[i] == cur && tok[i] == next);
+            if (hit) {
+                to = i0 + __builtin_ctzll(hit);
+                break;
             }
-            cur = to;
         }
-        if (lane == 0) {
-            p.accepted[s] = max(count - 1, 0);
-            p.next[s] = next;
-        }
+        cur = to;
     }
-    finish(p, &sh_last);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
+    finish(p, s, sp, count, next, line);
 }
 
 // Tokens that were drawn from the draft's probabilities, one after the other: row r + 1's token x stays where
 // accept[r + 1] q(x) < p(x), p and q at row r; the first that does not ends the sequence with a draw from
-// max(p - q, 0), and where all stay the draw is from p at the last row.  A workgroup a chunk: each finds the row at which
-// the sequence ends, and sums its chunk of that row's masses; the last one draws.
+// max(p - q, 0), and where all stay the draw is from p at the last row.  Every workgroup finds the row at which the
+// sequence ends, eight rows at a time, a wavefront each for p and for q; for max(p - q, 0) each wavefront then sums a
+// piece, and the last of them draws, else one alone does.
+constexpr int kChainWaves = 16;
 template <int XT>
-__global__ __launch_bounds__(kThreads) void verify_chain_kernel(VerifyParams p) {
-    __shared__ double sh[4];
-    __shared__ int sh_at[2], sh_last, sh_end;
-    __shared__ VerifyPart sh_t, sh_d;
-    const int s = blockIdx.y, k = blockIdx.x;
+__global__ __launch_bounds__(64 * kChainWaves) void verify_chain_kernel(VerifyParams p) {
+    __shared__ double table[kTable];
+    __shared__ VerifyPart sh_all[kChainWaves];
+    __shared__ double sh_x[kChainWaves];  // p(x), q(x); temperature 0: whether x stays
+    const int s = blockIdx.y, lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), k = blockIdx.x * kChainWaves + wave;
     const KvSpan sp = kv8_span(p.q, s);
     const double c = draw_factor(p, s);
-    if (sp.n == 0 && k > 0) return;
-    if (sp.n > 0) {
-        if (threadIdx.x == 0) sh_end = sp.n - 1;
-        __syncthreads();
-        for (int r0 = 0; r0 < sp.n - 1; r0 += kThreads / 64) {
-            const int r = r0 + (threadIdx.x >> 6);
-            if (r < sp.n - 1) {
-                const int64_t row = sp.r0 + r;
-                const VerifyPart t = row_part(p.part + row * p.chunks, p.chunks, c);
-                const int x = p.tokens[row + 1];
-                bool stays = false;
-                if (row_ok(t, c) && (uint32_t)x < (uint32_t)p.vocab) {
-                    if (c == 0.0) {
-                        stays = x == t.at;
-                    } else {
-                        const VerifyPart d = row_part(p.part + (p.q.T + row) * p.chunks, p.chunks, c);
-                        if (row_ok(d, c)) {
-                            const double pt = weight(logit<XT>(p.target, row * p.t_row + x), t.top, c) / t.sum;
-                            const double qt = weight(logit<XT>(p.draft, row * p.d_row + x), d.top, c) / d.sum;
-                            stays = (double)p.accept[row + 1] * qt < pt;
-                        }
-                    }
-                }
-                if (!stays && (threadIdx.x & 63) == 0) atomicMin(&sh_end, r);
+    if (sp.n == 0) {
+        if (k == 0) finish(p, s, sp, 0, -1, nullptr);
+        return;
+    }
+    constexpr int kRows = kChainWaves / 2;
+    const bool draws = c > 0.0;
+    if (draws) make_table(table);
+    int e;
+    for (int r0 = 0;; r0 += kRows) {
+        const int r = r0 + wave % kRows;
+        const bool of_draft = wave >= kRows;
+        const float limit = draws && lane < kRows && r0 + lane < sp.n - 1 ? p.accept[sp.r0 + r0 + lane + 1] : 0.f;
+        if (r < sp.n && !(of_draft && (r == sp.n - 1 || c == 0.0))) {
+            const int64_t row = sp.r0 + r;
+            const int x = r < sp.n - 1 ? p.tokens[row + 1] : -1;
+            const bool there = (uint32_t)x < (uint32_t)p.vocab;
+            float l = 0.f;
+            if (there) l = of_draft ? logit<XT>(p.draft, row * p.d_row + x) : logit<XT>(p.target, row * p.t_row + x);
+            const Row a = row_of(p.part + ((of_draft ? (int64_t)p.q.T : 0) + row) * p.pieces, p.pieces, c);
+            if (lane == 0) {
+                sh_all[wave] = a.all;
+                sh_x[wave] = c == 0.0 ? (double)(x == a.all.at) : there ? weight(l, a.all.top, c) / a.all.sum : 0.0;
             }
-            __syncthreads();
-            if (sh_end <= r0 + kThreads / 64 - 1) break;
         }
-        const int e = sh_end;
-        const int64_t row = sp.r0 + e;
-        if (threadIdx.x < 64) {
-            const VerifyPart t = row_part(p.part + row * p.chunks, p.chunks, c);
-            if (threadIdx.x == 0) sh_t = t;
-        } else if (threadIdx.x < 128) {
-            VerifyPart d = {0.0, 0.f, 0};
-            if (e < sp.n - 1) d = row_part(p.part + (p.q.T + row) * p.chunks, p.chunks, c);
-            if (threadIdx.x == 64) sh_d = d;
+        __syncthreads();
+        bool stays = false;
+        const int ri = r0 + lane;
+        if (lane < kRows && ri < sp.n - 1 && row_ok(sh_all[lane], c)) {
+            stays = sh_x[lane] > 0.0;
+            if (c > 0.0) stays = row_ok(sh_all[lane + kRows], c) && (double)limit * sh_x[lane + kRows] < sh_x[lane];
+        }
+        const uint64_t ends = __ballot(lane < kRows && !stays);
+        if (ends) {
+            e = r0 + __builtin_ctzll(ends);
+            break;
         }
         __syncthreads();
     }
-    const int e = sp.n > 0 ? sh_end : 0;
     const int64_t row = sp.r0 + e;
-    const bool ok = sp.n > 0 && row_ok(sh_t, c), drawn = ok && c > 0.0;
-    Mass<XT> mass = {p.target, p.draft, row * p.t_row, row * p.d_row, ok ? sh_t.top : 0.f, 0.f, c, 0.0, 0.0};
-    if (drawn) {
-        mass.t_inv = 1.0 / sh_t.sum;
-        if (e < sp.n - 1 && row_ok(sh_d, c)) mass.d_top = sh_d.top, mass.d_inv = 1.0 / sh_d.sum;
-        double sum = 0.0;
-        const int lo = k * p.chunk, hi = min(lo + p.chunk, p.vocab);
-        for (int i = lo + threadIdx.x; i < hi; i += kThreads) sum += mass(i);
-        sum = group_sum(sum, sh);
-        if (threadIdx.x == 0) __hip_atomic_store(&p.mass[(int64_t)s * p.chunks + k], sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const VerifyPart t = sh_all[e % kRows];
+    const bool ok = row_ok(t, c), drawn = ok && c > 0.0;
+    float d_top = 0.f;
+    double d_inv = 0.0;
+    if (drawn && e < sp.n - 1) {
+        const VerifyPart d = sh_all[e % kRows + kRows];
+        if (row_ok(d, c)) d_top = d.top, d_inv = 1.0 / d.sum;
     }
-    if (!last_of(&p.tickets[s], sp.n > 0 ? p.chunks : 1, &sh_last)) return;
+    const bool shared = d_inv != 0.0;  // all wavefronts have a part in the draw
+    if (!shared && k > 0) return;
+    Mass<XT> mass = {p.target, p.draft, row * p.t_row, row * p.d_row, Weigh(t.top, c, table), Weigh(d_top, c, table), 0.0, 0.0,
+                     p.vocab};
+    mass.t_inv = mass.t.rest / t.sum;
+    if (shared) mass.d_inv = mass.d.rest * d_inv;
+    double* m = p.mass + (int64_t)s * p.pieces;
+    const double u = drawn ? (double)p.sample[row] : 0.0;
+    if (shared) {
+        if (k < p.pieces) {
+            const bool last = (k + 1) * kPiece > p.vocab;
+            double v[2][8], sum = 0.0;
+            mass(k * kPiece + 8 * lane, last, v[0]);
+            mass(k * kPiece + kStep + 8 * lane, last, v[1]);
+#pragma unroll
+            for (int x = 0; x < 16; x++) sum += v[x >> 3][x & 7];
+            sum = wave_sum(sum);
+            if (lane == 0) hand_over(&m[k], sum);
+        }
+        if (!last_group_of(&p.tickets[s], gridDim.x)) return;
+    }
     int token = -1;
     if (ok) {
-        token = sh_t.at;
+        token = t.at;
         if (drawn) {
-            const double* m = p.mass + (int64_t)s * p.chunks;
-            double all = 0.0;
-            for (int i = threadIdx.x & 63; i < p.chunks; i += 64) all += m[i];
-            all = wave_sum(all);
-            const double u = (double)p.sample[row];
-            ChunkAt ch;
-            if (all > 0.0) {
-                ch = find_chunk([&](int i) { return m[i]; }, p.chunks, u * all);
-            } else {  // the draft's probabilities are nowhere below the target's
-                mass.d_inv = 0.0;
-                const VerifyPart* part = p.part + row * p.chunks;
-                all = 1.0;
-                ch = find_chunk([&](int i) { return part[i].sum == 0.0 ? 0.0 : part[i].sum * weight(part[i].top, sh_t.top, c) * mass.t_inv; }, p.chunks, u);
+            double goal = 0.0;
+            PieceAt at = {-1, 0.0};
+            if (shared) {
+                Row pieces;
+                pieces.all = t;
+                double all = 0.0;
+#pragma unroll
+                for (int i = 0; i < kHeld; i++) {
+                    pieces.mass[i] = 64 * i + lane < p.pieces ? handed(&m[64 * i + lane]) : 0.0;
+                    all += pieces.mass[i];
+                }
+                for (int i = 64 * kHeld + lane; i < p.pieces; i += 64) all += handed(&m[i]);
+                goal = u * wave_sum(all);
+                at = p.pieces > 64 * kHeld ? find_piece([&](int i) { return handed(&m[i]); }, p.pieces, goal)
+                                           : find_held(pieces, p.pieces, goal);
             }
-            const int lo = ch.k * p.chunk;
-            token = find_in_chunk(mass, lo, min(lo + p.chunk, p.vocab), u * all - ch.before, sh, sh_at);
+            if (at.k < 0) {  // or the draft's probabilities are nowhere below the target's
+                const VerifyPart* part = p.part + row * p.pieces;
+                mass.d_inv = 0.0;
+                mass.t_inv = mass.t.rest;
+                goal = u * t.sum;
+                at = find_piece(row_of(part, p.pieces, c), part, p.pieces, c, goal);
+            }
+            token = find_in_piece(mass, at.k, goal - at.before);
         }
     }
-    if (threadIdx.x < 64)  // what other workgroups read is written by the wavefront that ends with the fence
-        for (int i = threadIdx.x; sp.n > 0 && i <= e; i += 64) p.line[sp.r0 + i] = sp.r0 + i;
-    if (threadIdx.x == 0) {
-        p.accepted[s] = e;
-        p.next[s] = token;
-    }
-    finish(p, &sh_last);
-}
-
-// Chunks of a row: 64 at most, so that a wavefront joins them at once, and no less than 4096 values.
-int chunk_of(int vocab) {
-    const int64_t per = ((int64_t)vocab + 63) / 64, unit = 4096;
-    return (int)std::max(unit, (per + unit - 1) / unit * unit);
+    finish(p, s, sp, e + 1, token, nullptr);
 }
 
 template <int XT>
-hipError_t launch_one(const VerifyParams& p, hipStream_t s) {
-    const int64_t groups = (int64_t)p.chunks * p.q.max_new * (p.draft ? 2 : 1);
+hipError_t launch_one(VerifyParams p, hipStream_t s) {
+    const int64_t rows = (int64_t)p.q.max_new * (p.draft ? 2 : 1);
+    p.per = (int)std::clamp<int64_t>(rows * p.q.seqs * p.pieces / 8192, 1, 8);
+    const int64_t groups = (rows * ((p.pieces + p.per - 1) / p.per) + 3) / 4;
     for (int64_t first = 0; first < groups; first += kLaunchGroups)
-        verify_part_kernel<XT><<<dim3((uint32_t)std::min(groups - first, kLaunchGroups), p.q.seqs), kThreads, 0, s>>>(p, (uint32_t)first);
+        verify_part_kernel<XT><<<dim3((uint32_t)std::min(groups - first, kLaunchGroups), p.q.seqs), 256, 0, s>>>(p, (uint32_t)first);
     if (p.draft)
-        verify_chain_kernel<XT><<<dim3(p.chunks, p.q.seqs), kThreads, 0, s>>>(p);
+        verify_chain_kernel<XT><<<dim3((p.pieces + kChainWaves - 1) / kChainWaves, p.q.seqs), 64 * kChainWaves, 0, s>>>(p);
     else
-        verify_tree_kernel<XT><<<dim3(p.q.max_new, p.q.seqs), kThreads, 0, s>>>(p);
+        verify_tree_kernel<XT><<<dim3((p.q.max_new + 3) / 4, p.q.seqs), 256, 0, s>>>(p);
     return hipGetLastError();
 }
 
@@ -499,19 +722,18 @@ hipError_t launch_tree_plan(const KvSeqs& q, const int32_t* parents, uint32_t* m
 }
 
 size_t verify_workspace(const KvSeqs& q, int vocab) {
-    const size_t chunks = (vocab + chunk_of(vocab) - 1) / chunk_of(vocab), T = q.T, seqs = q.seqs;
-    return 2 * T * chunks * sizeof(VerifyPart) + up16(seqs * chunks * 8) + 2 * up16(T * 4) + up16((seqs + 1) * 4);
+    const size_t pieces = (vocab + kPiece - 1) / kPiece, T = q.T, seqs = q.seqs;
+    return 2 * T * pieces * sizeof(VerifyPart) + up16(seqs * pieces * 8) + 2 * up16(T * 4) + up16((seqs + 1) * 4);
 }
 
 hipError_t launch_draft_verify(VerifyParams p, void* ws, hipStream_t s) {
-    p.chunk = chunk_of(p.vocab);
-    p.chunks = (p.vocab + p.chunk - 1) / p.chunk;
+    p.pieces = (p.vocab + kPiece - 1) / kPiece;
     const size_t T = p.q.T, seqs = p.q.seqs;
     char* at = (char*)ws;
     p.part = (VerifyPart*)at;
-    at += 2 * T * p.chunks * sizeof(VerifyPart);
+    at += 2 * T * p.pieces * sizeof(VerifyPart);
     p.mass = (double*)at;
-    at += up16(seqs * p.chunks * 8);
+    at += up16(seqs * p.pieces * 8);
     p.drawn = (int32_t*)at;
     at += up16(T * 4);
     p.line = (int32_t*)at;

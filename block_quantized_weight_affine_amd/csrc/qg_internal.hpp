@@ -150,10 +150,10 @@ hipError_t launch_kv8_rope(const KvCache& c, const KvSeqs& q, const KvRope& a, i
 hipError_t launch_tree_plan(const KvSeqs& q, const int32_t* parents, uint32_t* mask, int words, int32_t* pos, int window,
                             hipStream_t s);
 
-// Drafted tokens against the target's probabilities.  Set by the launcher: elements a chunk of a row, chunks a row, and
+// Drafted tokens against the target's probabilities.  Set by the launcher: pieces a row, pieces a wavefront takes, and
 // the workspace's parts.
 struct VerifyPart {
-    double sum;  // of exp((l - top) / temperature) over a chunk; NaN where the chunk has a NaN
+    double sum;  // of exp((l - top) / temperature) over a piece of a row; NaN where it has a NaN
     float top;
     int at;      // the first index that holds it
 };
@@ -165,9 +165,9 @@ struct VerifyParams {
     int xt, vocab;
     const float *temps, *accept, *sample;
     int32_t *accepted, *next, *rows_out, *path, *kv_out;
-    int chunk, chunks;
-    VerifyPart* part;     // [target, draft][T][chunks]
-    double* mass;         // [seqs][chunks]
+    int pieces, per;
+    VerifyPart* part;     // [target, draft][T][pieces]
+    double* mass;         // [seqs][pieces]
     int32_t *drawn, *line; // [T]
     uint32_t* tickets;    // [seqs + 1]
 };
