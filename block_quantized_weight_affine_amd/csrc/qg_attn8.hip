@@ -14,6 +14,7 @@ constexpr int64_t kTileFrom = 64;
 // Tokens a split at least, and tokens that are not split however few the heads are: 1024 of 8 heads of 128 take
 // 9.4 us in one launch; 5.8 and 3.8 us in two.
 constexpr int64_t kMinChunk = 256, kAlone = 1024;
+constexpr int64_t kTreeAlone = 1100;  // the same for a tree's tiles of 16 rows
 void set_tiles(AttnParams& a, int xt) {
     const int64_t rows = (int64_t)a.q.max_new * a.group;
     a.tile_rows = rows >= kTileFrom ? attn8_tile_rows(a, xt) : 16;
@@ -52,6 +53,55 @@ int64_t wanted_splits(const AttnParams& a, int xt, int64_t span) {
     }
     return best;
 }
+void set_chunk(AttnParams& a, int64_t span, int64_t chunk) {
+    const int64_t unit = a.tile_rows > 16 ? 64 : 64 * a.row_waves;
+    if (chunk < kMinChunk) chunk = kMinChunk;
+    a.chunk = (int)((chunk + unit - 1) / unit * unit);
+    a.splits = (int)((span + a.chunk - 1) / a.chunk);
+    if (a.splits < 1) a.splits = 1;
+}
+
+// A tree's call: tiles of 16 rows, of 128 or of 256.  16 rows decode the codes for themselves, which takes 5 us for 1000
+// tokens on each CU; a tile of 128 rows takes 22 us, and its workgroups longer to start.  Microseconds of 16 rows and of 128,
+// each at its best splits, bf16, 32 heads of 128 on 8 (drafted rows times 4 a K/V head): 1 sequence of 1000 tokens, 25 / 100
+// drafted rows 10.9 and 20.0 / 11.7 and 22.7; of 8000, 25 / 61: 20.5 and 22.9 / 30.6 and 30.5; 16 of 2000, 16 / 25 / 61: 29 and 37
+// / 47 and 42 / 92 and 58; 16 of up to 8191, 16 / 25 / 61: 52 and 67 / 78 and 71 / 145 and 117; 4 of 30000, f32, heads of 96, 9 / 30:
+// 84 and 127 / 169 and 133; 4 of up to 10000, heads of 256, 30: 36 and 47.
+bool tree_in_rows(const AttnParams& a, int64_t span) {
+    const int64_t rows = (int64_t)a.q.max_new * a.group, r16 = (rows + 15) / 16, r128 = (rows + 127) / 128;
+    const double load = std::max((double)a.q.seqs * a.c.heads * span / 256, 1.0);  // tokens a CU of one tile
+    return r16 < 4.5 * r128 + 2400 / load;
+}
+// Splits that fill the card, and more of them where the tokens are many, as their lengths may differ: tiles of 16 rows 5
+// sequences of up to 120000 tokens 4 splits 130 us, 8 86, 16 82 (f32, 45 rows on 4 heads); 128 rows 5 of up to 30000 6 splits 84 us, 16
+// 73, 16 of up to 8191 2 splits 82 us, 4 70; 256 rows 16 of up to 8191 1 split 198 us, 2 127, 4 136; 5 of up to 30000 6 108 us, 8 90; tiles of
+// 16 rows 16 of up to 8191 (512 workgroups) 1 split 53 us, 2 58.
+// wide: two workgroups a CU.
+int64_t tree_splits(const AttnParams& a, int tile_rows, bool wide, int64_t span) {
+    const int64_t rows = (int64_t)a.q.max_new * a.group;
+    const int64_t base = (int64_t)a.q.seqs * a.c.heads * ((rows + tile_rows - 1) / tile_rows);
+    const bool two = wide && tile_rows == 128;
+    const int64_t full = tile_rows == 16 || two ? 1024 : 320, tokens = two ? 2048 : 4096;
+    if (tile_rows == 16 && (span <= kTreeAlone || base >= 256)) return 1;
+    return std::max<int64_t>({256 / base, std::min(full / base, (span + tokens - 1) / tokens), 1});
+}
+void plan_tree(AttnParams& a, int xt) {
+    int64_t span = a.q.max_kv;
+    if (a.window > 0) span = std::min(span, (int64_t)a.window + a.q.max_new + 64);
+    const int64_t rows = (int64_t)a.q.max_new * a.group, pairs = (int64_t)a.q.seqs * a.c.heads;
+    const bool wide = xt != XT_F32 && a.c.dim <= 128;
+    a.tile_rows = tree_in_rows(a, span) ? 16 : 128;
+    // 256 rows share a stage's decoding where every CU has some 24 stages (16 of 2000 tokens, 244 rows: 58 us of 128, 66 of 256;
+    // of up to 8191: 117 and 110)
+    if (a.tile_rows == 128 && wide && rows > 128 &&
+        (a.q.max_new > kPairTreeRows || pairs * span / 64 * ((rows + 255) / 256) >= 24 * 256))
+        a.tile_rows = 256;
+    a.tiles = (int)((rows + a.tile_rows - 1) / a.tile_rows);
+    const int64_t want = tree_splits(a, a.tile_rows, wide, span);
+    // 8 wavefronts a workgroup, or 4 where there are enough of few tokens (512 of 2000: 29 us, of 8 30; 2048: 91 and 113)
+    a.row_waves = rows_late(xt == XT_F32 ? 2 : 1, a.c.dim) || pairs * a.tiles < 512 || span > 4 * kAlone ? 8 : 4;
+    set_chunk(a, span, (span + want - 1) / want);
+}
 }  // namespace
 
 int attn8_max_splits(AttnParams a) {
@@ -62,17 +112,20 @@ int attn8_max_splits(AttnParams a) {
         const int64_t w = wanted_splits(a, xt, a.q.max_kv);
         if (w > want) want = w;
     }
+    if (a.q.max_new <= kMaxTreeRows)
+        for (int rows : {16, 128, 256})
+            for (bool wide : {false, true}) want = std::max(want, tree_splits(a, rows, wide, a.q.max_kv));
     return (int)(most < want ? most : want);
 }
 
 // Kernel, tiles and splits of a call, from the host's bounds alone.
 void attn8_plan(AttnParams& a, int xt) {
+    if (a.mask) return plan_tree(a, xt);
     set_tiles(a, xt);
     // tokens that a tile's rows may see: all, or their window, started at a multiple of 64
     int64_t span = a.q.max_kv;
     const int64_t seen = (int64_t)a.window + a.tile_rows / a.group + 65;
     if (a.causal && a.window > 0 && seen < span) span = seen;
-    if (a.mask && a.window > 0) span = std::min(span, (int64_t)a.window + a.q.max_new + 64);
     const int64_t want = wanted_splits(a, xt, span);
     int64_t chunk = (span + want - 1) / want;
     // 8 wavefronts a workgroup where its registers let a CU hold one, or there are few (320 workgroups of one
@@ -80,11 +133,7 @@ void attn8_plan(AttnParams& a, int xt) {
     const int64_t groups = want * a.q.seqs * a.c.heads * a.tiles;
     const bool wide = a.tile_rows == 16 && (want == 1 ? groups < 512 : groups <= 256 && chunk >= 1024);
     a.row_waves = rows_late(xt == XT_F32 ? 2 : 1, a.c.dim) || wide ? 8 : 4;
-    const int64_t unit = a.tile_rows > 16 ? 64 : 64 * a.row_waves;
-    if (chunk < kMinChunk) chunk = kMinChunk;
-    a.chunk = (int)((chunk + unit - 1) / unit * unit);
-    a.splits = (int)((span + a.chunk - 1) / a.chunk);
-    if (a.splits < 1) a.splits = 1;
+    set_chunk(a, span, chunk);
 }
 
 size_t attn8_workspace(const AttnParams& a) {

@@ -198,6 +198,7 @@ __device__ __forceinline__ int q_exponent(uint32_t top) {
 // The kernel of tiles of 128 or 256 rows (qg_attn8_tile.hip), and which of them a call takes.
 int attn8_tile_rows(const AttnParams& a, int xt);
 hipError_t launch_attn8_tile(const AttnParams& a, int xt, hipStream_t s);
+constexpr int kPairTreeRows = 128;  // drafted rows of a sequence that two workgroups a CU have shared memory for
 // The same kernels with masks among the batch's rows.
 hipError_t launch_attn8_tree(const AttnParams& a, int xt, hipStream_t s);
 hipError_t launch_attn8_tree_tile(const AttnParams& a, int xt, hipStream_t s);

@@ -62,12 +62,15 @@ __global__ __launch_bounds__(64 * W, W == 4 && rows_registers(XT == XT_F32 ? 2 :
 
     const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // The tiles of a head and split read the same codes: eight workgroups apart, they share a die's cache (8 sequences of
+    // 20000 tokens, 48 rows on each of 8 heads of 128: 146 -> 105 us).
     int b = a.first + blockIdx.x;
-    const int tile = b % a.tiles;
-    b /= a.tiles;
+    const int tile = b / 8 % a.tiles;
+    b = b / 8 / a.tiles * 8 + b % 8;
     const int h = b % a.c.heads;
     b /= a.c.heads;
     const int split = b % a.splits, s = b / a.splits;
+    if (s >= a.q.seqs) return;
     const KvSpan sp = kv8_span(a.q, s);
     const int rows = sp.n * a.group;
     if (tile * 16 >= rows) return;
@@ -426,7 +429,7 @@ constexpr int64_t kJoinWide = 2048;  // rows that are joined by a workgroup each
 
 template <bool TREE, int XT, int D>
 hipError_t launch_one(AttnParams a, hipStream_t s) {
-    const int64_t grid = (int64_t)a.q.seqs * a.splits * a.c.heads * a.tiles;
+    const int64_t grid = ((int64_t)a.q.seqs * a.splits * a.c.heads + 7) / 8 * 8 * a.tiles;
     if (a.tile_rows > 16) {
         const hipError_t e = TREE ? launch_attn8_tree_tile(a, XT, s) : launch_attn8_tile(a, XT, s);
         if (e != hipSuccess) return e;

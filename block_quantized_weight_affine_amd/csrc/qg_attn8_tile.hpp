@@ -15,6 +15,9 @@ typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 
 constexpr int kInfo = 256;  // blocks looked up at a time
+// Two workgroups of the kernel of 128 rows share a CU.
+template <int XT, int D, int NW>
+constexpr bool kPair = NW == 4 && XT != XT_F32 && D <= 128;
 
 // All lanes' LDS reads and writes so far are done, in every wavefront; loads from memory stay in flight.
 __device__ __forceinline__ void lds_barrier() {
@@ -57,7 +60,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // a stage (one wavefront issues an instruction every 6.5 cycles), 32-token stages 10 %, half of the
 // wavefronts half a stage behind the others the same.
 template <bool TREE, int XT, int D, int NW, int CT>
-__global__ __launch_bounds__(64 * NW, NW == 4 && XT != XT_F32 && D <= 128 ? 2 : 1) void attn8_tile_kernel(AttnParams a) {
+__global__ __launch_bounds__(64 * NW, (kPair<XT, D, NW> ? 2 : 1)) void attn8_tile_kernel(AttnParams a) {
     constexpr int NP = XT == XT_F32 ? 2 : 1;  // f16 pieces of a q value and of a weight
     constexpr int NK = D / 16, NT = D / 32;
     constexpr int UN = (D / 16 + NW - 1) / NW;  // 1 KiB pieces of K, and of V, that a wavefront decodes
@@ -70,6 +73,11 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && XT != XT_F32 && D <= 128 ? 2 : 
     __shared__ uint32_t in_sg[2 * kInfo];
     __shared__ int in_top[NW];
     __shared__ FarSum sh_far[NW][CT][64];
+    // A tree's rows: the first token that each may see, and which tokens of the last stages it does; n drafted tokens lie
+    // in no more than (n + 62) / 64 + 1 stages.
+    constexpr int kEdge = ((kPair<XT, D, NW> ? kPairTreeRows : kMaxTreeRows) + 62) / 64 + 1;
+    __shared__ uint64_t sh_vis[TREE ? kEdge : 1][TREE ? 32 * CT * NW : 1];
+    __shared__ int sh_lo[TREE ? 32 * CT * NW : 1];
     bool any_far = false;  // sh_far holds sums
 
     const int lane = threadIdx.x & 63, col = lane & 31, g = lane >> 5;
@@ -123,7 +131,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && XT != XT_F32 && D <= 128 ? 2 : 
 #pragma unroll
     for (int c = 0; c < CT; c++) {
         const int r = min(w0 + 32 * c + col, rows - 1), ri = r / a.group, head = h * a.group + r % a.group;
-        see[c] = row_sight<TREE>(a, sp, ri);
+        if constexpr (!TREE) see[c] = row_sight<TREE>(a, sp, ri);
         const int64_t at = (int64_t)(sp.r0 + ri) * a.q_row + head * a.q_head + 8 * g;
 #pragma unroll
         for (int k = 0; k < NK; k++)
@@ -132,6 +140,17 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && XT != XT_F32 && D <= 128 ? 2 : 
     }
     __builtin_amdgcn_sched_barrier(0);
 
+    if constexpr (TREE) {
+        for (int x = tid; x < BR; x += 64 * NW) {
+            const int i = min(tile * BR + x, rows - 1) / a.group;
+            sh_lo[x] = row_sight<TREE>(a, sp, i).lo;
+            // the first stage that holds a token behind hi_all, and those that follow
+            int tb = t0 + (max(hi_all - t0, 0) & ~63);
+#pragma unroll 1
+            for (int k = 0; k < kEdge && tb < t1; k++, tb += 64)
+                sh_vis[min((tb + 63 - hi_all) >> 6, kEdge - 1)][x] = ones64(hi_all - tb) | drafted_bits(a, sp, i, tb);
+        }
+    }
     int bi0 = -1, e0 = 0, eb = -1000;
     float ks0 = 0.f, vs0 = 0.f;
     if (tid < kInfo) {
@@ -243,12 +262,14 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && XT != XT_F32 && D <= 128 ? 2 : 
             const i32x4_t bi = *(const i32x4_t*)&in_bi[x];
 #pragma unroll
             for (int c = 0; c < CT; c++) {
-                const int jl = see[c].lo - tb - 4 * g, jh = see[c].hi - tb - 4 * g;
+                int jl = 0, jh = 0;
                 uint64_t vis = 0;
                 if constexpr (TREE) {
-                    vis = bits_between64(see[c].lo - tb, see[c].hi - tb);
-                    if (tb + 64 > see[c].hi) vis |= drafted_bits(a, sp, (min(w0 + 32 * c + col, rows - 1)) / a.group, tb);
-                    vis >>= 4 * g;
+                    const int row = wave * 32 * CT + 32 * c + col, edge = (tb + 63 - hi_all) >> 6;
+                    vis = tb + 64 > hi_all ? sh_vis[min(edge, kEdge - 1)][row] : ~0ull;
+                    vis = (vis & ~ones64(sh_lo[row] - tb)) >> (4 * g);
+                } else {
+                    jl = see[c].lo - tb - 4 * g, jh = see[c].hi - tb - 4 * g;
                 }
 #pragma unroll
                 for (int q = 0; q < 4; q++) {

@@ -15,7 +15,7 @@ namespace {
 
 constexpr int kMaxKv = 1 << 24;
 constexpr int kMaxRows = 1 << 21;
-constexpr int kMaxTree = 1024;  // drafted rows of a sequence
+constexpr int kMaxTree = qg::kMaxTreeRows;
 constexpr int kMaxDim = 1024;   // of rows that are turned
 constexpr int kMaxVocab = 1 << 24;
 constexpr int64_t kMaxStride = (int64_t)1 << 40;

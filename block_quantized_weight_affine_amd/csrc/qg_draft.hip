@@ -10,7 +10,7 @@ namespace qg {
 namespace {
 
 // ---- the plan of a tree -------------------------------------------------------------------------------------------
-constexpr int kMaxRows = 1024;  // rows of a sequence
+constexpr int kMaxRows = kMaxTreeRows;
 
 // A workgroup a sequence, a thread a row: it walks up its parents, whose indices fall, and so writes its mask's words
 // from the last to the first.  Bound by latency: lengths, parents, then a step of the walk after the other.

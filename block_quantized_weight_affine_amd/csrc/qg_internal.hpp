@@ -174,6 +174,8 @@ struct VerifyParams {
 size_t verify_workspace(const KvSeqs& q, int vocab);
 hipError_t launch_draft_verify(VerifyParams p, void* ws, hipStream_t s);
 
+constexpr int kMaxTreeRows = 1024;  // drafted rows of a sequence
+
 struct AttnParams {
     KvCache c;
     KvSeqs q;
