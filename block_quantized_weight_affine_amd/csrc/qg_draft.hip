@@ -266,19 +266,22 @@ __global__ __launch_bounds__(256) void verify_part_kernel(VerifyParams p, uint32
     const int s = blockIdx.y, lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const KvSpan sp = kv8_span(p.q, s);
-    if (p.sample) make_table(table);
+    const int count = p.listed ? min(p.listed[s], sp.n) : sp.n;
+    const uint32_t waves = (p.pieces + p.per - 1) / p.per;
     uint32_t b = (group0 + blockIdx.x) * 4 + wave;
     if (b == 0 && lane == 0) {
         p.tickets[s] = 0;
         if (s == 0) p.tickets[p.q.seqs] = 0;
     }
-    const uint32_t waves = (p.pieces + p.per - 1) / p.per;
+    if (!p.draft && (b - wave) / waves >= (uint32_t)count) return;  // nothing for any of the four
+    if (p.sample) make_table(table);
     const int k0 = b % waves * p.per, k1 = min(k0 + p.per, p.pieces);
     b /= waves;
-    const int r = b % p.q.max_new;
-    b /= p.q.max_new;
+    int r = b % p.rows;
+    b /= p.rows;
     const bool of_draft = b == 1;
-    if (b > (p.draft ? 1 : 0) || r >= sp.n || (of_draft && r == sp.n - 1)) return;
+    if (b > (p.draft ? 1 : 0) || r >= count || (of_draft && r == sp.n - 1)) return;
+    if (p.listed) r = p.list[sp.r0 + r];
     const double c = draw_factor(p, s);
     if (of_draft && c == 0.0) return;
     const int64_t row = sp.r0 + r;
@@ -523,59 +526,105 @@ __device__ __forceinline__ void finish(const VerifyParams& p, int s, const KvSpa
     for (int i = total + lane; i < p.q.T; i += 64) p.path[i] = -1;
 }
 
-// Tokens that were chosen: every row draws its own next token, and the sequence follows the rows that hold what was
-// drawn.  A wavefront a row, four of them a workgroup; the last workgroup of a sequence follows it.
+// What follows a row of the target by its own probabilities: the token drawn, or the largest; -1 if there is none.
+template <int XT>
+__device__ __forceinline__ int draw_row(const VerifyParams& p, int64_t row, double c, const double* table) {
+    const VerifyPart* part = p.part + row * p.pieces;
+    const float u = p.sample ? p.sample[row] : 0.f;
+    const Row all = row_of(part, p.pieces, c);
+    if (!row_ok(all.all, c)) return -1;
+    if (c == 0.0) return all.all.at;
+    const double goal = (double)u * all.all.sum;
+    const PieceAt at = find_piece(all, part, p.pieces, c, goal);
+    Mass<XT> mass = {p.target, nullptr, row * p.t_row, 0, Weigh(all.all.top, c, table), Weigh(0.f, c, table), 0.0, 0.0, p.vocab};
+    mass.t_inv = mass.t.rest;
+    return find_in_piece(mass, at.k, goal - at.before);
+}
+__device__ __forceinline__ int parent_of(const VerifyParams& p, const KvSpan& sp, int i) {
+    const int u = p.parents ? p.parents[sp.r0 + i] : i - 1;
+    return u >= 0 && u < i ? u : -1;
+}
+// The first of rows up[] / tok[] that follows `row` and holds `token`; n if none does.  By a wavefront.
+__device__ __forceinline__ int follower(const int* up, const int* tok, int n, int row, int token) {
+    if (token < 0) return n;
+    for (int i0 = row + 1; i0 < n; i0 += 64) {
+        const int i = min(i0 + (int)(threadIdx.x & 63), n - 1);
+        const uint64_t hit = __ballot(i >= i0 && up[i] == row && tok[i] == token);
+        if (hit) return i0 + __builtin_ctzll(hit);
+    }
+    return n;
+}
+
+// The first rows of large trees by themselves, a wavefront a sequence: what follows row 0, and the rows that descend from the
+// one that holds it.  No other can be reached, so only those are looked at afterwards: of 45 rows some ten.
+template <int XT>
+__global__ __launch_bounds__(64) void verify_first_kernel(VerifyParams p) {
+    __shared__ double table[kTable];
+    __shared__ int up[kMaxRows], tok[kMaxRows];
+    __shared__ volatile int in[kMaxRows];
+    const int s = blockIdx.x, lane = threadIdx.x;
+    const KvSpan sp = kv8_span(p.q, s);
+    int listed = 0;
+    if (sp.n > 0) {
+        const double c = draw_factor(p, s);
+        if (c > 0.0) make_table(table);
+        for (int i = lane; i < sp.n; i += 64) up[i] = parent_of(p, sp, i), tok[i] = p.tokens[sp.r0 + i];
+        const int token = draw_row<XT>(p, sp.r0, c, table);
+        if (lane == 0) p.drawn[sp.r0] = token;
+        __syncthreads();
+        const int child = follower(up, tok, sp.n, 0, token);
+        for (int i0 = 0; i0 < sp.n && child < sp.n; i0 += 64) {
+            const int i = i0 + lane;
+            const bool row = i >= child && i < sp.n;
+            const int parent = row ? up[i] : -1;
+            bool on = row && i == child;
+            in[min(i, kMaxRows - 1)] = on;
+            for (;;) {  // parents come before their rows: a turn for each step down within these 64
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
+                const bool more = row && !on && parent >= child && in[parent];
+                if (!__any(more)) break;
+                if (more) on = true, in[i] = 1;
+            }
+            const uint64_t all = __ballot(on);
+            if (on) p.list_out[sp.r0 + listed + __builtin_popcountll(all & ((1ull << lane) - 1))] = i;
+            listed += __builtin_popcountll(all);
+        }
+    }
+    if (lane == 0) p.listed_out[s] = listed;
+}
+
+// Tokens that were chosen: every row, or every one listed, draws its own next token, and the sequence follows the rows that
+// hold what was drawn.  A wavefront a row, four of them a workgroup; the last workgroup of a sequence follows it.
 template <int XT>
 __global__ __launch_bounds__(256) void verify_tree_kernel(VerifyParams p) {
     __shared__ double table[kTable];
     __shared__ int up[kMaxRows], tok[kMaxRows], drew[kMaxRows], line[kMaxRows];
     const int s = blockIdx.y, lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = blockIdx.x * 4 + wave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int r = blockIdx.x * 4 + wave;
     const KvSpan sp = kv8_span(p.q, s);
-    if (blockIdx.x * 4 >= max(sp.n, 1)) return;
+    const int rows = p.listed ? min(p.listed[s], sp.n) : sp.n;
+    if (blockIdx.x * 4 >= max(rows, 1)) return;
     const double c = draw_factor(p, s);
     if (c > 0.0) make_table(table);
-    if (r < sp.n) {
-        const int64_t row = sp.r0 + r;
-        const VerifyPart* part = p.part + row * p.pieces;
-        const float u = p.sample ? p.sample[row] : 0.f;
-        const Row all = row_of(part, p.pieces, c);
-        int token = -1;
-        if (row_ok(all.all, c)) {
-            token = all.all.at;
-            if (c > 0.0) {
-                const double goal = (double)u * all.all.sum;
-                const PieceAt at = find_piece(all, part, p.pieces, c, goal);
-                Mass<XT> mass = {p.target, nullptr, row * p.t_row, 0, Weigh(all.all.top, c, table), Weigh(0.f, c, table), 0.0, 0.0, p.vocab};
-                mass.t_inv = mass.t.rest;
-                token = find_in_piece(mass, at.k, goal - at.before);
-            }
-        }
-        if (lane == 0) hand_over(&p.drawn[row], token);
+    if (r < rows) {
+        if (p.listed) r = p.list[sp.r0 + r];
+        const int token = draw_row<XT>(p, sp.r0 + r, c, table);
+        if (lane == 0) hand_over(&p.drawn[sp.r0 + r], token);
     }
-    if (!last_group_of(&p.tickets[s], (max(sp.n, 1) + 3) / 4)) return;
+    if (!last_group_of(&p.tickets[s], (max(rows, 1) + 3) / 4)) return;
     for (int i = lane; i < sp.n; i += 64) {
-        const int u = p.parents ? p.parents[sp.r0 + i] : i - 1;
-        up[i] = u >= 0 && u < i ? u : -1;
+        up[i] = parent_of(p, sp, i);
         tok[i] = p.tokens[sp.r0 + i];
-        drew[i] = handed(&p.drawn[sp.r0 + i]);
+        drew[i] = handed(&p.drawn[sp.r0 + i]);  // of those that can be reached
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");  // one wavefront is left
-    int cur = 0, count = 0, next = -1;
-    while (cur < sp.n) {  // cur grows
+    int count = 0, next = -1;
+    for (int cur = 0; cur < sp.n;) {  // cur grows
         next = drew[cur];
         if (lane == 0) line[count] = cur;
         count++;
-        int to = sp.n;
-        for (int i0 = cur + 1; i0 < sp.n && next >= 0; i0 += 64) {
-            const int i = min(i0 + lane, sp.n - 1);
-            const uint64_t hit = __ballot(i == i0 + lane && up[i] == cur && tok[i] == next);
-            if (hit) {
-                to = i0 + __builtin_ctzll(hit);
-                break;
-            }
-        }
-        cur = to;
+        cur = follower(up, tok, sp.n, cur, next);
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
     finish(p, s, sp, count, next, line);
@@ -698,12 +747,30 @@ __global__ __launch_bounds__(64 * kChainWaves) void verify_chain_kernel(VerifyPa
 }
 
 template <int XT>
-hipError_t launch_one(VerifyParams p, hipStream_t s) {
-    const int64_t rows = (int64_t)p.q.max_new * (p.draft ? 2 : 1);
-    p.per = (int)std::clamp<int64_t>(rows * p.q.seqs * p.pieces / 8192, 1, 8);
+void launch_parts(VerifyParams p, hipStream_t s) {
+    const int64_t rows = (int64_t)p.rows * (p.draft ? 2 : 1);
+    // a wavefront's start is worth some pieces where all SIMDs have several; of listed rows there are a quarter or so
+    p.per = (int)std::clamp<int64_t>(rows * p.q.seqs * p.pieces / (p.listed ? 4 * 8192 : 8192), 1, 8);
     const int64_t groups = (rows * ((p.pieces + p.per - 1) / p.per) + 3) / 4;
     for (int64_t first = 0; first < groups; first += kLaunchGroups)
         verify_part_kernel<XT><<<dim3((uint32_t)std::min(groups - first, kLaunchGroups), p.q.seqs), 256, 0, s>>>(p, (uint32_t)first);
+}
+
+// Pieces of a batch of trees from which the first rows go before the others, in two launches more (MEASURED).
+constexpr int64_t kFirstFrom = 32768;
+
+template <int XT>
+hipError_t launch_one(VerifyParams p, hipStream_t s) {
+    p.rows = p.q.max_new;
+    if (p.parents && (int64_t)p.q.max_new * p.q.seqs * p.pieces >= kFirstFrom) {
+        p.rows = 1;
+        launch_parts<XT>(p, s);
+        verify_first_kernel<XT><<<p.q.seqs, 64, 0, s>>>(p);
+        p.rows = p.q.max_new;
+        p.listed = p.listed_out;
+        p.list = p.list_out;
+    }
+    launch_parts<XT>(p, s);
     if (p.draft)
         verify_chain_kernel<XT><<<dim3((p.pieces + kChainWaves - 1) / kChainWaves, p.q.seqs), 64 * kChainWaves, 0, s>>>(p);
     else
@@ -723,7 +790,7 @@ hipError_t launch_tree_plan(const KvSeqs& q, const int32_t* parents, uint32_t* m
 
 size_t verify_workspace(const KvSeqs& q, int vocab) {
     const size_t pieces = (vocab + kPiece - 1) / kPiece, T = q.T, seqs = q.seqs;
-    return 2 * T * pieces * sizeof(VerifyPart) + up16(seqs * pieces * 8) + 2 * up16(T * 4) + up16((seqs + 1) * 4);
+    return 2 * T * pieces * sizeof(VerifyPart) + up16(seqs * pieces * 8) + 3 * up16(T * 4) + up16(seqs * 4) + up16((seqs + 1) * 4);
 }
 
 hipError_t launch_draft_verify(VerifyParams p, void* ws, hipStream_t s) {
@@ -738,6 +805,10 @@ hipError_t launch_draft_verify(VerifyParams p, void* ws, hipStream_t s) {
     at += up16(T * 4);
     p.line = (int32_t*)at;
     at += up16(T * 4);
+    p.list_out = (int32_t*)at;
+    at += up16(T * 4);
+    p.listed_out = (int32_t*)at;
+    at += up16(seqs * 4);
     p.tickets = (uint32_t*)at;
     if (p.xt == XT_F32) return launch_one<XT_F32>(p, s);
     if (p.xt == XT_F16) return launch_one<XT_F16>(p, s);

@@ -170,6 +170,9 @@ struct VerifyParams {
     double* mass;         // [seqs][pieces]
     int32_t *drawn, *line; // [T]
     uint32_t* tickets;    // [seqs + 1]
+    int rows;             // rows of a sequence that a launch takes, by their number or
+    const int32_t *list, *listed;       // from a list [T], so many of each sequence [seqs]
+    int32_t *list_out, *listed_out;
 };
 size_t verify_workspace(const KvSeqs& q, int vocab);
 hipError_t launch_draft_verify(VerifyParams p, void* ws, hipStream_t s);
