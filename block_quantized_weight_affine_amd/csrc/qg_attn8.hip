@@ -81,7 +81,7 @@ int64_t tree_splits(const AttnParams& a, int tile_rows, bool wide, int64_t span)
     const int64_t rows = (int64_t)a.q.max_new * a.group;
     const int64_t base = (int64_t)a.q.seqs * a.c.heads * ((rows + tile_rows - 1) / tile_rows);
     const bool two = wide && tile_rows == 128;
-    const int64_t full = tile_rows == 16 || two ? 1024 : 320, tokens = two ? 2048 : 4096;
+    const int64_t full = tile_rows == 16 || two ? 1024 : 256, tokens = two ? 2048 : 4096;
     if (tile_rows == 16 && (span <= kTreeAlone || base >= 256)) return 1;
     return std::max<int64_t>({256 / base, std::min(full / base, (span + tokens - 1) / tokens), 1});
 }
