@@ -756,8 +756,10 @@ void launch_parts(VerifyParams p, hipStream_t s) {
         verify_part_kernel<XT><<<dim3((uint32_t)std::min(groups - first, kLaunchGroups), p.q.seqs), 256, 0, s>>>(p, (uint32_t)first);
 }
 
-// Pieces of a batch of trees from which the first rows go before the others, in two launches more (MEASURED).
-constexpr int64_t kFirstFrom = 32768;
+// Pieces of a batch of trees from which the first rows go before the others, in two launches more.  All rows at once and the
+// first before the others, half of the tokens drawn, bf16: 8 trees of 45 rows of 32000 values (11520 pieces) 21 and 22 us, 16
+// (23040) 29 and 26, 16 of 25 of 131072 (51200) 46 and 30, 64 of 61 of 32000 (124928) 97 and 45.
+constexpr int64_t kFirstFrom = 20000;
 
 template <int XT>
 hipError_t launch_one(VerifyParams p, hipStream_t s) {

@@ -410,6 +410,47 @@ def test_verify_chosen(i, temp):
         print("accepted", got[0][:8], flush=True)
 
 
+LARGE = [
+    # rows of each sequence, how far back a row's parent may be, vocab, type, padding: batches whose first rows go before the others
+    ([90, 0, 1, 2, 63, 64, 65, 88, 33, 90, 17, 45, 90, 5, 70, 31, 32, 90, 1, 80], 9, 20001, "bf16", 3),
+    ([1000, 3, 0, 130], 1, 9000, "f32", 0), ([1024, 1, 40, 700], 30, 9000, "f16", 0),
+]
+
+
+@pytest.mark.parametrize("temp", ["one", "mixed", "none"])
+@pytest.mark.parametrize("i", range(len(LARGE)))
+def test_verify_large_trees(i, temp):
+    """Trees of many rows, whose tokens often are what is drawn, so that the way through them is long; parents that are none, or
+    that do not come before their rows."""
+    rows, back, vocab, xt, padded = LARGE[i]
+    print(f"verify large trees {i} {temp}: {LARGE[i]}", flush=True)
+    assert max(rows) * len(rows) * -(-vocab // 1024) >= 32768
+    rng = np.random.default_rng(170 + i)
+    b = Batch([(n, n + 5) for n in rows], 1, 64, 16, i)
+    target, _ = _inputs(rng, b.T, vocab, xt, 0.3, padded)
+    target *= 4
+    par = np.concatenate([_trees(rng, n, back) for n in rows if n]).astype(np.int32)
+    for at, bad in zip(rng.permutation(b.T)[:20], (-1, -2, 5000, 2 ** 31 - 1, -2 ** 31) * 4):
+        par[at] = bad
+    best = target.argmax(1).cpu().numpy()
+    tokens = rng.integers(0, vocab, b.T)
+    for s, n in enumerate(rows):
+        for r in range(1, n):
+            up = par[b.rows[s] + r]
+            if 0 <= up < r and rng.random() < (0.98 if back == 1 else 0.5):
+                tokens[b.rows[s] + r] = best[b.rows[s] + up]
+    kw = {}
+    if temp != "none":
+        kw["sample"] = rng.random(b.T).astype(np.float32)
+    if temp == "mixed":
+        kw["temps"] = np.where(rng.random(len(rows)) < 0.4, 0, rng.uniform(0.1, 1, len(rows))).astype(np.float32)
+    got = _check_verify(b, tokens, target, parents=par, **kw)
+    print("accepted", got[0], flush=True)
+    target[b.rows[0]] = float("nan")                           # a first row without a largest: nothing follows it
+    got = _check_verify(b, tokens, target, parents=par, **kw)
+    assert got[0][0] == 0 and got[1][0] == -1
+
+
 def test_verify_borders():
     """Draws of 0, of the largest value below 1 and at the edge of a token; ties; tokens that have no probability."""
     inf = float("inf")
