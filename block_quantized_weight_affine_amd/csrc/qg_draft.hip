@@ -76,10 +76,9 @@ __device__ __forceinline__ void exp2_64(double a, const double* table, double& u
     u = fma(y, f, 1.0);
     v = __builtin_amdgcn_ldexp(table[k & (kTable - 1)], k >> 8);
 }
-// The table, by all threads of a workgroup.
+// The table, by all threads of a workgroup, for use behind their next barrier.
 __device__ __forceinline__ void make_table(double* table) {
     for (int i = threadIdx.x; i < kTable; i += blockDim.x) table[i] = exp2_64(i / (double)kTable);
-    __syncthreads();
 }
 
 // A logit's weight below the row's largest; c = log2(e) / temperature.  0 where nothing is left to compare (both
@@ -274,7 +273,10 @@ __global__ __launch_bounds__(256) void verify_part_kernel(VerifyParams p, uint32
         if (s == 0) p.tickets[p.q.seqs] = 0;
     }
     if (!p.draft && (b - wave) / waves >= (uint32_t)count) return;  // nothing for any of the four
-    if (p.sample) make_table(table);
+    if (p.sample) {
+        make_table(table);
+        __syncthreads();
+    }
     const int k0 = b % waves * p.per, k1 = min(k0 + p.per, p.pieces);
     b /= waves;
     int r = b % p.rows;
@@ -330,7 +332,7 @@ __global__ __launch_bounds__(256) void verify_part_kernel(VerifyParams p, uint32
     }
 }
 
-// The probabilities in a draw of the tokens that load_raw gives for i: the target's, less the draft's.
+// The probabilities in a draw of the tokens of a piece, 16 a lane: the target's, less the draft's.
 template <int XT>
 struct Mass {
     const void *target, *draft;
@@ -339,27 +341,39 @@ struct Mass {
     double t_inv, d_inv;  // 1 / sum times the weights' common factor; d_inv 0: the target's alone
     int vocab;
     __device__ __forceinline__ int start(int i) const { return row_start<XT>(i, vocab); }
-    __device__ __forceinline__ void operator()(int i, bool last, double (&m)[8]) const {
-        float v[8], w[8];
-        const Raw8<XT> rt = load_raw<XT>(target, t_at, i, vocab);
-        Raw8<XT> rd;
-        if (d_inv != 0.0) rd = load_raw<XT>(draft, d_at, i, vocab);
-        open_raw<XT>(rt, i, vocab, last, v);
+    __device__ __forceinline__ void operator()(int k, double (&m)[2][8]) const {
+        const int i0 = k * kPiece + 8 * (threadIdx.x & 63);
+        const bool last = (k + 1) * kPiece > vocab, both = d_inv != 0.0;
+        Raw8<XT> rt[2], rd[2];
 #pragma unroll
-        for (int e = 0; e < 8; e++) {
-            double f, g;
-            t(v[e], f, g);
-            m[e] = f * g * t_inv;
+        for (int h = 0; h < 2; h++) rt[h] = load_raw<XT>(target, t_at, i0 + h * kStep, vocab);
+        if (both)
+#pragma unroll
+            for (int h = 0; h < 2; h++) rd[h] = load_raw<XT>(draft, d_at, i0 + h * kStep, vocab);
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            float v[8];
+            open_raw<XT>(rt[h], i0 + h * kStep, vocab, last, v);
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                double f, g;
+                t(v[e], f, g);
+                m[h][e] = f * g * t_inv;
+            }
         }
-        if (d_inv == 0.0) return;
-        open_raw<XT>(rd, i, vocab, last, w);
+        if (!both) return;
 #pragma unroll
-        for (int e = 0; e < 8; e++) {
+        for (int h = 0; h < 2; h++) {
+            float v[8];
+            open_raw<XT>(rd[h], i0 + h * kStep, vocab, last, v);
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
 #pragma clang fp contract(off)  // equal probabilities leave nothing
-            double f, g;
-            d(w[e], f, g);
-            const double q = f * g * d_inv;
-            m[e] = fmax(m[e] - q, 0.0);
+                double f, g;
+                d(v[e], f, g);
+                const double q = f * g * d_inv;
+                m[h][e] = fmax(m[h][e] - q, 0.0);
+            }
         }
     }
 };
@@ -371,8 +385,7 @@ __device__ __forceinline__ int find_in_piece(const M& mass, int k, double goal) 
     const int lane = threadIdx.x & 63, i0 = k * kPiece + 8 * lane;
     double m[2][8], before = 0.0;
     int last = -1;
-#pragma unroll
-    for (int h = 0; h < 2; h++) mass(i0 + h * kStep, (k + 1) * kPiece > mass.vocab, m[h]);
+    mass(k, m);
 #pragma unroll
     for (int h = 0; h < 2; h++) {
         double own = 0.0;
@@ -526,19 +539,20 @@ __device__ __forceinline__ void finish(const VerifyParams& p, int s, const KvSpa
     for (int i = total + lane; i < p.q.T; i += 64) p.path[i] = -1;
 }
 
-// What follows a row of the target by its own probabilities: the token drawn, or the largest; -1 if there is none.
+// What follows a row of the target, whose parts are joined, by its own probabilities: the token drawn, or the largest; -1 if
+// there is none.
 template <int XT>
-__device__ __forceinline__ int draw_row(const VerifyParams& p, int64_t row, double c, const double* table) {
-    const VerifyPart* part = p.part + row * p.pieces;
-    const float u = p.sample ? p.sample[row] : 0.f;
-    const Row all = row_of(part, p.pieces, c);
+__device__ __forceinline__ int draw_row(const VerifyParams& p, const Row& all, int64_t row, double u, double c, const double* table) {
     if (!row_ok(all.all, c)) return -1;
     if (c == 0.0) return all.all.at;
-    const double goal = (double)u * all.all.sum;
-    const PieceAt at = find_piece(all, part, p.pieces, c, goal);
+    const double goal = u * all.all.sum;
+    const PieceAt at = find_piece(all, p.part + row * p.pieces, p.pieces, c, goal);
     Mass<XT> mass = {p.target, nullptr, row * p.t_row, 0, Weigh(all.all.top, c, table), Weigh(0.f, c, table), 0.0, 0.0, p.vocab};
     mass.t_inv = mass.t.rest;
     return find_in_piece(mass, at.k, goal - at.before);
+}
+__device__ __forceinline__ Row row_of(const VerifyParams& p, int64_t row, double c) {
+    return row_of(p.part + row * p.pieces, p.pieces, c);
 }
 __device__ __forceinline__ int parent_of(const VerifyParams& p, const KvSpan& sp, int i) {
     const int u = p.parents ? p.parents[sp.r0 + i] : i - 1;
@@ -567,9 +581,12 @@ __global__ __launch_bounds__(64) void verify_first_kernel(VerifyParams p) {
     int listed = 0;
     if (sp.n > 0) {
         const double c = draw_factor(p, s);
-        if (c > 0.0) make_table(table);
+        const double u = p.sample ? p.sample[sp.r0] : 0.f;
+        const Row first = row_of(p, sp.r0, c);
         for (int i = lane; i < sp.n; i += 64) up[i] = parent_of(p, sp, i), tok[i] = p.tokens[sp.r0 + i];
-        const int token = draw_row<XT>(p, sp.r0, c, table);
+        if (c > 0.0) make_table(table);
+        __syncthreads();
+        const int token = draw_row<XT>(p, first, sp.r0, u, c, table);
         if (lane == 0) p.drawn[sp.r0] = token;
         __syncthreads();
         const int child = follower(up, tok, sp.n, 0, token);
@@ -606,10 +623,18 @@ __global__ __launch_bounds__(256) void verify_tree_kernel(VerifyParams p) {
     const int rows = p.listed ? min(p.listed[s], sp.n) : sp.n;
     if (blockIdx.x * 4 >= max(rows, 1)) return;
     const double c = draw_factor(p, s);
-    if (c > 0.0) make_table(table);
-    if (r < rows) {
+    const bool some = r < rows;
+    Row row;
+    double u = 0.0;
+    if (some) {
         if (p.listed) r = p.list[sp.r0 + r];
-        const int token = draw_row<XT>(p, sp.r0 + r, c, table);
+        if (p.sample) u = p.sample[sp.r0 + r];
+        row = row_of(p, sp.r0 + r, c);
+    }
+    if (c > 0.0) make_table(table);
+    __syncthreads();
+    if (some) {
+        const int token = draw_row<XT>(p, row, sp.r0 + r, u, c, table);
         if (lane == 0) hand_over(&p.drawn[sp.r0 + r], token);
     }
     if (!last_group_of(&p.tickets[s], (max(rows, 1) + 3) / 4)) return;
@@ -651,7 +676,6 @@ __global__ __launch_bounds__(64 * kChainWaves) void verify_chain_kernel(VerifyPa
     }
     constexpr int kRows = kChainWaves / 2;
     const bool draws = c > 0.0;
-    if (draws) make_table(table);
     int e;
     for (int r0 = 0;; r0 += kRows) {
         const int r = r0 + wave % kRows;
@@ -669,6 +693,7 @@ __global__ __launch_bounds__(64 * kChainWaves) void verify_chain_kernel(VerifyPa
                 sh_x[wave] = c == 0.0 ? (double)(x == a.all.at) : there ? weight(l, a.all.top, c) / a.all.sum : 0.0;
             }
         }
+        if (draws && r0 == 0) make_table(table);
         __syncthreads();
         bool stays = false;
         const int ri = r0 + lane;
@@ -702,10 +727,8 @@ __global__ __launch_bounds__(64 * kChainWaves) void verify_chain_kernel(VerifyPa
     const double u = drawn ? (double)p.sample[row] : 0.0;
     if (shared) {
         if (k < p.pieces) {
-            const bool last = (k + 1) * kPiece > p.vocab;
             double v[2][8], sum = 0.0;
-            mass(k * kPiece + 8 * lane, last, v[0]);
-            mass(k * kPiece + kStep + 8 * lane, last, v[1]);
+            mass(k, v);
 #pragma unroll
             for (int x = 0; x < 16; x++) sum += v[x >> 3][x & 7];
             sum = wave_sum(sum);
