@@ -777,8 +777,10 @@ __global__ __launch_bounds__(64 * kChainWaves) void verify_chain_kernel(VerifyPa
 template <int XT>
 void launch_parts(VerifyParams p, hipStream_t s) {
     const int64_t rows = (int64_t)p.rows * (p.draft ? 2 : 1);
-    // a wavefront's start is worth some pieces where all SIMDs have several; of listed rows there are a quarter or so
-    p.per = (int)std::clamp<int64_t>(rows * p.q.seqs * p.pieces / (p.listed ? 4 * 8192 : 8192), 1, 8);
+    // a wavefront's start is worth some pieces where all SIMDs have several, but longer ones even out worse (whole calls of 1 / 3 / 8
+    // pieces, bf16, 128000 logits: 32 users of up to 8 rows 45.5 / 40.5 / 54 us, of 8 rows 62 / 57 / 58, 8 users 30.6 / 30.5 / 33);
+    // of listed rows there are a quarter or so
+    p.per = (int)std::clamp<int64_t>(rows * p.q.seqs * p.pieces / (p.listed ? 4 * 8192 : 8192), 1, 3);
     const int64_t groups = (rows * ((p.pieces + p.per - 1) / p.per) + 3) / 4;
     for (int64_t first = 0; first < groups; first += kLaunchGroups)
         verify_part_kernel<XT><<<dim3((uint32_t)std::min(groups - first, kLaunchGroups), p.q.seqs), 256, 0, s>>>(p, (uint32_t)first);
