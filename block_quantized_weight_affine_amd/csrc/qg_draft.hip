@@ -662,8 +662,8 @@ __global__ __launch_bounds__(256) void verify_tree_kernel(VerifyParams p) {
 // Tokens that were drawn from the draft's probabilities, one after the other: row r + 1's token x stays where
 // accept[r + 1] q(x) < p(x), p and q at row r; the first that does not ends the sequence with a draw from
 // max(p - q, 0), and where all stay the draw is from p at the last row.  Every workgroup finds the row at which the
-// sequence ends, eight rows at a time, a wavefront each for p and for q; for max(p - q, 0) each wavefront then sums a
-// piece, and the last of them draws, else one alone does.  One user 6.8 us, 3 of them until the row is found, 1.4 for the last piece;
+// sequence ends, eight rows at a time, a wavefront each for p and for q; for max(p - q, 0) the first p.per wavefronts then sum a
+// piece each, and the last workgroup draws, else one alone does.  One user 6.8 us, 3 of them until the row is found, 1.4 for the last piece;
 // 32 users of 128000 logits 16.9 us, 5 of them 64-bit instructions of the masses.
 constexpr int kChainWaves = 16;
 template <int XT>
@@ -672,7 +672,8 @@ __global__ __launch_bounds__(64 * kChainWaves) void verify_chain_kernel(VerifyPa
     __shared__ VerifyPart sh_all[kChainWaves];
     __shared__ double sh_x[kChainWaves];  // p(x), q(x); temperature 0: whether x stays
     const int s = blockIdx.y, lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), k = blockIdx.x * kChainWaves + wave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int k = wave < p.per ? blockIdx.x * p.per + wave : p.pieces;  // its piece, if it has one
     const KvSpan sp = kv8_span(p.q, s);
     const double c = draw_factor(p, s);
     if (sp.n == 0) {
@@ -786,6 +787,16 @@ void launch_parts(VerifyParams p, hipStream_t s) {
         verify_part_kernel<XT><<<dim3((uint32_t)std::min(groups - first, kLaunchGroups), p.q.seqs), 256, 0, s>>>(p, (uint32_t)first);
 }
 
+// Pieces of max(p - q, 0) a workgroup: 16, or fewer where that leaves no more workgroups than CUs, as the wavefronts of one wait
+// for each other (16 a workgroup and by this rule: one user of 32000 logits 13.9 and 12.4 us a call, 8 of 128000 30.2 and 28.5, 32 of
+// 32000 29.5 and 27.1; 32 of 128000 by twice as many workgroups 64, by 256 57).
+template <int XT>
+void launch_chains(VerifyParams p, hipStream_t s) {
+    p.per = kChainWaves;
+    while (p.per > 1 && (int64_t)p.q.seqs * ((p.pieces + p.per / 2 - 1) / (p.per / 2)) <= 256) p.per /= 2;
+    verify_chain_kernel<XT><<<dim3((p.pieces + p.per - 1) / p.per, p.q.seqs), 64 * kChainWaves, 0, s>>>(p);
+}
+
 // Pieces of a batch of trees from which the first rows go before the others, in two launches more.  All rows at once and the
 // first before the others, half of the tokens drawn, bf16: 8 trees of 45 rows of 32000 values (11520 pieces) 21 and 22 us, 16
 // (23040) 29 and 26, 16 of 25 of 131072 (51200) 46 and 30, 64 of 61 of 32000 (124928) 97 and 45.
@@ -804,7 +815,7 @@ hipError_t launch_one(VerifyParams p, hipStream_t s) {
     }
     launch_parts<XT>(p, s);
     if (p.draft)
-        verify_chain_kernel<XT><<<dim3((p.pieces + kChainWaves - 1) / kChainWaves, p.q.seqs), 64 * kChainWaves, 0, s>>>(p);
+        launch_chains<XT>(p, s);
     else
         verify_tree_kernel<XT><<<dim3((p.q.max_new + 3) / 4, p.q.seqs), 256, 0, s>>>(p);
     return hipGetLastError();
