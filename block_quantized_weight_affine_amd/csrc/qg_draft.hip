@@ -727,7 +727,7 @@ __global__ __launch_bounds__(64 * kChainWaves) void verify_chain_kernel(VerifyPa
     if (!shared && k > 0) return;
     Mass<XT> mass = {p.target, p.draft, row * p.t_row, row * p.d_row, Weigh(t.top, c, table), Weigh(d_top, c, table), 0.0, 0.0,
                      p.vocab};
-    mass.t_inv = mass.t.rest / t.sum;
+    mass.t_inv = mass.t.rest * (1.0 / t.sum);  // rounded like the draft's, as equal probabilities have to leave nothing
     if (shared) mass.d_inv = mass.d.rest * d_inv;
     double* m = p.mass + (int64_t)s * p.pieces;
     const double u = drawn ? (double)p.sample[row] : 0.0;

@@ -478,6 +478,17 @@ def test_verify_borders():
     assert got[0][0] == 0 and 0 <= got[1][0] < 1000
 
 
+@pytest.mark.parametrize("xt", ["f32", "f16", "bf16"])
+def test_verify_equal_logits_leave_nothing(xt):
+    """A target and a draft of the same logits: what is left of one less the other is nothing, whatever their sums and
+    temperatures, so a token that goes is followed by a draw from the target."""
+    rng = np.random.default_rng(21)
+    b = Batch([(3, 9)] * 96, 1, 64, 16, 1)
+    target, _ = _inputs(rng, b.T, 1500, xt, 0.0, 1)
+    _check_verify(b, np.full(b.T, -1), target, draft=target.clone(), temps=rng.uniform(0.3, 3, 96).astype(np.float32),
+                  sample=rng.random(b.T).astype(np.float32), accept=np.full(b.T, 0.5, np.float32))
+
+
 @pytest.mark.parametrize("xt", ["f32", "bf16"])
 def test_verify_rows_without_probabilities(xt):
     """NaN, infinities and temperatures that are none end a sequence with -1, and reach no other."""
