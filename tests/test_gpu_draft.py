@@ -302,6 +302,20 @@ def test_attend_bad_pages_and_lengths():
         assert torch.all(got[2 * new:] == 9)
 
 
+@pytest.mark.parametrize("new,xt", [(2, "f16"), (12, "bf16"), (12, "f32")])
+def test_attend_many_sequences(new, xt):
+    """More sequences than a wavefront has lanes, of very different lengths and split."""
+    print(f"attend many sequences {new} {xt}", flush=True)
+    rng = np.random.default_rng(9)
+    lens = [(int(n), int(n + rng.integers(0, 1 << int(rng.integers(1, 13))))) for n in rng.integers(0, new + 1, 71)]
+    b = Batch(lens, 1, 64, 32, 31, max_kv=5000).upload()
+    par = np.concatenate([_trees(b.rng, n, 4) for n, _ in lens if n]).astype(np.int32)
+    mask, pos = od.plan(par, b.spans(), 1, 0, b.T)
+    q = _values(b.rng, (b.T, 8, 64), xt).cuda()
+    got = _attend(b, q, 8, 0.125, mask, 0, None)
+    _check_attend(b, q, xt, 8, 0.125, mask, 0, pos, got)
+
+
 def test_a_chain_of_masks_is_causal():
     """Masks of all rows up to one's own: what qg_attn_kv8 computes."""
     for new, q_heads, xt in ((7, 4, "bf16"), (90, 4, "f16")):
@@ -624,6 +638,50 @@ def test_a_step_and_the_rows_that_stay():
     serve8.kv8_write(b.vc, b.vs, b.table, sp, st.v[pick].float().cpu().numpy())
     b.kv_len, b.rows = kv, rows                            # what lies behind is of no sequence
     _check_cache(b, None, None)
+
+
+@pytest.mark.parametrize("drawn", [False, True])
+def test_captured_verification_of_many_rows(drawn):
+    """Large trees, and many users' drafts with probabilities, verified in a graph: every replay on other inputs gives the plain
+    result, with eager work and another graph on the same workspace between."""
+    rows, vocab = ([8, 3, 0, 6] * 8, 9000) if drawn else ([130, 1, 77, 200], 26000)
+    print(f"captured verification drawn={drawn}", flush=True)
+    b = Batch([(n, n + 5) for n in rows], 1, 64, 16, 3)
+    n, T = len(rows), b.T
+    seqs = qg.kv8_seqs(_dev(b.table), _dev(b.rows), _dev(b.kv_len), T, b.max_new, b.max_kv)
+    work = torch.full((qg.qg_draft_verify_workspace(seqs, vocab),), 255, dtype=torch.uint8, device="cuda")
+    target, draft = (torch.zeros(T, vocab, device="cuda") for _ in "td")
+    sample, accept = (torch.zeros(T, device="cuda") for _ in "sa")
+    tokens, parents = (torch.zeros(T, dtype=torch.int32, device="cuda") for _ in "tp")
+    kw = dict(draft=draft, accept=accept) if drawn else dict(parents=parents)
+    outs = [[torch.full((m,), -9, dtype=torch.int32, device="cuda") for m in (n, n, n + 1, T, n)] for _ in range(2)]
+    graphs = []
+    for o in outs:
+        qg.qg_draft_verify(seqs, tokens, target, *o, sample=sample, workspace=work, **kw)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            qg.qg_draft_verify(seqs, tokens, target, *o, sample=sample, workspace=work, **kw)
+    for turn in range(3):
+        rng = np.random.default_rng(40 + turn)
+        p, q = _inputs(rng, T, vocab, "f32", 0.4)
+        target.copy_(p)
+        draft.copy_(q)
+        sample.copy_(_dev(rng.random(T).astype(np.float32)))
+        accept.copy_(_dev(rng.random(T).astype(np.float32)))
+        par = np.concatenate([_trees(rng, r, 5) for r in rows if r]).astype(np.int32)
+        parents.copy_(_dev(par))
+        up = torch.from_numpy(np.repeat(b.rows[:-1], rows) + (np.concatenate([np.arange(r) - 1 for r in rows]) if drawn else par))
+        tokens.copy_(torch.where(torch.rand(T, device="cuda") < 0.6, p.argmax(1)[up.clamp(min=0).cuda()].int(), 5))
+        torch.cuda.synchronize()
+        plain = {k: v.double().cpu().numpy() if v.is_floating_point() else v.cpu().numpy() for k, v in kw.items()}
+        want = od.verify(b.spans(), b.kv_len, T, tokens.cpu().numpy(), p.double().cpu().numpy(), sample.cpu().numpy(), **plain)
+        for g in graphs + graphs[:1]:
+            g.replay()
+        torch.cuda.synchronize()
+        for o in outs:
+            for x, y in zip(o, want):
+                assert np.array_equal(x.cpu().numpy(), y)
 
 
 def test_captured_steps_replay():
