@@ -12,29 +12,65 @@ namespace {
 // ---- the plan of a tree -------------------------------------------------------------------------------------------
 constexpr int kMaxRows = kMaxTreeRows;
 
-// A workgroup a sequence, a thread a row: it walks up its parents, whose indices fall, and so writes its mask's words
-// from the last to the first.  Bound by latency: lengths, parents, then a step of the walk after the other.  A tree of 25 rows
-// 1.9 us, 64 trees of up to 255 rows 6.4 us.
-__global__ __launch_bounds__(256) void tree_plan_kernel(KvSeqs q, const int32_t* parents, uint32_t* mask, int words,
-                                                        int32_t* pos, int window) {
-    __shared__ int up[kMaxRows];
+// A workgroup a sequence.  A parent's index is below its row's, so rows go in groups of 64, of which a wavefront first finds
+// what a row's ancestors within the group are, a lane a row, doubling the steps that all of them know (6 turns at most), and
+// the row that those follow; groups then take the rest of that row's mask, one after the other.  A row's depth is the number
+// of its mask's bits, and a window keeps the last ones.  Bound by latency: lengths, parents, turns.  A tree of 25 rows 2.6
+// us; 64 trees of 255 rows, each following one of two before it, 5.2, and 8 chains of 1000 16.7, by 256 threads 33 (a thread a row
+// that walks up all of its parents: 2.7, 20 and 264).
+template <int N>
+__global__ __launch_bounds__(N) void tree_plan_kernel(KvSeqs q, const int32_t* parents, uint32_t* mask, int words, int32_t* pos,
+                                                     int window) {
+    constexpr int kThreads = N;
+    __shared__ uint32_t bits[N][N / 32 + 1];  // of row r the words up to its group's
+    __shared__ int follows[N], lowest[N];     // the earlier group's row that a row descends from, -1; the first row of its window
     const KvSpan sp = kv8_span(q, blockIdx.x);
-    for (int r = threadIdx.x; r < sp.n; r += 256) {
-        const int p = parents[sp.r0 + r];
-        up[r] = p >= 0 && p < r ? p : -1;
+    const int lane = threadIdx.x & 63;
+    for (int r = threadIdx.x; r < (sp.n + 63 & ~63); r += kThreads) {
+        const int g = r & ~63, p = r < sp.n ? parents[sp.r0 + r] : -1;
+        int up = p >= g && p < r ? p - g : -1, from = p >= 0 && p < g ? p : -1;
+        uint32_t lo = lane < 32 ? 1u << lane : 0, hi = lane < 32 ? 0 : 1u << (lane - 32);
+        while (__any(up >= 0)) {
+            const int at = max(up, 0);
+            const uint32_t l = __shfl(lo, at), h = __shfl(hi, at);
+            const int u = __shfl(up, at), f = __shfl(from, at);
+            if (up >= 0) lo |= l, hi |= h, up = u, from = f;
+        }
+        bits[r][g / 32] = lo;
+        bits[r][g / 32 + 1] = hi;
+        follows[r] = from;
     }
     __syncthreads();
-    for (int r = threadIdx.x; r < sp.n; r += 256) {
-        uint32_t* out = mask + (int64_t)(sp.r0 + r) * words;
-        int depth = 0, w = words - 1;
-        uint32_t bits = 0;
-        for (int a = r; a >= 0; a = up[a], depth++) {
-            if (window > 0 && depth >= window) continue;
-            for (; w > a >> 5; w--) out[w] = bits, bits = 0;
-            bits |= 1u << (a & 31);
+    for (int g = 64; g < sp.n; g += 64) {
+        for (int x = threadIdx.x; x < 64 * (g / 32); x += kThreads) {
+            const int r = g + (x & 63), w = x >> 6, from = follows[r];
+            bits[r][w] = from >= 0 && w <= (from >> 5 | 1) ? bits[from][w] : 0;
         }
-        for (; w >= 0; w--) out[w] = bits, bits = 0;
+        __syncthreads();
+    }
+    for (int r = threadIdx.x; r < sp.n; r += kThreads) {
+        int depth = 0, low = 0;
+        for (int w = r >> 5; w >= 0; w--) {
+            const uint32_t x = bits[r][w];
+            const int need = window - depth;  // the window's first row is the one that has so many from it on
+            depth += __builtin_popcount(x);
+            if (window > 0 && need > 0 && depth >= window) {
+                int at = 0;
+#pragma unroll
+                for (int b = 16; b > 0; b >>= 1)
+                    if (__builtin_popcount(x >> (at + b)) >= need) at += b;
+                low = 32 * w + at;
+            }
+        }
+        lowest[r] = low;
         pos[sp.r0 + r] = sp.len - sp.n + depth - 1;
+    }
+    __syncthreads();
+    for (int x = threadIdx.x; x < sp.n * words; x += kThreads) {
+        const int r = x / words, w = x - r * words, low = lowest[r];
+        uint32_t out = w <= r >> 5 ? bits[r][w] : 0;
+        if (w <= low >> 5) out = w < low >> 5 ? 0 : out & ~0u << (low & 31);
+        mask[(int64_t)sp.r0 * words + x] = out;
     }
 }
 
@@ -260,7 +296,7 @@ __device__ __forceinline__ bool row_ok(const VerifyPart& a, double c) {
 
 // Pieces of a row by a wavefront, p.per of them one after the other, the next one's values on their way: each piece's
 // largest logit, where that stands first (temperature 0), and the sum of weights below it.  Bound by vector instructions, 18 a
-// logit: 32 users' seven drafts, 128000 bf16 logits a row, 30.5 us; one user's five of 32000 4.4 us, a launch and its loads.
+// logit: 32 users' seven drafts, 128000 bf16 logits a row, 24 us; one user's five of 32000 4.4 us, a launch and its loads.
 template <int XT>
 __global__ __launch_bounds__(256) void verify_part_kernel(VerifyParams p, uint32_t group0) {
     __shared__ double table[kTable];
@@ -663,8 +699,8 @@ __global__ __launch_bounds__(256) void verify_tree_kernel(VerifyParams p) {
 // accept[r + 1] q(x) < p(x), p and q at row r; the first that does not ends the sequence with a draw from
 // max(p - q, 0), and where all stay the draw is from p at the last row.  Every workgroup finds the row at which the
 // sequence ends, eight rows at a time, a wavefront each for p and for q; for max(p - q, 0) the first p.per wavefronts then sum a
-// piece each, and the last workgroup draws, else one alone does.  One user 6.8 us, 3 of them until the row is found, 1.4 for the last piece;
-// 32 users of 128000 logits 16.9 us, 5 of them 64-bit instructions of the masses.
+// piece each, and the last workgroup draws, else one alone does.  One user 6.4 us, 3 of them until the row is found, 1.4 for the last piece;
+// 32 users of 128000 logits 16.4 us, 5 of them 64-bit instructions of the masses.
 constexpr int kChainWaves = 16;
 template <int XT>
 __global__ __launch_bounds__(64 * kChainWaves) void verify_chain_kernel(VerifyParams p) {
@@ -827,7 +863,12 @@ size_t up16(size_t n) { return (n + 15) / 16 * 16; }
 
 hipError_t launch_tree_plan(const KvSeqs& q, const int32_t* parents, uint32_t* mask, int words, int32_t* pos, int window,
                             hipStream_t s) {
-    tree_plan_kernel<<<q.seqs, 256, 0, s>>>(q, parents, mask, words, pos, window);
+    if (q.max_new <= 64)
+        tree_plan_kernel<64><<<q.seqs, 64, 0, s>>>(q, parents, mask, words, pos, window);
+    else if (q.max_new <= 256)
+        tree_plan_kernel<256><<<q.seqs, 256, 0, s>>>(q, parents, mask, words, pos, window);
+    else
+        tree_plan_kernel<kMaxRows><<<q.seqs, kMaxRows, 0, s>>>(q, parents, mask, words, pos, window);
     return hipGetLastError();
 }
 

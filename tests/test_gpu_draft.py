@@ -159,7 +159,8 @@ def test_write_rope_bad_tables(new):
 
 @pytest.mark.parametrize("lens,words,window", [
     ([(1, 1)], 1, 0), ([(25, 1025)], 1, 0), ([(32, 40), (33, 33), (0, 9), (31, 1000)], 2, 0), ([(64, 64), (65, 100)], 7, 3),
-    ([(200, 5000), (1, 2), (199, 199)], 7, 1), ([(1024, 1024), (1000, 100000)], 32, 0)])
+    ([(200, 5000), (1, 2), (199, 199)], 7, 1), ([(1024, 1024), (1000, 100000)], 32, 0),
+    ([(1000, 1200), (5, 9), (0, 3), (8, 8)], 32, 7), ([(255, 300), (1000, 1000), (1024, 5000)], 32, 300), ([(256, 256)] * 9, 8, 255)])
 def test_plan(lens, words, window):
     print(f"plan {lens} words={words} window={window}", flush=True)
     rng = np.random.default_rng(len(lens))
