@@ -590,45 +590,41 @@ def rotary(freqs, interleaved=False, mscale=1.0):
     return _Desc(QgRotary(freqs.data_ptr(), 2 * freqs.numel(), int(bool(interleaved)), mscale), (freqs,))
 
 
-def _ints(where, n, *tensors):
-    """Contiguous int32 tensors of at least n values."""
-    for x in tensors:
-        if x is not None:
-            if x.dtype is not _int32:
-                raise QGError(QG_EINVAL, where)
-            if x.numel() < n:
-                raise QGError(QG_ESHAPE, where)
-            if not x.is_contiguous():
-                raise QGError(QG_EALIGN, where)
+def _int(where, n, x):
+    """A contiguous int32 tensor of at least n values."""
+    if x.dtype is not _int32:
+        raise QGError(QG_EINVAL, where)
+    if x.numel() < n:
+        raise QGError(QG_ESHAPE, where)
+    if not x.is_contiguous():
+        raise QGError(QG_EALIGN, where)
 
 
-def _floats(where, n, *tensors):
-    """Contiguous f32 tensors of at least n values."""
-    for x in tensors:
-        if x is not None:
-            if _XT.get(x.dtype) != QG_X_F32:
-                raise QGError(QG_EINVAL, where)
-            if x.numel() < n:
-                raise QGError(QG_ESHAPE, where)
-            if not x.is_contiguous():
-                raise QGError(QG_EALIGN, where)
+def _float(where, n, x):
+    """A contiguous f32 tensor of at least n values."""
+    if _XT.get(x.dtype) != QG_X_F32:
+        raise QGError(QG_EINVAL, where)
+    if x.numel() < n:
+        raise QGError(QG_ESHAPE, where)
+    if not x.is_contiguous():
+        raise QGError(QG_EALIGN, where)
 
 
 def qg_rope(rot, pos, x, y, stream=None):
     """x [T][heads][dim] (any row and head strides) at positions pos [T] turned into y, which may be x."""
     call = _entries.get("qg_rope") or _entry("qg_rope")
-    xt = x.dtype
-    if xt is not y.dtype or xt not in _XT:
+    xt, shape = _XT.get(x.dtype), x.shape
+    if x.dtype is not y.dtype or xt is None:
         raise QGError(QG_EINVAL, "qg_rope")
-    if x.dim() != 3 or x.shape != y.shape:
+    if len(shape) != 3 or y.shape != shape:
         raise QGError(QG_ESHAPE, "qg_rope")
-    T, heads, dim = x.shape
-    _ints("qg_rope", T, pos)
+    T, heads, dim = shape
+    _int("qg_rope", T, pos)
     x_row, x_head, x_one = x.stride()
     y_row, y_head, y_one = y.stride()
     if x_one != 1 or y_one != 1:
         raise QGError(QG_EALIGN, "qg_rope")
-    status = call(rot.ptr, pos.data_ptr(), x.data_ptr(), x_row, x_head, y.data_ptr(), y_row, y_head, _XT[xt], T, heads, dim,
+    status = call(rot.ptr, pos.data_ptr(), x.data_ptr(), x_row, x_head, y.data_ptr(), y_row, y_head, xt, T, heads, dim,
                   _stream(stream))
     if status:
         raise QGError(status, "qg_rope")
@@ -639,30 +635,33 @@ def qg_kv8_write_rope(cache, seqs, rot, k, v, q=None, q_out=None, pos=None, src=
     than the rows' places; src [T]: row r is row src[r] of k and v, which then have any number of rows."""
     where = "qg_kv8_write_rope"
     call = _entries.get(where) or _entry(where)
-    xt, rows, inner = k.dtype, k.shape[0], (cache.heads, cache.dim)
-    if xt is not v.dtype or xt not in _XT:
+    xt, shape, dim, T = _XT.get(k.dtype), k.shape, cache.dim, seqs.T
+    if k.dtype is not v.dtype or xt is None:
         raise QGError(QG_EINVAL, where)
-    if k.shape[1:] != inner or v.shape != k.shape or (src is None and rows != seqs.T):
+    if len(shape) != 3 or shape[1] != cache.heads or shape[2] != dim or v.shape != shape or (src is None and shape[0] != T):
         raise QGError(QG_ESHAPE, where)
-    if pos is not None or src is not None:
-        _ints(where, seqs.T, pos, src)
+    if pos is not None:
+        _int(where, T, pos)
+    if src is not None:
+        _int(where, T, src)
     k_row, k_head, k_one = k.stride()
     v_row, v_head, v_one = v.stride()
     if k_one != 1 or v_one != 1:
         raise QGError(QG_EALIGN, where)
     qs = (None, 0, 0, None, 0, 0, 0)
     if q is not None:
-        if q_out is None or q.dtype is not xt or q_out.dtype is not xt:
+        if q_out is None or q.dtype is not k.dtype or q_out.dtype is not k.dtype:
             raise QGError(QG_EINVAL, where)
-        if q.dim() != 3 or q.shape != q_out.shape or q.shape[0] != seqs.T or q.shape[2] != cache.dim or q.shape[1] == 0:
+        turned = q.shape
+        if len(turned) != 3 or q_out.shape != turned or turned[0] != T or turned[2] != dim or turned[1] == 0:
             raise QGError(QG_ESHAPE, where)
         q_row, q_head, q_one = q.stride()
         o_row, o_head, o_one = q_out.stride()
         if q_one != 1 or o_one != 1:
             raise QGError(QG_EALIGN, where)
-        qs = (q.data_ptr(), q_row, q_head, q_out.data_ptr(), o_row, o_head, q.shape[1])
+        qs = (q.data_ptr(), q_row, q_head, q_out.data_ptr(), o_row, o_head, turned[1])
     status = call(cache.ptr, seqs.ptr, rot.ptr, None if pos is None else pos.data_ptr(), k.data_ptr(), k_row, k_head,
-                  v.data_ptr(), v_row, v_head, None if src is None else src.data_ptr(), rows, *qs, _XT[xt], _stream(stream))
+                  v.data_ptr(), v_row, v_head, None if src is None else src.data_ptr(), shape[0], *qs, xt, _stream(stream))
     if status:
         raise QGError(status, where)
 
@@ -671,18 +670,20 @@ def _masks(where, seqs, mask):
     """Words of a mask [T][words]."""
     if mask.dtype is not _int32:
         raise QGError(QG_EINVAL, where)
-    if mask.dim() != 2 or mask.shape[0] < seqs.T:
+    shape = mask.shape
+    if len(shape) != 2 or shape[0] < seqs.T:
         raise QGError(QG_ESHAPE, where)
     if not mask.is_contiguous():
         raise QGError(QG_EALIGN, where)
-    return mask.shape[1]
+    return shape[1]
 
 
 def qg_tree_plan(seqs, parents, mask, pos, window=0, stream=None):
     """Masks (int32 [T][words]) and positions (int32 [T]) of a batch of trees from their parents [T]."""
     call = _entries.get("qg_tree_plan") or _entry("qg_tree_plan")
     words = _masks("qg_tree_plan", seqs, mask)
-    _ints("qg_tree_plan", seqs.T, parents, pos)
+    _int("qg_tree_plan", seqs.T, parents)
+    _int("qg_tree_plan", seqs.T, pos)
     status = call(seqs.ptr, parents.data_ptr(), mask.data_ptr(), words, pos.data_ptr(), window, _stream(stream))
     if status:
         raise QGError(status, "qg_tree_plan")
@@ -693,21 +694,21 @@ def qg_attn_kv8_tree(cache, seqs, mask, q, o, q_heads, scale, window=0, pos=None
     [T][words]); pos [T] is read with a window alone.  Workspace as for qg_attn_kv8."""
     where = "qg_attn_kv8_tree"
     call = _entries.get(where) or _entry(where)
-    xt, shape = q.dtype, (seqs.T, q_heads, cache.dim)
-    if xt is not o.dtype or xt not in _XT:
+    xt, shape = _XT.get(q.dtype), (seqs.T, q_heads, cache.dim)
+    if q.dtype is not o.dtype or xt is None:
         raise QGError(QG_EINVAL, where)
     if q.shape != shape or o.shape != shape:
         raise QGError(QG_ESHAPE, where)
     words = _masks(where, seqs, mask)
     if pos is not None:
-        _ints(where, seqs.T, pos)
+        _int(where, shape[0], pos)
     q_row, q_head, q_one = q.stride()
     o_row, o_head, o_one = o.stride()
     if q_one != 1 or o_one != 1:
         raise QGError(QG_EALIGN, where)
     wp, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
     status = call(cache.ptr, seqs.ptr, mask.data_ptr(), words, None if pos is None else pos.data_ptr(), q.data_ptr(), q_row,
-                  q_head, o.data_ptr(), o_row, o_head, _XT[xt], q_heads, scale, window, wp, size, _stream(stream))
+                  q_head, o.data_ptr(), o_row, o_head, xt, q_heads, scale, window, wp, size, _stream(stream))
     if status:
         raise QGError(status, where)
 
@@ -724,23 +725,26 @@ def qg_draft_verify(seqs, tokens, target, accepted, next, rows_out, path, kv_out
     chains); workspace: a device tensor of at least qg_draft_verify_workspace bytes."""
     where = "qg_draft_verify"
     call = _entries.get(where) or _entry(where)
-    xt, T, n = target.dtype, seqs.T, seqs.struct.seqs
-    if xt not in _XT or (draft is not None and draft.dtype is not xt):
+    xt, shape, T, n = _XT.get(target.dtype), target.shape, seqs.T, seqs.struct.seqs
+    if xt is None or (draft is not None and draft.dtype is not target.dtype):
         raise QGError(QG_EINVAL, where)
-    if target.dim() != 2 or target.shape[0] < T or (draft is not None and draft.shape != target.shape):
+    if len(shape) != 2 or shape[0] < T or (draft is not None and draft.shape != shape):
         raise QGError(QG_ESHAPE, where)
     t_row, one = target.stride()
     d_row, d_one = (0, 1) if draft is None else draft.stride()
     if one != 1 or d_one != 1:
         raise QGError(QG_EALIGN, where)
-    _ints(where, T, tokens, path, parents)
-    _ints(where, n, accepted, next, kv_out)
-    _ints(where, n + 1, rows_out)
-    _floats(where, T, sample, accept)
-    _floats(where, n, temps)
+    for x in (tokens, path) if parents is None else (tokens, path, parents):
+        _int(where, T, x)
+    for x in (accepted, next, kv_out):
+        _int(where, n, x)
+    _int(where, n + 1, rows_out)
+    for x, least in ((sample, T), (accept, T), (temps, n)):
+        if x is not None:
+            _float(where, least, x)
     wp, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
     status = call(seqs.ptr, None if parents is None else parents.data_ptr(), tokens.data_ptr(), target.data_ptr(), t_row,
-                  None if draft is None else draft.data_ptr(), d_row, _XT[xt], target.shape[1],
+                  None if draft is None else draft.data_ptr(), d_row, xt, shape[1],
                   None if temps is None else temps.data_ptr(), None if accept is None else accept.data_ptr(),
                   None if sample is None else sample.data_ptr(), accepted.data_ptr(), next.data_ptr(), rows_out.data_ptr(),
                   path.data_ptr(), kv_out.data_ptr(), wp, size, _stream(stream))
