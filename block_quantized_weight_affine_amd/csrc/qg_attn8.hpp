@@ -195,7 +195,7 @@ __device__ __forceinline__ int q_exponent(uint32_t top) {
     return eb == 0 || eb == 255 ? 0 : 141 - eb;
 }
 
-// The kernel of tiles of 128 or 256 rows (qg_attn8_tile.hip), and which of them a call takes.
+// The kernel of tiles of 128 or 256 rows (qg_attn8_tile.hpp), and which of them a call takes.
 int attn8_tile_rows(const AttnParams& a, int xt);
 hipError_t launch_attn8_tile(const AttnParams& a, int xt, hipStream_t s);
 constexpr int kPairTreeRows = 128;  // drafted rows of a sequence that two workgroups a CU have shared memory for
