@@ -137,14 +137,14 @@ __device__ __forceinline__ int v_exponent(float vs) {
 }
 
 // Tokens [lo, hi) that row i of a sequence sees.  TREE: those before the batch's rows; of these it sees the ones that
-// its mask has.
+// its mask has, however small the window.
 template <bool TREE>
 __device__ __forceinline__ KvSight row_sight(const AttnParams& a, const KvSpan& sp, int i) {
     if constexpr (!TREE) return kv8_sight(sp, i, a.causal, a.window);
     const int hist = sp.len - sp.n;
     int p = sp.len - 1;
     if (a.window > 0) p = min(max(a.pos[sp.r0 + i], hist), sp.len - 1);
-    return KvSight{a.window > 0 ? max(p - a.window + 1, 0) : 0, hist};
+    return KvSight{a.window > 0 ? min(max(p - a.window + 1, 0), hist) : 0, hist};
 }
 // The same for the first or last row of some, so that every one of them sees lo and what follows it from `last` on, and
 // none sees what lies before `first`'s lo.  A tree's rows have positions in no order.
