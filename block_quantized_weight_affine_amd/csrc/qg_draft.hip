@@ -294,6 +294,11 @@ __device__ __forceinline__ bool row_ok(const VerifyPart& a, double c) {
     return c > 0.0 && a.sum > 0.0 && a.sum < __builtin_inf();
 }
 
+// The r-th row listed of a sequence; one that overlaps another may find the other's.
+__device__ __forceinline__ int listed_row(const VerifyParams& p, const KvSpan& sp, int r) {
+    return min(p.list[sp.r0 + r], sp.n - 1);
+}
+
 // Pieces of a row by a wavefront, p.per of them one after the other, the next one's values on their way: each piece's
 // largest logit, where that stands first (temperature 0), and the sum of weights below it.  Bound by vector instructions, 18 a
 // logit: 32 users' seven drafts, 128000 bf16 logits a row, 24 us; one user's five of 32000 4.4 us, a launch and its loads.
@@ -321,7 +326,7 @@ __global__ __launch_bounds__(256) void verify_part_kernel(VerifyParams p, uint32
     b /= p.rows;
     const bool of_draft = b == 1;
     if (b > (p.draft ? 1 : 0) || r >= count || (of_draft && r == sp.n - 1)) return;
-    if (p.listed) r = p.list[sp.r0 + r];
+    if (p.listed) r = listed_row(p, sp, r);
     const double c = draw_factor(p, s);
     if (of_draft && c == 0.0) return;
     const int64_t row = sp.r0 + r;
@@ -522,7 +527,7 @@ __device__ __forceinline__ bool last_group_of(uint32_t* ticket, uint32_t n) {
 }
 
 // Ends a sequence of span sp whose rows line[0 .. count - 1] stay (counted from its first; NULL: 0 .. count - 1): the last
-// sequence to end packs the rows of all.  By a wavefront.
+// sequence to end packs the rows of all, T at most, as sequences that overlap could have more.  By a wavefront.
 __device__ __forceinline__ void finish(const VerifyParams& p, int s, const KvSpan& sp, int count, int next, const int* line) {
     const int lane = threadIdx.x & 63;
     if (lane == 0) p.next[s] = next;
@@ -559,7 +564,7 @@ __device__ __forceinline__ void finish(const VerifyParams& p, int s, const KvSpa
             if (lane >= o) run += u;
         }
         if (s < p.q.seqs) {
-            const int to = total + run - count;
+            const int to = min(total + run - count, p.q.T), end = min(to + count, p.q.T);
             p.rows_out[s] = to;
             p.kv_out[s] = kv - sp.n + count;
             for (int i = 0; i < count; i += 8) {
@@ -568,12 +573,12 @@ __device__ __forceinline__ void finish(const VerifyParams& p, int s, const KvSpa
                 for (int j = 0; j < 8; j++) r[j] = line ? handed(&p.line[sp.r0 + min(i + j, count - 1)]) : i + j;
 #pragma unroll
                 for (int j = 0; j < 8; j++)
-                    if (i + j < count) p.path[to + i + j] = sp.r0 + r[j];
+                    if (to + i + j < end) p.path[to + i + j] = sp.r0 + r[j];
             }
         }
         total += __shfl(run, 63);
     }
-    if (lane == 0) p.rows_out[p.q.seqs] = total;
+    if (lane == 0) p.rows_out[p.q.seqs] = min(total, p.q.T);
     for (int i = total + lane; i < p.q.T; i += 64) p.path[i] = -1;
 }
 
@@ -667,7 +672,7 @@ __global__ __launch_bounds__(256) void verify_tree_kernel(VerifyParams p) {
     Row row;
     double u = 0.0;
     if (some) {
-        if (p.listed) r = p.list[sp.r0 + r];
+        if (p.listed) r = listed_row(p, sp, r);
         if (p.sample) u = p.sample[sp.r0 + r];
         row = row_of(p, sp.r0 + r, c);
     }

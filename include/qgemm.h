@@ -639,7 +639,8 @@ qg_status qg_attn_kv8_tree(const qg_kv8_cache* cache, const qg_kv8_seqs* seqs, c
  * accept and sample: f32 [T] in [0, 1).  Logits may be -inf; a row with a NaN, with nothing but -inf, or (drawn from) with
  * +inf, and a temperature below 0, NaN or infinite have no next token: -1, and nothing after that row stays.  A draft row
  * without probabilities gives its token up, and the next one is drawn from p.  Drafted tokens outside of 0 .. vocab - 1
- * never stay.  A sequence without rows: accepted 0, next -1.
+ * never stay.  A sequence without rows: accepted 0, next -1.  Of sequences whose rows overlap the results are not specified;
+ * path ends at T rows.
  * All probabilities and sums are in 64 bits; the result is the same every time.
  * 1 <= vocab <= 2^24, max_new <= 1024, strides <= 2^40 else QG_ESHAPE; logits aligned to their elements, workspace 16-byte
  * (QG_EALIGN); QG_EWORKSPACE if NULL or smaller than qg_draft_verify_workspace.  It needs no initialisation; calls that
