@@ -124,14 +124,21 @@ __device__ __forceinline__ double weight(float l, float top, double c) {
     return exp2_64(fmax(((double)l - (double)top) * c, -1100.0));
 }
 // The same for many values up to one top: 2^(-(m - 256 l c) / 256), m = 256 top c rounded up so that no difference falls
-// below 0, and what m gained by that as a factor of all of them.  0 for a NaN: pieces note those apart.
+// below 0, and what m gained by that as a factor e^x of all of them.  m stays below 2^44, c halved as often as that takes: from
+// 2^43 on logits that differ do so by 2^-24 of them, 2^19 in the exponent, so that the lower one weighs nothing whatever c, and x,
+// 2^-16 at most, needs no more than its square (a larger m gained so much that the largest logit itself weighed nothing).
+// 0 for a NaN: pieces note those apart.
 struct Weigh {
     double c, m, rest;
     const double* table;
     __device__ __forceinline__ Weigh(float top, double c_, const double* t) : c(256.0 * c_), table(t) {
         m = (double)top * c;
+        const int over = min(44 - __builtin_amdgcn_frexp_exp(m), 0);
+        c = __builtin_amdgcn_ldexp(c, over);
+        m = __builtin_amdgcn_ldexp(m, over);
         m = fma(fabs(m), 2.220446049250313e-16, m);
-        rest = fma(fma(-(double)top, c, m), 0.69314718055994531 / 256, 1.0);
+        const double x = fma(-(double)top, c, m) * (0.69314718055994531 / 256);
+        rest = fma(fma(x, 0.5, 1.0), x, 1.0);
     }
     __device__ __forceinline__ void operator()(float l, double& u, double& v) const {
         exp2_64(fmin(fma(-(double)l, c, m), 281600.0), table, u, v);
