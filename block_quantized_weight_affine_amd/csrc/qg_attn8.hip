@@ -14,7 +14,6 @@ constexpr int64_t kTileFrom = 64;
 // Tokens a split at least, and tokens that are not split however few the heads are: 1024 of 8 heads of 128 take
 // 9.4 us in one launch; 5.8 and 3.8 us in two.
 constexpr int64_t kMinChunk = 256, kAlone = 1024;
-constexpr int64_t kTreeAlone = 1100;  // the same for a tree's tiles of 16 rows
 void set_tiles(AttnParams& a, int xt) {
     const int64_t rows = (int64_t)a.q.max_new * a.group;
     a.tile_rows = rows >= kTileFrom ? attn8_tile_rows(a, xt) : 16;
@@ -72,6 +71,13 @@ bool tree_in_rows(const AttnParams& a, int64_t span) {
     const double load = std::max((double)a.q.seqs * a.c.heads * span / 256, 1.0);  // tokens a CU of one tile
     return r16 < 4.5 * r128 + 2400 / load;
 }
+// Tokens of a tree's tiles of 16 rows that are not split: for heads of up to 128 values up to 1280, wider ones 1024, half as many
+// more where CUs get two splits at most.  Several splits and one, us, bf16 heads of 128: 8 workgroups 1152 tokens 10.3 and 10.1, 1280 10.3
+// and 10.3, 1408 10.7 and 11.7, 1536 10.4 and 11.7; 56 of 1280 10.6 and 10.5, of 1536 11.0 and 12.0; 104 of 1152 13.1 and 10.4, of
+// 1792 13.3 and 12.7, of 2048 13.6 and 14.4.  f32, 96: 8 of 1280 11.6 and 11.7, of 1536 11.6 and 13.4; 120 of 1536 14.9 and 13.6, of 2048
+// 15.2 and 16.2.  bf16, 256: 40 of 896 14.4 and 14.9, of 1152 14.7 and 16.3, 104 of 1152 19.6 and 16.5, of 1536 19.7 and 19.2, of 2048
+// 20.3 and 22.9; f32: 24 of 896 18.0 and 19.7, 72 of 1024 19.3 and 19.9, 104 of 1152 23.9 and 21.4, of 1408 24.1 and 24.9.
+int64_t tree_alone(const AttnParams& a, int64_t base) { return (a.c.dim <= 128 ? 1280 : 1024) * (256 / base > 2 ? 2 : 3) / 2; }
 // Splits that fill the card, and more of them where the tokens are many, as their lengths may differ: tiles of 16 rows 5
 // sequences of up to 120000 tokens 4 splits 130 us, 8 86, 16 82 (f32, 45 rows on 4 heads); 128 rows 5 of up to 30000 6 splits 84 us, 16
 // 73, 16 of up to 8191 2 splits 82 us, 4 70; 256 rows 16 of up to 8191 1 split 198 us, 2 127, 4 136; 5 of up to 30000 6 108 us, 8 90; tiles of
@@ -82,7 +88,7 @@ int64_t tree_splits(const AttnParams& a, int tile_rows, bool wide, int64_t span)
     const int64_t base = (int64_t)a.q.seqs * a.c.heads * ((rows + tile_rows - 1) / tile_rows);
     const bool two = wide && tile_rows == 128;
     const int64_t full = tile_rows == 16 || two ? 1024 : 256, tokens = two ? 2048 : 4096;
-    if (tile_rows == 16 && (span <= kTreeAlone || base >= 256)) return 1;
+    if (tile_rows == 16 && (base >= 256 || span <= tree_alone(a, base))) return 1;
     return std::max<int64_t>({256 / base, std::min(full / base, (span + tokens - 1) / tokens), 1});
 }
 void plan_tree(AttnParams& a, int xt) {
