@@ -91,22 +91,41 @@ int64_t tree_splits(const AttnParams& a, int tile_rows, bool wide, int64_t span)
     if (tile_rows == 16 && (base >= 256 || span <= tree_alone(a, base))) return 1;
     return std::max<int64_t>({256 / base, std::min(full / base, (span + tokens - 1) / tokens), 1});
 }
+bool tree_wide(const AttnParams& a, int xt) { return xt != XT_F32 && a.c.dim <= 128; }
+// Rows a tile of a tree's call; never fewer over more tokens.
+int tree_tile_rows(const AttnParams& a, int xt, int64_t span) {
+    if (tree_in_rows(a, span)) return 16;
+    const int64_t rows = (int64_t)a.q.max_new * a.group, pairs = (int64_t)a.q.seqs * a.c.heads;
+    // 256 rows share a stage's decoding where every CU has some 24 stages (16 of 2000 tokens, 244 rows: 58 us of 128, 66 of 256;
+    // of up to 8191: 117 and 110)
+    if (tree_wide(a, xt) && rows > 128 &&
+        (a.q.max_new > kPairTreeRows || pairs * span / 64 * ((rows + 255) / 256) >= 24 * 256))
+        return 256;
+    return 128;
+}
 void plan_tree(AttnParams& a, int xt) {
     int64_t span = a.q.max_kv;
     if (a.window > 0) span = std::min(span, (int64_t)a.window + a.q.max_new + 64);
     const int64_t rows = (int64_t)a.q.max_new * a.group, pairs = (int64_t)a.q.seqs * a.c.heads;
-    const bool wide = xt != XT_F32 && a.c.dim <= 128;
-    a.tile_rows = tree_in_rows(a, span) ? 16 : 128;
-    // 256 rows share a stage's decoding where every CU has some 24 stages (16 of 2000 tokens, 244 rows: 58 us of 128, 66 of 256;
-    // of up to 8191: 117 and 110)
-    if (a.tile_rows == 128 && wide && rows > 128 &&
-        (a.q.max_new > kPairTreeRows || pairs * span / 64 * ((rows + 255) / 256) >= 24 * 256))
-        a.tile_rows = 256;
+    a.tile_rows = tree_tile_rows(a, xt, span);
     a.tiles = (int)((rows + a.tile_rows - 1) / a.tile_rows);
-    const int64_t want = tree_splits(a, a.tile_rows, wide, span);
+    const int64_t want = tree_splits(a, a.tile_rows, tree_wide(a, xt), span);
     // 8 wavefronts a workgroup, or 4 where there are enough of few tokens (512 of 2000: 29 us, of 8 30; 2048: 91 and 113)
     a.row_waves = rows_late(xt == XT_F32 ? 2 : 1, a.c.dim) || pairs * a.tiles < 512 || span > 4 * kAlone ? 8 : 4;
     set_chunk(a, span, (span + want - 1) / want);
+}
+// Splits of any tree's call: a tile's height has most of them over the most tokens that it is taken for.
+int64_t most_tree_splits(const AttnParams& a, int xt) {
+    int64_t most = 1;
+    for (int rows : {16, 128, 256}) {
+        int64_t lo = 0, hi = a.q.max_kv;  // the most tokens of tiles of no more rows
+        while (lo < hi) {
+            const int64_t mid = (lo + hi + 1) / 2;
+            tree_tile_rows(a, xt, mid) <= rows ? lo = mid : hi = mid - 1;
+        }
+        if (lo > 0 && tree_tile_rows(a, xt, lo) == rows) most = std::max(most, tree_splits(a, rows, tree_wide(a, xt), lo));
+    }
+    return most;
 }
 }  // namespace
 
@@ -117,21 +136,19 @@ int attn8_max_splits(AttnParams a) {
         set_tiles(a, xt);
         const int64_t w = wanted_splits(a, xt, a.q.max_kv);
         if (w > want) want = w;
+        if (a.q.max_new > 1 && a.q.max_new <= kMaxTreeRows) want = std::max(want, most_tree_splits(a, xt));
     }
-    if (a.q.max_new <= kMaxTreeRows)
-        for (int rows : {16, 128, 256})
-            for (bool wide : {false, true}) want = std::max(want, tree_splits(a, rows, wide, a.q.max_kv));
     return (int)(most < want ? most : want);
 }
 
 // Kernel, tiles and splits of a call, from the host's bounds alone.
 void attn8_plan(AttnParams& a, int xt) {
-    if (a.mask) return plan_tree(a, xt);
+    if (a.mask && a.q.max_new > 1) return plan_tree(a, xt);
     set_tiles(a, xt);
     // tokens that a tile's rows may see: all, or their window, started at a multiple of 64
     int64_t span = a.q.max_kv;
     const int64_t seen = (int64_t)a.window + a.tile_rows / a.group + 65;
-    if (a.causal && a.window > 0 && seen < span) span = seen;
+    if ((a.causal || a.mask) && a.window > 0 && seen < span) span = seen;
     const int64_t want = wanted_splits(a, xt, span);
     int64_t chunk = (span + want - 1) / want;
     // 8 wavefronts a workgroup where its registers let a CU hold one, or there are few (320 workgroups of one

@@ -513,9 +513,10 @@ qg_status qg_kv8_read(const qg_kv8_cache* cache, const qg_kv8_seqs* seqs, void* 
                       int64_t k_head, void* v, int64_t v_row, int64_t v_head, qg_xtype yt,
                       hipStream_t stream);
 
-/* Bytes of workspace that qg_attn_kv8 needs for these descriptors and q_heads, whatever its mask (0: none,
- * or arguments that it would refuse).  Smaller bounds can need more (more splits of the tokens): a buffer
- * for several calls has the largest of their sizes. */
+/* Bytes of workspace that qg_attn_kv8, and with 2 <= max_new <= 1024 qg_attn_kv8_tree, need for these
+ * descriptors and q_heads, whatever their masks (0: none, or arguments that they would refuse).  Smaller bounds
+ * can need more (more splits of the tokens): a buffer for several calls has the largest of their sizes.  A tree of
+ * max_new 1 needs what a single token does. */
 size_t qg_attn_kv8_workspace(const qg_kv8_cache* cache, const qg_kv8_seqs* seqs, int q_heads);
 
 /* Attention of the rows q [T][q_heads][dim] over the cache, o of the same shape and type.  Head h reads K/V

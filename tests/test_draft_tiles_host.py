@@ -1,7 +1,9 @@
-"""CPU checks of what test_gpu_draft_tiles.py rests on: which kernel the library's own plan gives its batches, and its definition
-against oracle/draft.py's."""
+"""CPU checks of the attention's plans: which kernel the library gives the batches of test_gpu_draft_tiles.py, whose definition is
+held against oracle/draft.py's, and that the workspace has room for any call under its bounds and no more than it needs."""
 import ctypes as C
+import math
 import os
+import random
 import subprocess
 
 import numpy as np
@@ -18,17 +20,17 @@ NAMES = {"f32": qg.QG_X_F32, "f16": qg.QG_X_F16, "bf16": qg.QG_X_BF16}
 
 @pytest.fixture(scope="session")
 def plan(tmp_path_factory):
-    """(rows a tile, splits) of a tree's call, by the function that the library itself goes by."""
+    """(rows a tile, splits) of a call, by the function that the library itself goes by."""
     qg.lib()
     d = tmp_path_factory.mktemp("plan")
     (d / "plan.cpp").write_text('''
 #include "qg_internal.hpp"
-extern "C" void plan(int seqs, int T, int max_new, int max_kv, int heads, int q_heads, int dim, int window, int xt, int* out) {
+extern "C" void plan(int seqs, int T, int max_new, int max_kv, int heads, int q_heads, int dim, int window, int xt, int tree, int* out) {
     static const uint32_t some = 0;
     qg::AttnParams a{};
     a.c.heads = heads; a.c.dim = dim;
     a.q.seqs = seqs; a.q.T = T; a.q.max_new = max_new; a.q.max_kv = max_kv;
-    a.q_heads = q_heads; a.group = q_heads / heads; a.window = window; a.mask = &some;
+    a.q_heads = q_heads; a.group = q_heads / heads; a.window = window; a.causal = !tree; a.mask = tree ? &some : nullptr;
     qg::attn8_plan(a, xt);
     out[0] = a.tile_rows; out[1] = a.splits; out[2] = qg::attn8_max_splits(a);
 }
@@ -39,10 +41,10 @@ extern "C" void plan(int seqs, int T, int max_new, int max_kv, int heads, int q_
                     "-Wl,-rpath," + lib], check=True)
     call = C.CDLL(str(so)).plan
 
-    def of(seqs, T, max_new, max_kv, heads, q_heads, dim, window, xt):
+    def of(seqs, T, max_new, max_kv, heads, q_heads, dim, window, xt, tree=True):
         out = (C.c_int * 3)()
-        call(seqs, T, max_new, max_kv, heads, q_heads, dim, window, NAMES[xt], out)
-        assert out[1] <= out[2]
+        call(seqs, T, max_new, max_kv, heads, q_heads, dim, window, NAMES[xt], int(tree), out)
+        assert out[1] <= out[2]                             # what the workspace has room for
         return out[0], out[1]
     return of
 
@@ -80,3 +82,32 @@ def test_the_definition_for_all_rows(window):
     want = od.attend(b.kc, b.ks, b.vc, b.vs, b.table, b.spans(), q.double().numpy(), 0.1, mask, window, pos)
     for x, y in zip((o, mean, reach), want):
         assert np.allclose(x, y, rtol=1e-12, atol=1e-13)
+
+
+def test_the_workspace_has_room_for_every_plan(plan):
+    """Any window, type and kind of call under the same bounds (the fixture compares)."""
+    rng = random.Random(3)
+    log = lambda lo, hi: max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi + 1)))))))  # noqa: E731
+    for _ in range(3000):
+        seqs, heads, group, new = log(1, 200), log(1, 32), log(1, 64), log(1, 1024)
+        tokens = max(new, log(1, 1 << 24))
+        for _ in range(4):
+            window = rng.choice([0, log(1, tokens)])
+            for xt in NAMES:
+                for tree in (True, False):
+                    plan(seqs, seqs * new, new, tokens, heads, heads * group, rng.choice([64, 96, 128, 192, 256]), window, xt, tree)
+
+
+def test_the_workspace_of_calls_without_trees():
+    """Single tokens and prompts of more than 1024 rows, which no tree has, ask for their own splits alone; what trees of no more than
+    1024 rows add is what their largest plan takes.  32 heads of 128 on 8: a split's part is 32 x 130 x 4 bytes a row."""
+    def asked(seqs, new, tokens):
+        c = qg.QgKv8Cache(0x10000, 0x10000, 0x10000, 0x10000, 8, 64, 8, 128)
+        s = qg.QgKv8Seqs(0x10000, 0x10000, 0x10000, seqs, 1 << 17, seqs * new, new, tokens)
+        size, part = qg.lib().qg_attn_kv8_workspace(C.addressof(c), C.addressof(s), 32), seqs * new * 32 * 130 * 4
+        assert size % part == 0
+        return size // part
+    assert asked(1, 1, 200000) == 32 and asked(64, 1, 8192) == 6 and asked(16, 1, 32768) == 8
+    assert asked(1, 1, 1000) == 0 and asked(1, 2048, 200000) == 0
+    assert asked(1, 1024, 200000) == 2                     # 128 tiles of 256 rows, twice for 256 CUs
+    assert asked(16, 64, 1 << 15) == 2

@@ -47,3 +47,17 @@ def test_attend(name, kind):
     _check(b, q, xt, q_heads, scale, mask, window, pos, got)
     assert torch.equal(got, _attend(b, q, q_heads, scale, mask, window, pos))
 
+
+
+@pytest.mark.parametrize("heads,group,dim,window,xt", [(2, 4, 128, 0, "bf16"), (1, 64, 64, 700, "f16"), (3, 7, 96, 0, "f32"),
+                                                       (1, 2, 256, 33, "f32"), (8, 1, 192, 2000, "bf16"), (2, 65, 128, 0, "f16")])
+def test_single_rows(heads, group, dim, window, xt):
+    """Trees of no more than one row a sequence, that see themselves or not, over histories of any length."""
+    print(f"tree single rows heads={heads} group={group} dim={dim} window={window} {xt}", flush=True)
+    b = Batch([(1, 5000), (1, 1), (0, 9), (1, 300), (1, 64), (1, 1025)], heads, dim, 32, heads).upload()
+    mask = np.array([[1], [0], [0xffffffff], [0xfffffffe], [1]], np.uint32)
+    pos = np.array([5000, -3, 10, 63, 2 ** 31 - 1], np.int32)
+    q = _values(b.rng, (b.T, heads * group, dim), xt).cuda()
+    got = _attend(b, q, heads * group, 0.1, mask, window, pos if window else None)
+    _check(b, q, xt, heads * group, 0.1, mask, window, pos, got)
+    assert torch.all(got[1] == 0)
