@@ -62,8 +62,9 @@ __global__ __launch_bounds__(64 * W, W == 4 && rows_registers(XT == XT_F32 ? 2 :
 
     const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    // The tiles of a head and split read the same codes: eight workgroups apart, they share a die's cache (8 sequences of
-    // 20000 tokens, 48 rows on each of 8 heads of 128: 146 -> 105 us).
+    // The tiles of a head and split read the same codes: eight workgroups apart, they share a die's cache (trees of 8 sequences
+    // of 20000 tokens, 48 rows on each of 8 heads of 128: 146 -> 105 us; qg_attn_kv8, bf16, 64 sequences of 2000 on 8 heads of
+    // 128, 20 rows each 79 -> 48, 48 114 -> 65, 60 150 -> 83; one sequence of 200 within 0.1 us).
     int b = a.first + blockIdx.x;
     const int tile = b / 8 % a.tiles;
     b = b / 8 / a.tiles * 8 + b % 8;
