@@ -26,26 +26,40 @@ CASES = {
 }
 
 
-def attend(b, q, scale, mask, window, pos, device):
-    """o, the weighted means of |v| and the largest scale * sum |q k| of every row and head, f64; rows of no sequence are 0."""
-    T, QH, D = q.shape
-    G = QH // b.H
-    q = q.double().to(device)
-    o, mean, reach = torch.zeros_like(q), torch.zeros_like(q), torch.zeros(T, QH, 1, dtype=torch.float64, device=device)
+def sights(b, mask, window, pos):
+    """Which tokens each row sees by its mask and window: (sequence, first row, [rows][tokens]) of each sequence with rows."""
+    out = []
     for s, (r0, n, total) in enumerate(b.spans()):
         if not n:
             continue
-        hist, j = total - n, np.arange(total)
+        hist = total - n
         bits = np.unpackbits(np.ascontiguousarray(mask[r0:r0 + n]).view(np.uint8), axis=1, bitorder="little")[:, :n].astype(bool)
         seen = np.zeros((n, total), bool)
         for i in range(n):
             since = min(max(int(pos[r0 + i]), hist), total - 1) - window + 1 if window > 0 else 0
             seen[i, max(since, 0):hist] = True
         seen[:, hist:] = bits
+        out.append((s, r0, seen))
+    return out
+
+
+def attend(b, q, scale, mask, window, pos, device):
+    """Of every row and head, f64: o, the weighted means of |v|, the largest scale * sum |q k| and the largest (weight / sum of
+    weights) * |V scale|; rows of no sequence are 0."""
+    T, QH, D = q.shape
+    G = QH // b.H
+    q = q.double().to(device)
+    o, mean = torch.zeros_like(q), torch.zeros_like(q)
+    reach, peak = (torch.zeros(T, QH, 1, dtype=torch.float64, device=device) for _ in "rp")
+    for s, r0, seen in sights(b, mask, window, pos):
+        n, total = seen.shape
+        j = np.arange(total)
+        page, off = b.table[s][j // b.page], j % b.page // 16
+        page = np.where((page >= 0) & (page < b.P), page, 0)
         for h in range(b.H):
             k, there = serve8.tokens(b.kc, b.ks, b.table, s, h, total)
             v, _ = serve8.tokens(b.vc, b.vs, b.table, s, h, total)
-            k, v = torch.from_numpy(k).to(device), torch.from_numpy(v).to(device)
+            k, v, vd = (torch.from_numpy(x).to(device) for x in (k, v, np.abs(b.vs[page, h, off].astype(np.float64))))
             see = torch.from_numpy(seen & there).to(device).repeat_interleave(G, 0)
             x = q[r0:r0 + n, h * G:(h + 1) * G].reshape(n * G, D)
             sc = (x @ k.t().contiguous() * scale).masked_fill(~see, -torch.inf)
@@ -57,4 +71,5 @@ def attend(b, q, scale, mask, window, pos, device):
             o[at] = (w @ v).view(n, G, D)
             mean[at] = (w @ v.abs()).view(n, G, D)
             reach[at] = abs(scale) * far.view(n, G, 1)
-    return o, mean, reach
+            peak[at] = (w * vd).amax(1).view(n, G, 1)
+    return o, mean, reach, peak

@@ -78,10 +78,11 @@ def test_the_definition_for_all_rows(window):
     mask[::4] = 0
     pos = b.rng.integers(-5, 60, b.T).astype(np.int32)
     q = _values(b.rng, (b.T, 6, 64), "f32")
-    o, mean, reach = (x.numpy() for x in attend(b, q, 0.1, mask, window, pos, "cpu"))
+    o, mean, reach, peak = (x.numpy() for x in attend(b, q, 0.1, mask, window, pos, "cpu"))
     want = od.attend(b.kc, b.ks, b.vc, b.vs, b.table, b.spans(), q.double().numpy(), 0.1, mask, window, pos)
     for x, y in zip((o, mean, reach), want):
         assert np.allclose(x, y, rtol=1e-12, atol=1e-13)
+    assert np.all(mean <= 127 * 40 * peak) and np.all(peak <= b.vs.max())
 
 
 def test_the_workspace_has_room_for_every_plan(plan):
