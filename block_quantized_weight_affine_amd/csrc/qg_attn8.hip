@@ -63,9 +63,9 @@ void set_chunk(AttnParams& a, int64_t span, int64_t chunk) {
 // A tree's call: tiles of 16 rows, of 128 or of 256.  16 rows decode the codes for themselves, which takes 5 us for 1000
 // tokens on each CU; a tile of 128 rows takes 22 us, and its workgroups longer to start.  Microseconds of 16 rows and of 128,
 // each at its best splits, bf16, 32 heads of 128 on 8 (drafted rows times 4 a K/V head): 1 sequence of 1000 tokens, 25 / 100
-// drafted rows 10.9 and 20.0 / 11.7 and 22.7; of 8000, 25 / 61: 20.5 and 22.9 / 30.6 and 30.5; 16 of 2000, 16 / 25 / 61: 29 and 37
-// / 47 and 42 / 92 and 58; 16 of up to 8191, 16 / 25 / 61: 52 and 67 / 78 and 71 / 145 and 117; 4 of 30000, f32, heads of 96, 9 / 30:
-// 84 and 127 / 169 and 133; 4 of up to 10000, heads of 256, 30: 36 and 47.
+// drafted rows 10.6 and 18.0 / 11.5 and 21.1; of 8000, 25 / 61: 19.9 and 21.8 / 32.9 and 28.6; 16 of 2000, 16 / 25 / 61: 28 and 36
+// / 44 and 41 / 84 and 53; 16 of up to 8191, 16 / 25 / 61: 71 and 74 / 102 and 78 / 208 and 132; 4 of 30000, f32, 20 heads of 96 on
+// 4, 9 / 30: 50 and 69 / 132 and 123; 4 of up to 10000, heads of 256, 30: 68 and 56.
 bool tree_in_rows(const AttnParams& a, int64_t span) {
     const int64_t rows = (int64_t)a.q.max_new * a.group, r16 = (rows + 15) / 16, r128 = (rows + 127) / 128;
     const double load = std::max((double)a.q.seqs * a.c.heads * span / 256, 1.0);  // tokens a CU of one tile
@@ -79,9 +79,9 @@ bool tree_in_rows(const AttnParams& a, int64_t span) {
 // 20.3 and 22.9; f32: 24 of 896 18.0 and 19.7, 72 of 1024 19.3 and 19.9, 104 of 1152 23.9 and 21.4, of 1408 24.1 and 24.9.
 int64_t tree_alone(const AttnParams& a, int64_t base) { return (a.c.dim <= 128 ? 1280 : 1024) * (256 / base > 2 ? 2 : 3) / 2; }
 // Splits that fill the card, and more of them where the tokens are many, as their lengths may differ: tiles of 16 rows 5
-// sequences of up to 120000 tokens 4 splits 130 us, 8 86, 16 82 (f32, 45 rows on 4 heads); 128 rows 5 of up to 30000 6 splits 84 us, 16
-// 73, 16 of up to 8191 2 splits 82 us, 4 70; 256 rows 16 of up to 8191 1 split 198 us, 2 127, 4 136; 5 of up to 30000 6 108 us, 8 90; tiles of
-// 16 rows 16 of up to 8191 (512 workgroups) 1 split 53 us, 2 58.
+// sequences of up to 120000 tokens 4 splits 79 us, 8 86, 17 70, 32 76 (f32, 45 rows on 4 heads of 96), 16 of up to 8191 (512
+// workgroups) 1 split 71 us, 2 72, 4 81; 128 rows, 25 drafted, 5 of up to 30000 6 splits 57 us, 16 49, 24 62, 16 of up to 8191 2 splits 95
+// us, 4 78, 8 79; 256 rows, 61 drafted, 16 of up to 8191 1 split 198 us, 2 121, 4 136, 5 of up to 30000 4 splits 94 us, 6 76, 8 69, 12 94.
 // wide: two workgroups a CU.
 int64_t tree_splits(const AttnParams& a, int tile_rows, bool wide, int64_t span) {
     const int64_t rows = (int64_t)a.q.max_new * a.group;
@@ -96,8 +96,8 @@ bool tree_wide(const AttnParams& a, int xt) { return xt != XT_F32 && a.c.dim <= 
 int tree_tile_rows(const AttnParams& a, int xt, int64_t span) {
     if (tree_in_rows(a, span)) return 16;
     const int64_t rows = (int64_t)a.q.max_new * a.group, pairs = (int64_t)a.q.seqs * a.c.heads;
-    // 256 rows share a stage's decoding where every CU has some 24 stages (16 of 2000 tokens, 244 rows: 58 us of 128, 66 of 256;
-    // of up to 8191: 117 and 110)
+    // 256 rows share a stage's decoding where every CU has some 24 stages (16 of 2000 tokens, 244 rows: 53 us of 128, 64 of 256;
+    // of up to 8191: 132 and 121)
     if (tree_wide(a, xt) && rows > 128 &&
         (a.q.max_new > kPairTreeRows || pairs * span / 64 * ((rows + 255) / 256) >= 24 * 256))
         return 256;
@@ -110,7 +110,7 @@ void plan_tree(AttnParams& a, int xt) {
     a.tile_rows = tree_tile_rows(a, xt, span);
     a.tiles = (int)((rows + a.tile_rows - 1) / a.tile_rows);
     const int64_t want = tree_splits(a, a.tile_rows, tree_wide(a, xt), span);
-    // 8 wavefronts a workgroup, or 4 where there are enough of few tokens (512 of 2000: 29 us, of 8 30; 2048: 91 and 113)
+    // 8 wavefronts a workgroup, or 4 where there are enough of few tokens (512 of 2000: 28.7 us, of 8 29.5; 2048: 105 and 123)
     a.row_waves = rows_late(xt == XT_F32 ? 2 : 1, a.c.dim) || pairs * a.tiles < 512 || span > 4 * kAlone ? 8 : 4;
     set_chunk(a, span, (span + want - 1) / want);
 }

@@ -15,8 +15,8 @@ constexpr int kMaxRows = kMaxTreeRows;
 // A workgroup a sequence.  A parent's index is below its row's, so rows go in groups of 64, of which a wavefront first finds
 // what a row's ancestors within the group are, a lane a row, doubling the steps that all of them know (6 turns at most), and
 // the row that those follow; groups then take the rest of that row's mask, one after the other.  A row's depth is the number
-// of its mask's bits, and a window keeps the last ones.  Bound by latency: lengths, parents, turns.  A tree of 25 rows 2.6
-// us; 64 trees of 255 rows, each following one of two before it, 5.2, and 8 chains of 1000 16.7, by 256 threads 33 (a thread a row
+// of its mask's bits, and a window keeps the last ones.  Bound by latency: lengths, parents, turns.  A tree of 25 rows 2.2
+// us; 64 trees of 255 rows, each following one of two before it, 5.3, and 8 chains of 1000 16.7, by 256 threads 33 (a thread a row
 // that walks up all of its parents: 2.7, 20 and 264).
 template <int N>
 __global__ __launch_bounds__(N) void tree_plan_kernel(KvSeqs q, const int32_t* parents, uint32_t* mask, int words, int32_t* pos,
@@ -307,8 +307,9 @@ __device__ __forceinline__ int listed_row(const VerifyParams& p, const KvSpan& s
 }
 
 // Pieces of a row by a wavefront, p.per of them one after the other, the next one's values on their way: each piece's
-// largest logit, where that stands first (temperature 0), and the sum of weights below it.  Bound by vector instructions, 18 a
-// logit: 32 users' seven drafts, 128000 bf16 logits a row, 24 us; one user's five of 32000 4.4 us, a launch and its loads.
+// largest logit, where that stands first (temperature 0), and the sum of weights below it.  32 users' seven drafts, 128000 bf16
+// logits a row, 25 us: 20 vector instructions for each of a lane's logits issue in 16 of them, the rest waits for a piece's loads, its largest
+// logit, its weights and their sum, one after the other.  One user's five of 32000 4.4 us, a launch and its loads.
 template <int XT>
 __global__ __launch_bounds__(256) void verify_part_kernel(VerifyParams p, uint32_t group0) {
     __shared__ double table[kTable];
@@ -712,7 +713,7 @@ __global__ __launch_bounds__(256) void verify_tree_kernel(VerifyParams p) {
 // max(p - q, 0), and where all stay the draw is from p at the last row.  Every workgroup finds the row at which the
 // sequence ends, eight rows at a time, a wavefront each for p and for q; for max(p - q, 0) the first p.per wavefronts then sum a
 // piece each, and the last workgroup draws, else one alone does.  One user 6.4 us, 3 of them until the row is found, 1.4 for the last piece;
-// 32 users of 128000 logits 16.4 us, 5 of them 64-bit instructions of the masses.
+// 32 users of 128000 logits 15.7 us, 5 of them 64-bit instructions of the masses.
 constexpr int kChainWaves = 16;
 template <int XT>
 __global__ __launch_bounds__(64 * kChainWaves) void verify_chain_kernel(VerifyParams p) {

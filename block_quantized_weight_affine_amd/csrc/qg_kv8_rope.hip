@@ -12,7 +12,8 @@ namespace {
 constexpr int kTurns = 2048;  // (cos, sin) pairs that a workgroup keeps
 
 // How a thread takes the values of a head: 16 bytes of either half of the turned part, or 16 bytes of adjacent pairs;
-// kSingle: a pair at a time, where halves do not begin at a multiple of 16 bytes.
+// kSingle: a pair at a time, where halves do not begin at a multiple of 16 bytes (8191 rows of 40 heads, bf16, 24 of 96 turned: 64
+// us, with 32 of 96 26).
 enum { kHalf = 0, kAdjacent = 1, kSingle = 2 };
 
 template <int XT>
@@ -159,7 +160,9 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeRows a, Rotary rt, const 
 // qg_kv8.hip's blocks, K turned before it is coded.  A workgroup takes one block of 16 tokens and four heads of K or of
 // V, a wavefront each; the block's turns are computed once by all of them.  Further workgroups turn q's rows, so that a step has one
 // launch where it had two.  Bound by memory: 7 sequences of up to 4096 rows, 32 heads of q and 8 of K and V, f16, 77 us for
-// 350 MB; a single row of 48 users 5.4 us, as long as qg_kv8.hip's without q.
+// 350 MB; a single row of 48 users 5.4 us, as long as qg_kv8.hip's without q; the
+// rows that stay of 16 users' 8, read through src, 4.6 us.  8192 rows of 8 heads of 96, bf16, 32 values turned 16.4 us, 24 of them, whose
+// halves begin off 16 bytes, 23.6.
 //   K  a lane takes two groups of 8 dims of a token: the halves of 8 pairs, or what lies side by side.
 template <int XT, int D>
 __global__ __launch_bounds__(64 * kWaves) void kv8_write_rope_kernel(KvCache c, KvSeqs q, KvRope a, uint32_t group0) {

@@ -561,7 +561,7 @@ qg_status qgemm_w8a8(const int8_t* w_codes, const float* w_scales, const void* X
  * Rotary positions: of every head's values the first `rot` are turned in pairs i < rot / 2,
  *     y_a = mscale (x_a cos t - x_b sin t),  y_b = mscale (x_b cos t + x_a sin t),  t = position * freqs[i],
  * (a, b) = (2i, 2i + 1) if interleaved, else (i, i + rot / 2); values from rot on stay.  Angles are reduced in 64 bits, sines
- * and cosines rounded to f32 (off by no more than 2^-22 and 2^-52 |t|), products in f32.  freqs: f64 [rot / 2] radians
+ * and cosines rounded to f32 (off by no more than 2^-22 and 2^-51 |t|), products in f32.  freqs: f64 [rot / 2] radians
  * a position, device memory, 8-byte aligned (QG_EALIGN).  rot even, 0 .. dim (QG_ESHAPE); 0 turns nothing, freqs unused. */
 typedef struct {
     const double* freqs;
@@ -641,7 +641,7 @@ qg_status qg_attn_kv8_tree(const qg_kv8_cache* cache, const qg_kv8_seqs* seqs, c
  * +inf, and a temperature below 0, NaN or infinite have no next token: -1, and nothing after that row stays.  A draft row
  * without probabilities gives its token up, and the next one is drawn from p.  Drafted tokens outside of 0 .. vocab - 1
  * never stay.  A sequence without rows: accepted 0, next -1.  Of sequences whose rows overlap the results are not specified;
- * path ends at T rows.
+ * path ends at T rows.  Outputs overlap neither each other nor an input, but for kv_out over kv_len.
  * All probabilities and sums are in 64 bits; the result is the same every time.
  * 1 <= vocab <= 2^24, max_new <= 1024, strides <= 2^40 else QG_ESHAPE; logits aligned to their elements, workspace 16-byte
  * (QG_EALIGN); QG_EWORKSPACE if NULL or smaller than qg_draft_verify_workspace.  It needs no initialisation; calls that
